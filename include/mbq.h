@@ -70,7 +70,7 @@ typedef enum {
 
 /* Element types.  Any other int32 value is MBQ_ERR_ARG (the range markers make it a valid
    mbq_dtype, so the check itself is defined). */
-typedef enum { MBQ_F32 = 0, MBQ_BF16 = 1, MBQ_DTYPE_MIN_ = INT32_MIN, MBQ_DTYPE_MAX_ = INT32_MAX } mbq_dtype;
+typedef enum { MBQ_F32 = 0, MBQ_BF16 = 1, MBQ_E4M3 = 2 /* mbq_fp8_* only */, MBQ_DTYPE_MIN_ = INT32_MIN, MBQ_DTYPE_MAX_ = INT32_MAX } mbq_dtype;
 
 /*
  * Kernel and tiling choices of the routed linear, for tests and tuning.  Every call that
@@ -400,6 +400,193 @@ mbq_status mbq_linear_lowrank(const mbq_desc* desc, const void* packed, int32_t 
                               const uint16_t* a, const uint16_t* b, int32_t rank, void* y,
                               mbq_dtype y_dtype, void* workspace, size_t ws_bytes,
                               const mbq_opts* opts, hipStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------------------
+ * Dense operators beside the routed linear: the 8-bit linear of layers that keep one
+ * precision, the gated half of a feed-forward block on it, the norms around a block, and
+ * the log probabilities that answers and perplexity are made of.
+ *
+ * e4m3 throughout: the 8-bit float of 4 exponent and 3 mantissa bits (largest value 448,
+ * one NaN, no infinity), rounded to nearest even.  A quantized vector of inputs has one
+ * float32 scale per block of 128; with a = max(max |v|, 2^-96) over the block,
+ *     code = e4m3(v * (448 / a)),   scale = a / 448
+ * (float32, every operation rounded once; a NaN or infinity makes its block's values NaN).
+ */
+
+/*
+ * Geometry of one packed 8-bit weight W [n x k] (gated == 0), or of two weights of the
+ * same shape that read the same inputs, Wg and Wu (gated == 1: interleaved, see below).
+ * Treat as read-only.
+ *
+ * Blob layout:
+ *   codes  at +0: row_blocks * k_blocks tiles of 2048 bytes, tile (rb, kb) at
+ *          (rb * k_blocks + kb) * 2048; inside a tile, byte 1024 h + 16 l + e of half
+ *          h = 0, 1 and lane l = 16 c + r is row r of the block at input
+ *          128 kb + 64 h + 16 c + e, e = 0..15.  Row block rb is rows 16 rb .. + 15 of W;
+ *          in a gated blob rows 16 (rb / 2) .. + 15 of Wg (rb even) or Wu (rb odd).
+ *          Rows >= n and inputs >= k are padding (code 0).
+ *   scales at +scales_offset: float32 [gated + 1][ceil(n / 128)][k_blocks], one per
+ *          128 x 128 block of each weight.
+ *   zeros  at +zeros_offset: 256 bytes of 0.
+ */
+typedef struct {
+  int32_t abi;             /* MBQ_ABI_VERSION */
+  int32_t n, k;            /* output rows of each weight, inputs */
+  int32_t gated;           /* 0: one weight, 1: two interleaved */
+  int32_t row_blocks;      /* ceil(n / 16) * (gated + 1) */
+  int32_t k_blocks;        /* ceil(k / 128) */
+  uint64_t scales_offset;  /* row_blocks * k_blocks * 2048 */
+  uint64_t zeros_offset;   /* scales_offset + the scales, rounded up to 256 */
+  uint64_t total_bytes;    /* zeros_offset + 256 */
+} mbq_fp8_desc;
+
+/* Host only: validates the shape (1 <= n, k <= 2^24, codes below 64 GiB) and fills *out.
+ * Launches nothing.  Every call below takes 0 <= t <= 2^21 rows; with t == 0 it launches
+ * nothing and t-sized pointers may be NULL. */
+mbq_status mbq_fp8_describe(int32_t n, int32_t k, int32_t gated, mbq_fp8_desc* out);
+
+/*
+ * Pack one weight into its blob.
+ *   part:     0 (the weight, or Wg of a gated blob), 1 (Wu).  A gated blob is complete
+ *             after both parts.
+ *   w:        [n x k] row-major: float32 or bfloat16 (quantized here, one scale per
+ *             128 x 128 block, by the formula above), or e4m3 codes (MBQ_E4M3) with
+ *   w_scale:  float32 [ceil(n / 128)][ceil(k / 128)], what a code of that block is
+ *             multiplied by; must be NULL for the other types.
+ *   packed:   desc->total_bytes, 256-byte aligned; every byte of the part is written.
+ *   dev_status: nullable int32; bit 0 is ORed in if w or w_scale holds a non-finite value.
+ */
+mbq_status mbq_fp8_pack(const mbq_fp8_desc* desc, int32_t part, const void* w, mbq_dtype w_dtype,
+                        const float* w_scale, void* packed, int32_t* dev_status, hipStream_t stream);
+
+/*
+ * Quantize activations x [t x k] (float32 or bfloat16, rows ldx elements apart) per token
+ * and 128 inputs.
+ *   q:     [t x k] e4m3 codes, rows ldq bytes apart; only bytes 0 .. k - 1 of a row are written.
+ *   scale: [ceil(k / 128) x t] float32: one row per block, tokens side by side.
+ */
+mbq_status mbq_fp8_quantize(int32_t t, int32_t k, const void* x, mbq_dtype x_dtype, int64_t ldx,
+                            void* q, int64_t ldq, float* scale, hipStream_t stream);
+
+/* Host only: bytes of device workspace mbq_fp8_linear / mbq_fp8_gated need for t tokens of
+ * this type (0 possible).  Depends only on desc, t and x_dtype. */
+mbq_status mbq_fp8_linear_workspace(const mbq_fp8_desc* desc, int32_t t, mbq_dtype x_dtype, size_t* bytes);
+
+/*
+ * 8-bit linear y = x . W^T with x quantized within the call:
+ *   y[t][i] = sum_kb xs[kb][t] ws[i / 128][kb] sum_{k in block kb} xq[t][k] wq[i][k].
+ *   packed:  a blob of mbq_fp8_pack for `desc` (desc->gated == 0).
+ *   x:       [t x k], rows ldx elements apart (ldx >= k): float32 or bfloat16, or e4m3
+ *            codes (MBQ_E4M3) of mbq_fp8_quantize or mbq_block_norm with
+ *   x_scale: their scales [ceil(k / 128) x t] (NULL for the other types).  Codes need
+ *            k % 16 == 0, ldx % 16 == 0 and 16-byte alignment (MBQ_ERR_SHAPE, MBQ_ERR_ARG).
+ *   y:       [t x n] row-major, float32 or bfloat16.
+ *   workspace: mbq_fp8_linear_workspace() bytes, 256-byte aligned, scratch (no state is
+ *            kept; calls that overlap in time must not share one).
+ * Blocks are scaled and added in float32.  The products of one block are summed by the
+ * fp8 matrix instruction when y is bfloat16 (its own sum is off by about 2^-16 of the
+ * result, below y's rounding), and in float32 by the bfloat16 instruction, at half the
+ * rate, when y is float32.  A token that holds a NaN or infinity yields NaN for its own row
+ * only.  Identical from run to run.
+ */
+mbq_status mbq_fp8_linear(const mbq_fp8_desc* desc, const void* packed, int32_t t, const void* x,
+                          mbq_dtype x_dtype, int64_t ldx, const float* x_scale, void* y, mbq_dtype y_dtype,
+                          void* workspace, size_t ws_bytes, hipStream_t stream);
+
+/* Activation of the gated half. */
+typedef enum {
+  MBQ_ACT_SILU = 0,      /* g / (1 + exp(-g)) */
+  MBQ_ACT_GELU_TANH = 1, /* g / 2 (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) */
+  MBQ_ACT_MIN_ = INT32_MIN,
+  MBQ_ACT_MAX_ = INT32_MAX
+} mbq_act;
+
+/*
+ * Gated half of a feed-forward block in one pass: y = act(x . Wg^T) * (x . Wu^T), on a
+ * gated blob (desc->gated == 1).  Both products are kept in float32 and reach no memory;
+ * everything else as in mbq_fp8_linear.
+ */
+mbq_status mbq_fp8_gated(const mbq_fp8_desc* desc, const void* packed, int32_t t, const void* x,
+                         mbq_dtype x_dtype, int64_t ldx, const float* x_scale, mbq_act act, void* y,
+                         mbq_dtype y_dtype, void* workspace, size_t ws_bytes, hipStream_t stream);
+
+typedef enum {
+  MBQ_NORM_RMS = 0,   /* v / sqrt(mean v^2 + eps) * weight */
+  MBQ_NORM_LAYER = 1, /* (v - mean v) / sqrt(mean (v - mean v)^2 + eps) * weight + bias */
+  MBQ_NORM_MIN_ = INT32_MIN,
+  MBQ_NORM_MAX_ = INT32_MAX
+} mbq_norm_kind;
+
+typedef enum {
+  MBQ_GATE_NONE = 0,
+  MBQ_GATE_CHANNEL = 1, /* float32 [k] */
+  MBQ_GATE_TOKEN = 2,   /* float32 [t] */
+  MBQ_GATE_FULL = 3,    /* [t x k] of x's type, contiguous */
+  MBQ_GATE_MIN_ = INT32_MIN,
+  MBQ_GATE_MAX_ = INT32_MAX
+} mbq_gate_kind;
+
+/* Arguments of mbq_block_norm (device pointers).  Rows of x, residual, y and h are ld*
+ * elements apart (at least k). */
+typedef struct {
+  int32_t t, k;
+  int32_t kind;              /* mbq_norm_kind, of both norms */
+  int32_t gate_kind;         /* mbq_gate_kind */
+  int32_t x_dtype;           /* of x (and a full gate): MBQ_F32 or MBQ_BF16 */
+  int32_t r_dtype;           /* of residual and y: MBQ_F32 or MBQ_BF16 */
+  int32_t h_dtype;           /* MBQ_F32, MBQ_BF16, or MBQ_E4M3 (codes, with scale) */
+  int32_t post;              /* 1: x is normed before the gate, 0: it is taken as it is */
+  const void* x;             /* [t x k] the block's output */
+  const void* residual;      /* [t x k], or NULL for zeros */
+  const float* post_weight;  /* [k] or NULL for ones */
+  const float* post_bias;    /* [k] or NULL (layer norm only) */
+  const float* pre_weight;   /* [k] or NULL for ones */
+  const float* pre_bias;     /* [k] or NULL (layer norm only) */
+  const void* gate;          /* by gate_kind */
+  void* y;                   /* [t x k] new residual stream, or NULL to not write it; may be
+                                residual itself (same ld), but overlap nothing else */
+  void* h;                   /* [t x k] normed input of the next block */
+  float* scale;              /* [ceil(k / 128) x t], for MBQ_E4M3 */
+  int64_t ldx, ldr, ldy, ldh;
+  float residual_scale, gate_scale, eps;
+} mbq_block_norm_args;
+
+/*
+ * The norms after a block and before the next, with the block's gate and scale:
+ *     z = post ? norm(x; post_weight, post_bias) : x
+ *     y = residual_scale * residual + gate_scale * gate * z
+ *     h = norm(y; pre_weight, pre_bias)
+ * in float32 from the inputs to the one rounding of y and h each (h is computed from y
+ * before its rounding; e4m3 codes from h in float32).  eps > 0; 1 <= k <= 2^24.
+ */
+mbq_status mbq_block_norm(const mbq_block_norm_args* args, hipStream_t stream);
+
+#define MBQ_MAX_TOP 64
+
+/* Host only: bytes of device workspace mbq_token_logprobs needs (0 where one workgroup
+ * holds a row).  Depends only on t, v and top. */
+mbq_status mbq_token_logprobs_workspace(int32_t t, int32_t v, int32_t top, size_t* bytes);
+
+/*
+ * Log probabilities of given tokens under softmax(inv_temperature * logits), one pass over
+ * the logits.
+ *   logits:  [t x v] float32 or bfloat16, rows ld elements apart; -infinity rules a token out.
+ *   targets: [t] int32 (target_bits == 32) or int64 (64).
+ *   logprob: [t] float32, of the target.     entropy: [t] float32, in nats.
+ *   rank:    [t] int32: 1 + the tokens with a larger logit, or an equal one and a lower index.
+ *   top_ids, top_logprobs: [t x top] int32 / float32, by descending logit, equal logits by
+ *            ascending index; 0 <= top <= min(v, MBQ_MAX_TOP), NULL when top == 0.
+ * A target outside [0, v) gives logprob 0 and rank 0 (a padded position).  A row of nothing
+ * but -infinity gives log probabilities of -infinity and entropy 0.  A row that holds a
+ * NaN or +infinity has no distribution: its floats are NaN, its rank 0, its top_ids -1.
+ * Sums are float32 about a running maximum, in a fixed order.  inv_temperature > 0 and
+ * finite (MBQ_ERR_RANGE).  workspace: 256-byte aligned scratch.
+ */
+mbq_status mbq_token_logprobs(int32_t t, int32_t v, const void* logits, mbq_dtype dtype, int64_t ld,
+                              const void* targets, int32_t target_bits, float inv_temperature, int32_t top,
+                              float* logprob, float* entropy, int32_t* rank, int32_t* top_ids,
+                              float* top_logprobs, void* workspace, size_t ws_bytes, hipStream_t stream);
 
 /* Static string for a status code. */
 const char* mbq_status_str(mbq_status status);

@@ -12,7 +12,7 @@ import os
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmbq.so")
 
-MBQ_F32, MBQ_BF16 = 0, 1
+MBQ_F32, MBQ_BF16, MBQ_E4M3 = 0, 1, 2
 STATIC_SCRATCH_BYTES = 16 << 20      # MBQ_STATIC_SCRATCH_BYTES
 ABI_VERSION = 3
 
@@ -24,7 +24,9 @@ EXPORTS = ("mbq_describe", "mbq_pack", "mbq_pack_rows", "mbq_pack_bitplane", "mb
            "mbq_route_linear_workspace", "mbq_route_prepare_workspace", "mbq_route_prepare",
            "mbq_route_linear_prepared",
            "mbq_linear_lowrank_workspace",
-           "mbq_linear_lowrank", "mbq_status_str", "mbq_abi_version")
+           "mbq_linear_lowrank", "mbq_fp8_describe", "mbq_fp8_pack", "mbq_fp8_quantize",
+           "mbq_fp8_linear_workspace", "mbq_fp8_linear", "mbq_fp8_gated", "mbq_block_norm",
+           "mbq_token_logprobs_workspace", "mbq_token_logprobs", "mbq_status_str", "mbq_abi_version")
 
 
 class MbqDesc(ctypes.Structure):
@@ -48,6 +50,29 @@ class MbqOpts(ctypes.Structure):
     """Kernel and tiling choices of the routed linear (mbq_opts in include/mbq.h)."""
     _fields_ = [("path", ctypes.c_int32), ("decode_mul", ctypes.c_int32),
                 ("prefill_slots", ctypes.c_int32), ("decode_launches", ctypes.c_int32)]
+
+
+MBQ_ACT_SILU, MBQ_ACT_GELU_TANH = 0, 1
+MBQ_NORM_RMS, MBQ_NORM_LAYER = 0, 1
+MBQ_GATE_NONE, MBQ_GATE_CHANNEL, MBQ_GATE_TOKEN, MBQ_GATE_FULL = 0, 1, 2, 3
+MBQ_MAX_TOP = 64
+
+
+class MbqFp8Desc(ctypes.Structure):
+    """Geometry of a packed 8-bit weight (mbq_fp8_desc in include/mbq.h)."""
+    _fields_ = [("abi", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("gated", ctypes.c_int32), ("row_blocks", ctypes.c_int32), ("k_blocks", ctypes.c_int32),
+                ("scales_offset", ctypes.c_uint64), ("zeros_offset", ctypes.c_uint64),
+                ("total_bytes", ctypes.c_uint64)]
+
+
+class MbqBlockNormArgs(ctypes.Structure):
+    """Arguments of mbq_block_norm (include/mbq.h)."""
+    _fields_ = ([(f, ctypes.c_int32) for f in ("t", "k", "kind", "gate_kind", "x_dtype", "r_dtype", "h_dtype", "post")]
+                + [(f, ctypes.c_void_p) for f in ("x", "residual", "post_weight", "post_bias", "pre_weight", "pre_bias",
+                                                  "gate", "y", "h", "scale")]
+                + [(f, ctypes.c_int64) for f in ("ldx", "ldr", "ldy", "ldh")]
+                + [(f, ctypes.c_float) for f in ("residual_scale", "gate_scale", "eps")])
 
 
 class MbqError(RuntimeError):
@@ -92,6 +117,17 @@ def _load() -> ctypes.CDLL:
     lib.mbq_linear_lowrank_workspace.argtypes = [D, I32, I32, I32, P(ctypes.c_size_t)]
     lib.mbq_linear_lowrank.argtypes = [D, VP, I32, VP, I32, VP, VP, VP, VP, I32, VP, I32, VP,
                                        ctypes.c_size_t, O, VP]
+    F8, I64, F = P(MbqFp8Desc), ctypes.c_int64, ctypes.c_float
+    lib.mbq_fp8_describe.argtypes = [I32, I32, I32, F8]
+    lib.mbq_fp8_pack.argtypes = [F8, I32, VP, I32, VP, VP, VP, VP]
+    lib.mbq_fp8_quantize.argtypes = [I32, I32, VP, I32, I64, VP, I64, VP, VP]
+    lib.mbq_fp8_linear_workspace.argtypes = [F8, I32, I32, P(ctypes.c_size_t)]
+    lib.mbq_fp8_linear.argtypes = [F8, VP, I32, VP, I32, I64, VP, VP, I32, VP, ctypes.c_size_t, VP]
+    lib.mbq_fp8_gated.argtypes = [F8, VP, I32, VP, I32, I64, VP, I32, VP, I32, VP, ctypes.c_size_t, VP]
+    lib.mbq_block_norm.argtypes = [P(MbqBlockNormArgs), VP]
+    lib.mbq_token_logprobs_workspace.argtypes = [I32, I32, I32, P(ctypes.c_size_t)]
+    lib.mbq_token_logprobs.argtypes = [I32, I32, VP, I32, I64, VP, I32, F, I32, VP, VP, VP, VP, VP, VP,
+                                       ctypes.c_size_t, VP]
     lib.mbq_status_str.argtypes = [I32]
     lib.mbq_status_str.restype = ctypes.c_char_p
     lib.mbq_abi_version.argtypes = []
@@ -145,4 +181,23 @@ def lowrank_workspace_bytes(desc: MbqDesc, t: int, x_dtype: int, rank: int) -> i
     n = ctypes.c_size_t(0)
     check(LIB.mbq_linear_lowrank_workspace(ctypes.byref(desc), t, x_dtype, rank, ctypes.byref(n)),
           "mbq_linear_lowrank_workspace")
+    return int(n.value)
+
+
+def fp8_describe(n: int, k: int, gated: bool = False) -> MbqFp8Desc:
+    d = MbqFp8Desc()
+    check(LIB.mbq_fp8_describe(n, k, int(gated), ctypes.byref(d)), "mbq_fp8_describe")
+    return d
+
+
+def fp8_linear_workspace_bytes(desc: MbqFp8Desc, t: int, x_dtype: int) -> int:
+    n = ctypes.c_size_t(0)
+    check(LIB.mbq_fp8_linear_workspace(ctypes.byref(desc), t, x_dtype, ctypes.byref(n)),
+          "mbq_fp8_linear_workspace")
+    return int(n.value)
+
+
+def token_logprobs_workspace_bytes(t: int, v: int, top: int) -> int:
+    n = ctypes.c_size_t(0)
+    check(LIB.mbq_token_logprobs_workspace(t, v, top, ctypes.byref(n)), "mbq_token_logprobs_workspace")
     return int(n.value)

@@ -9,18 +9,22 @@ from __future__ import annotations
 
 import ctypes
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
 from . import _lib
-from ._lib import (MBQ_BF16, MBQ_F32, MBQ_MUL_AUTO, MBQ_MUL_BF16, MBQ_MUL_FP8_FP4, MBQ_PATH_AUTO,
-                   MBQ_PATH_GENERIC, MbqDesc, MbqError, MbqOpts, check, describe)
+from ._lib import (MBQ_BF16, MBQ_E4M3, MBQ_F32, MBQ_MUL_AUTO, MBQ_MUL_BF16, MBQ_MUL_FP8_FP4, MBQ_PATH_AUTO,
+                   MBQ_PATH_GENERIC, MbqBlockNormArgs, MbqDesc, MbqError, MbqFp8Desc, MbqOpts, check, describe,
+                   fp8_describe)
 
 __all__ = ["PackedLinear", "pack", "pack_bitplane", "pack_concat", "route", "route_from_logits", "regroup", "linear",
            "linear_workspace", "describe", "MbqError", "MlpRouter", "route_mlp",
            "route_mlp_from_scores", "route_mlp_workspace", "linear_lowrank",
            "linear_lowrank_workspace", "route_linear", "route_linear_workspace", "linear_static", "opts",
-           "route_prepare", "route_prepare_workspace", "route_linear_prepared"]
+           "route_prepare", "route_prepare_workspace", "route_linear_prepared",
+           "Fp8Linear", "fp8_describe", "fp8_pack", "fp8_pack_gated", "fp8_quantize", "fp8_linear", "fp8_gated",
+           "fp8_linear_workspace", "block_norm", "TokenLogprobs", "token_logprobs", "token_logprobs_workspace"]
 
 _FLOATS = (torch.float32, torch.bfloat16)
 
@@ -490,3 +494,262 @@ def linear_lowrank(p: PackedLinear, x: torch.Tensor, perm: torch.Tensor, offsets
                                       _p(offsets), _p(a), _p(b), rank, _p(y), _dtype(y), _p(workspace),
                                       ws_bytes, _optp(options), _stream()), "mbq_linear_lowrank")
     return y
+
+
+# --- dense operators: the 8-bit linear, its gated form, the norms around a block and the
+# --- log probabilities of tokens
+
+_F8 = torch.float8_e4m3fn
+_CODE = {torch.float32: MBQ_F32, torch.bfloat16: MBQ_BF16, _F8: MBQ_E4M3}
+
+
+def _rows(t, name: str, dtypes, device=None, shape=None) -> int:
+    """A 2-D tensor whose rows may lie apart but are contiguous inside; returns the row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be 2-D")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if shape is not None and tuple(t.shape) != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    ld = t.stride(0) if rows > 1 else cols
+    if ld < cols:
+        raise ValueError(f"{name} has overlapping rows")
+    return ld
+
+
+@dataclass
+class Fp8Linear:
+    """A packed 8-bit weight, or the two of a gated half: geometry plus the blob."""
+    desc: MbqFp8Desc
+    blob: torch.Tensor
+
+    @property
+    def n(self): return self.desc.n
+
+    @property
+    def k(self): return self.desc.k
+
+    @property
+    def gated(self): return bool(self.desc.gated)
+
+
+def _fp8_pack(ws, scales, status, out) -> Fp8Linear:
+    for i, (w, s) in enumerate(zip(ws, scales)):
+        _dev(w, "w")
+        if w.dim() != 2 or w.dtype not in _CODE:
+            raise TypeError("w must be a 2-D float32, bfloat16 or float8_e4m3fn tensor")
+        if w.shape != ws[0].shape:
+            raise ValueError(f"both weights must have one shape, got {tuple(ws[0].shape)} and {tuple(w.shape)}")
+        if w.device != ws[0].device:
+            raise ValueError("both weights must be on one device")
+        if (w.dtype == _F8) != (s is not None):
+            raise TypeError("a float8_e4m3fn weight needs its scale, and only that")
+        _opt(s, "scale", (-(-w.shape[0] // 128), -(-w.shape[1] // 128)), (torch.float32,), w.device)
+    n, k = ws[0].shape
+    dev = ws[0].device
+    _opt(status, "status", (1,), (torch.int32,), dev)
+    d = fp8_describe(n, k, len(ws) == 2)
+    if out is None:
+        out = torch.empty(int(d.total_bytes), dtype=torch.uint8, device=dev)
+    _workspace(out, "out", int(d.total_bytes), dev)
+    for part, (w, s) in enumerate(zip(ws, scales)):
+        check(_lib.LIB.mbq_fp8_pack(ctypes.byref(d), part, _p(w), _CODE[w.dtype], _p(s), _p(out), _p(status),
+                                    _stream()), "mbq_fp8_pack")
+    return Fp8Linear(d, out)
+
+
+def fp8_pack(w: torch.Tensor, scale: torch.Tensor | None = None, status: torch.Tensor | None = None,
+             out: torch.Tensor | None = None) -> Fp8Linear:
+    """8-bit pack of W [n, k]: float32 or bfloat16 (quantized to e4m3, one scale per 128 x 128
+    block), or float8_e4m3fn codes with their scale [ceil(n / 128), ceil(k / 128)] float32."""
+    return _fp8_pack((w,), (scale,), status, out)
+
+
+def fp8_pack_gated(w_gate: torch.Tensor, w_up: torch.Tensor, scale_gate: torch.Tensor | None = None,
+                   scale_up: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                   out: torch.Tensor | None = None) -> Fp8Linear:
+    """The two weights [n, k] of a gated half in one blob, for fp8_gated."""
+    return _fp8_pack((w_gate, w_up), (scale_gate, scale_up), status, out)
+
+
+def fp8_quantize(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None):
+    """e4m3 codes of x [t, k] per token and 128 inputs.  Returns (q [t, k] float8_e4m3fn,
+    scale [ceil(k / 128), t] float32): x is about q * scale."""
+    ldx = _rows(x, "x", _FLOATS)
+    t, k = x.shape
+    if q is None:
+        q = torch.empty((t, k), dtype=_F8, device=x.device)
+    ldq = _rows(q, "q", (_F8,), x.device, (t, k))
+    if scale is None:
+        scale = torch.empty((-(-k // 128), t), dtype=torch.float32, device=x.device)
+    _arg(scale, "scale", (-(-k // 128), t), (torch.float32,), x.device)
+    check(_lib.LIB.mbq_fp8_quantize(t, k, _p(x), _dtype(x), ldx, _p(q), ldq, _p(scale), _stream()),
+          "mbq_fp8_quantize")
+    return q, scale
+
+
+def fp8_linear_workspace(p: Fp8Linear, t: int, x_dtype=torch.bfloat16) -> int:
+    return _lib.fp8_linear_workspace_bytes(p.desc, t, _CODE[x_dtype])
+
+
+def _fp8_args(p, x, scale, out_dtype, y, workspace):
+    """Checks the 8-bit linear's tensors; returns (t, ldx, y, workspace, its bytes)."""
+    ldx = _rows(x, "x", tuple(_CODE))
+    t, k = x.shape
+    dev = x.device
+    if k != p.k:
+        raise ValueError(f"x has {k} inputs, the weight {p.k}")
+    _blob(p, dev)
+    if x.dtype == _F8:
+        _arg(scale, "scale", (p.desc.k_blocks, t), (torch.float32,), dev)
+    elif scale is not None:
+        raise TypeError("scale belongs to float8_e4m3fn activations")
+    if y is None:
+        y = torch.empty((t, p.n), dtype=out_dtype or (torch.bfloat16 if x.dtype == _F8 else x.dtype), device=dev)
+    _arg(y, "y", (t, p.n), _FLOATS, dev)
+    need = _lib.fp8_linear_workspace_bytes(p.desc, t, _CODE[x.dtype])
+    _workspace(workspace, "workspace", need, dev)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    return t, ldx, y, workspace, 0 if workspace is None else workspace.numel()
+
+
+def fp8_linear(p: Fp8Linear, x: torch.Tensor, scale: torch.Tensor | None = None,
+               out_dtype: torch.dtype | None = None, y: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """8-bit linear y = x . W^T: x [t, k] float32 or bfloat16 (quantized per token and 128
+    inputs within the call), or the codes and scale of fp8_quantize / block_norm."""
+    if p.gated:
+        raise ValueError("a gated blob needs fp8_gated")
+    t, ldx, y, workspace, ws_bytes = _fp8_args(p, x, scale, out_dtype, y, workspace)
+    check(_lib.LIB.mbq_fp8_linear(ctypes.byref(p.desc), _p(p.blob), t, _p(x), _CODE[x.dtype], ldx, _p(scale), _p(y),
+                                  _dtype(y), _p(workspace), ws_bytes, _stream()), "mbq_fp8_linear")
+    return y
+
+
+_ACTS = {"silu": _lib.MBQ_ACT_SILU, "gelu_tanh": _lib.MBQ_ACT_GELU_TANH}
+
+
+def fp8_gated(p: Fp8Linear, x: torch.Tensor, scale: torch.Tensor | None = None, act: str = "silu",
+              out_dtype: torch.dtype | None = None, y: torch.Tensor | None = None,
+              workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Gated half of a feed-forward block: act(x . Wg^T) * (x . Wu^T) on a gated blob."""
+    if not p.gated:
+        raise ValueError("fp8_gated needs a blob of fp8_pack_gated")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    t, ldx, y, workspace, ws_bytes = _fp8_args(p, x, scale, out_dtype, y, workspace)
+    check(_lib.LIB.mbq_fp8_gated(ctypes.byref(p.desc), _p(p.blob), t, _p(x), _CODE[x.dtype], ldx, _p(scale),
+                                 _ACTS[act], _p(y), _dtype(y), _p(workspace), ws_bytes, _stream()), "mbq_fp8_gated")
+    return y
+
+
+_KINDS = {"rms": _lib.MBQ_NORM_RMS, "layer": _lib.MBQ_NORM_LAYER}
+
+
+def block_norm(x: torch.Tensor, residual: torch.Tensor | None = None, pre: torch.Tensor | None = None,
+               post: torch.Tensor | None = None, gate: torch.Tensor | None = None, residual_scale: float = 1.0,
+               gate_scale: float = 1.0, eps: float = 1e-6, kind: str = "rms", pre_bias: torch.Tensor | None = None,
+               post_bias: torch.Tensor | None = None, quantized: bool = False, out_dtype: torch.dtype | None = None,
+               y: torch.Tensor | None = None, h: torch.Tensor | None = None, scale: torch.Tensor | None = None):
+    """The norms around a block: y = residual_scale * residual + gate_scale * gate * z with
+    z = norm(x; post) if post is given, else x, and h = norm(y; pre).
+
+    x [t, k]; residual [t, k] or None; pre, post, pre_bias, post_bias [k] float32; gate None,
+    [k] or [t] float32 (with t == k: per channel), or [t, k] of x's type; kind 'rms' or
+    'layer'.  y has residual's type (x's without one) and may be residual itself; h has x's
+    type unless out_dtype says another.  Returns (y, h), or with quantized (y, codes [t, k]
+    float8_e4m3fn, scale [ceil(k / 128), t] float32), which fp8_linear takes."""
+    if kind not in _KINDS:
+        raise ValueError(f"kind must be one of {sorted(_KINDS)}")
+    ldx = _rows(x, "x", _FLOATS)
+    t, k = shape = tuple(x.shape)
+    dev, f32 = x.device, (torch.float32,)
+    a = MbqBlockNormArgs(t=t, k=k, kind=_KINDS[kind], x_dtype=_CODE[x.dtype], post=int(post is not None), x=x.data_ptr(),
+                         ldx=ldx, residual_scale=residual_scale, gate_scale=gate_scale, eps=eps)
+    if residual is not None:
+        a.ldr = _rows(residual, "residual", _FLOATS, dev, shape)
+        a.residual = residual.data_ptr()
+    for name, v in (("pre_weight", pre), ("post_weight", post), ("pre_bias", pre_bias), ("post_bias", post_bias)):
+        if v is not None:
+            _arg(v, name, (k,), f32, dev)
+            setattr(a, name, v.data_ptr())
+    if gate is not None:
+        if gate.dim() == 2:
+            _arg(gate, "gate", shape, (x.dtype,), dev)
+            a.gate_kind = _lib.MBQ_GATE_FULL
+        elif gate.shape == (k,):
+            _arg(gate, "gate", (k,), f32, dev)
+            a.gate_kind = _lib.MBQ_GATE_CHANNEL
+        else:
+            _arg(gate, "gate", (t,), f32, dev)
+            a.gate_kind = _lib.MBQ_GATE_TOKEN
+        a.gate = gate.data_ptr()
+    r_dtype = x.dtype if residual is None else residual.dtype
+    if y is None:
+        y = torch.empty(shape, dtype=r_dtype, device=dev)
+    a.ldy = _rows(y, "y", (r_dtype,), dev, shape)
+    h_dtype = _F8 if quantized else out_dtype or (x.dtype if h is None else h.dtype)
+    if h is None:
+        h = torch.empty(shape, dtype=h_dtype, device=dev)
+    a.ldh = _rows(h, "h", (_F8,) if quantized else _FLOATS, dev, shape)
+    if quantized:
+        if scale is None:
+            scale = torch.empty((-(-k // 128), t), dtype=torch.float32, device=dev)
+        _arg(scale, "scale", (-(-k // 128), t), f32, dev)
+        a.scale = scale.data_ptr()
+    elif scale is not None:
+        raise TypeError("scale belongs to quantized=True")
+    a.r_dtype, a.h_dtype, a.y, a.h = _CODE[r_dtype], _CODE[h.dtype], y.data_ptr(), h.data_ptr()
+    check(_lib.LIB.mbq_block_norm(ctypes.byref(a), _stream()), "mbq_block_norm")
+    return (y, h, scale) if quantized else (y, h)
+
+
+class TokenLogprobs(NamedTuple):
+    """Per row: log probability of the target, entropy (nats), rank of the target (1 is the
+    best), and with top > 0 the best tokens and their log probabilities."""
+    logprob: torch.Tensor
+    entropy: torch.Tensor
+    rank: torch.Tensor
+    top_ids: torch.Tensor | None = None
+    top_logprobs: torch.Tensor | None = None
+
+
+def token_logprobs_workspace(t: int, v: int, top: int = 0) -> int:
+    return _lib.token_logprobs_workspace_bytes(t, v, top)
+
+
+def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0, inv_temperature: float = 1.0,
+                   workspace: torch.Tensor | None = None) -> TokenLogprobs:
+    """Log probabilities of targets [t] (int32 or int64; outside [0, v): a padded position)
+    under softmax(inv_temperature * logits [t, v]), with entropy, rank and the top (<= 64)
+    alternatives, equal logits by ascending token."""
+    ld = _rows(logits, "logits", _FLOATS)
+    t, v = logits.shape
+    dev = logits.device
+    _arg(targets, "targets", (t,), (torch.int32, torch.int64), dev)
+    if not 0 <= top <= min(v, _lib.MBQ_MAX_TOP):
+        raise ValueError(f"top must lie in 0 .. {min(v, _lib.MBQ_MAX_TOP)}")
+    logprob = torch.empty(t, dtype=torch.float32, device=dev)
+    entropy = torch.empty(t, dtype=torch.float32, device=dev)
+    rank = torch.empty(t, dtype=torch.int32, device=dev)
+    ids = torch.empty((t, top), dtype=torch.int32, device=dev) if top else None
+    best = torch.empty((t, top), dtype=torch.float32, device=dev) if top else None
+    need = _lib.token_logprobs_workspace_bytes(t, v, top)
+    _workspace(workspace, "workspace", need, dev)
+    if need and workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    check(_lib.LIB.mbq_token_logprobs(t, v, _p(logits), _dtype(logits), ld, _p(targets), targets.element_size() * 8,
+                                      float(inv_temperature), top, _p(logprob), _p(entropy), _p(rank), _p(ids), _p(best),
+                                      _p(workspace), 0 if workspace is None else workspace.numel(), _stream()),
+          "mbq_token_logprobs")
+    return TokenLogprobs(logprob, entropy, rank, ids, best)

@@ -32,13 +32,18 @@ SOURCES = {
     "decode_stream.hip": [],
     "prefill.hip": [],
     "prefill_mfma.hip": [],
+    "fp8_quant.hip": [],
+    "fp8_linear.hip": [],
+    "block_norm.hip": [],
+    "token_logprobs.hip": [],
 }
 
 # Translation units whose kernels must not spill registers: their load pipelines rely on
 # exact waits on the in-order memory counter, which spill traffic (scratch loads and
 # stores) would stall, and the variants a launcher can pick are chosen to fit.  The build
 # reads the compiler's resource-usage remarks and fails on any spill to scratch memory.
-SPILL_FREE = ("decode_stream.hip", "prefill_mfma.hip", "route_mlp.hip", "lowrank.hip")
+SPILL_FREE = ("decode_stream.hip", "prefill_mfma.hip", "route_mlp.hip", "lowrank.hip",
+              "fp8_quant.hip", "fp8_linear.hip", "block_norm.hip", "token_logprobs.hip")
 
 COMMON = [
     "--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17",

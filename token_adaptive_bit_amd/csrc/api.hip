@@ -454,4 +454,167 @@ mbq_status mbq_linear_lowrank(const mbq_desc* desc, const void* packed, int32_t 
                      ws_bytes, opts, stream);
 }
 
+mbq_status mbq_fp8_describe(int32_t n, int32_t k, int32_t gated, mbq_fp8_desc* out) {
+  if (!out) return MBQ_ERR_ARG;
+  if (gated != 0 && gated != 1) return MBQ_ERR_ARG;
+  if (n < 1 || k < 1 || n > (1 << 24) || k > (1 << 24)) return MBQ_ERR_SHAPE;
+  mbq_fp8_desc d{};
+  d.abi = MBQ_ABI_VERSION;
+  d.n = n;
+  d.k = k;
+  d.gated = gated;
+  d.row_blocks = (n + mbq::kRowBlock - 1) / mbq::kRowBlock * (gated + 1);
+  d.k_blocks = (k + mbq::kFp8Block - 1) / mbq::kFp8Block;
+  d.scales_offset = uint64_t(d.row_blocks) * d.k_blocks * mbq::kFp8TileBytes;
+  if (d.scales_offset >= (uint64_t(1) << 36)) return MBQ_ERR_SHAPE;  // 64 GiB: grids stay in range
+  d.zeros_offset = d.scales_offset + align256(uint64_t(gated + 1) * ((n + 127) / 128) * d.k_blocks * 4);
+  d.total_bytes = d.zeros_offset + 256;
+  *out = d;
+  return MBQ_OK;
+}
+
+namespace {
+
+mbq_status check_fp8_desc(const mbq_fp8_desc* d) {
+  if (!d) return MBQ_ERR_ARG;
+  if (d->abi != MBQ_ABI_VERSION) return MBQ_ERR_UNSUPPORTED;
+  mbq_fp8_desc ref;
+  const mbq_status st = mbq_fp8_describe(d->n, d->k, d->gated, &ref);
+  if (st != MBQ_OK) return st;
+  if (ref.row_blocks != d->row_blocks || ref.k_blocks != d->k_blocks || ref.scales_offset != d->scales_offset ||
+      ref.zeros_offset != d->zeros_offset || ref.total_bytes != d->total_bytes)
+    return MBQ_ERR_SHAPE;
+  return MBQ_OK;
+}
+
+bool valid_rows(int32_t t) { return t >= 0 && t <= (1 << 21); }  // grids of 1024 threads a row stay below 2^32
+uintptr_t element(int32_t t) { return t == MBQ_F32 ? 4 : t == MBQ_BF16 ? 2 : 1; }
+
+mbq_status fp8_linear(const mbq_fp8_desc* desc, int32_t gated, const void* packed, int32_t t, const void* x,
+                      mbq_dtype x_dtype, int64_t ldx, const float* x_scale, int act, void* y, mbq_dtype y_dtype,
+                      void* workspace, size_t ws_bytes, hipStream_t stream) {
+  const mbq_status st = check_fp8_desc(desc);
+  if (st != MBQ_OK) return st;
+  if (desc->gated != gated) return MBQ_ERR_UNSUPPORTED;
+  const bool codes = x_dtype == MBQ_E4M3;
+  if ((!valid_dtype(x_dtype) && !codes) || !valid_dtype(y_dtype)) return MBQ_ERR_ARG;
+  if (!valid_rows(t) || int64_t(t) * desc->n >= (int64_t(1) << 38)) return MBQ_ERR_SHAPE;
+  if (t == 0) return MBQ_OK;
+  if (!packed || !x || !y || codes != (x_scale != nullptr)) return MBQ_ERR_ARG;
+  if (!aligned(packed, 256) || !aligned(x, codes ? 16 : element(x_dtype)) || !aligned(x_scale, 4) ||
+      !aligned(y, element(y_dtype)))
+    return MBQ_ERR_ARG;
+  if (ldx < desc->k || (codes && (desc->k % 16 != 0 || ldx % 16 != 0))) return MBQ_ERR_SHAPE;
+  const size_t need = mbq::fp8_linear_workspace(*desc, t, x_dtype);
+  if (need && (!workspace || ws_bytes < need || !aligned(workspace, 256))) return MBQ_ERR_WORKSPACE;
+  return launched(mbq::launch_fp8_linear(*desc, packed, t, x, x_dtype, ldx, x_scale, act, y, y_dtype == MBQ_BF16,
+                                         workspace, stream));
+}
+
+}  // namespace
+
+mbq_status mbq_fp8_pack(const mbq_fp8_desc* desc, int32_t part, const void* w, mbq_dtype w_dtype, const float* w_scale,
+                        void* packed, int32_t* dev_status, hipStream_t stream) {
+  const mbq_status st = check_fp8_desc(desc);
+  if (st != MBQ_OK) return st;
+  if (part < 0 || part > desc->gated) return MBQ_ERR_ARG;
+  if (!valid_dtype(w_dtype) && w_dtype != MBQ_E4M3) return MBQ_ERR_ARG;
+  if (!w || !packed || (w_dtype == MBQ_E4M3) != (w_scale != nullptr)) return MBQ_ERR_ARG;
+  if (!aligned(packed, 256) || !aligned(w, element(w_dtype)) || !aligned(w_scale, 4) || !aligned(dev_status, 4))
+    return MBQ_ERR_ARG;
+  return launched(mbq::launch_fp8_pack(*desc, part, w, w_dtype, w_scale, packed, dev_status, stream));
+}
+
+mbq_status mbq_fp8_quantize(int32_t t, int32_t k, const void* x, mbq_dtype x_dtype, int64_t ldx, void* q, int64_t ldq,
+                            float* scale, hipStream_t stream) {
+  if (!valid_dtype(x_dtype)) return MBQ_ERR_ARG;
+  if (!valid_rows(t) || k < 1 || k > (1 << 24)) return MBQ_ERR_SHAPE;
+  if (t == 0) return MBQ_OK;
+  if (!x || !q || !scale || !aligned(x, element(x_dtype)) || !aligned(scale, 4)) return MBQ_ERR_ARG;
+  if (ldx < k || ldq < k) return MBQ_ERR_SHAPE;
+  return launched(mbq::launch_fp8_quantize(t, k, x, x_dtype == MBQ_BF16, ldx, q, ldq, false, scale, stream));
+}
+
+mbq_status mbq_fp8_linear_workspace(const mbq_fp8_desc* desc, int32_t t, mbq_dtype x_dtype, size_t* bytes) {
+  const mbq_status st = check_fp8_desc(desc);
+  if (st != MBQ_OK) return st;
+  if (!bytes || (!valid_dtype(x_dtype) && x_dtype != MBQ_E4M3)) return MBQ_ERR_ARG;
+  if (!valid_rows(t)) return MBQ_ERR_SHAPE;
+  *bytes = mbq::fp8_linear_workspace(*desc, t, x_dtype);
+  return MBQ_OK;
+}
+
+mbq_status mbq_fp8_linear(const mbq_fp8_desc* desc, const void* packed, int32_t t, const void* x, mbq_dtype x_dtype,
+                          int64_t ldx, const float* x_scale, void* y, mbq_dtype y_dtype, void* workspace,
+                          size_t ws_bytes, hipStream_t stream) {
+  return fp8_linear(desc, 0, packed, t, x, x_dtype, ldx, x_scale, -1, y, y_dtype, workspace, ws_bytes, stream);
+}
+
+mbq_status mbq_fp8_gated(const mbq_fp8_desc* desc, const void* packed, int32_t t, const void* x, mbq_dtype x_dtype,
+                         int64_t ldx, const float* x_scale, mbq_act act, void* y, mbq_dtype y_dtype, void* workspace,
+                         size_t ws_bytes, hipStream_t stream) {
+  if (act != MBQ_ACT_SILU && act != MBQ_ACT_GELU_TANH) return MBQ_ERR_ARG;
+  return fp8_linear(desc, 1, packed, t, x, x_dtype, ldx, x_scale, int(act), y, y_dtype, workspace, ws_bytes, stream);
+}
+
+mbq_status mbq_block_norm(const mbq_block_norm_args* a, hipStream_t stream) {
+  if (!a) return MBQ_ERR_ARG;
+  const auto type = [](int32_t d) { return d == MBQ_F32 || d == MBQ_BF16; };
+  const bool codes = a->h_dtype == MBQ_E4M3;
+  if (!type(a->x_dtype) || !type(a->r_dtype) || (!type(a->h_dtype) && !codes)) return MBQ_ERR_ARG;
+  if (a->kind != MBQ_NORM_RMS && a->kind != MBQ_NORM_LAYER) return MBQ_ERR_ARG;
+  if (a->gate_kind < MBQ_GATE_NONE || a->gate_kind > MBQ_GATE_FULL || (a->post != 0 && a->post != 1)) return MBQ_ERR_ARG;
+  if (!valid_rows(a->t) || a->k < 1 || a->k > (1 << 24)) return MBQ_ERR_SHAPE;
+  if (!(a->eps > 0.f) || !std::isfinite(a->eps) || !std::isfinite(a->residual_scale) || !std::isfinite(a->gate_scale))
+    return MBQ_ERR_RANGE;
+  if (!a->post && (a->post_weight || a->post_bias)) return MBQ_ERR_ARG;
+  if (a->kind == MBQ_NORM_RMS && (a->post_bias || a->pre_bias)) return MBQ_ERR_ARG;
+  if ((a->gate_kind == MBQ_GATE_NONE) != (a->gate == nullptr) && a->t > 0) return MBQ_ERR_ARG;
+  if (a->t == 0) return MBQ_OK;
+  if (!a->x || !a->h || codes != (a->scale != nullptr)) return MBQ_ERR_ARG;
+  const uintptr_t xe = element(a->x_dtype), re = element(a->r_dtype);
+  if (!aligned(a->x, xe) || !aligned(a->residual, re) || !aligned(a->y, re) || !aligned(a->h, element(a->h_dtype)) ||
+      !aligned(a->gate, a->gate_kind == MBQ_GATE_FULL ? xe : 4) || !aligned(a->scale, 4) ||
+      !aligned(a->post_weight, 4) || !aligned(a->post_bias, 4) || !aligned(a->pre_weight, 4) || !aligned(a->pre_bias, 4))
+    return MBQ_ERR_ARG;
+  if (a->ldx < a->k || a->ldh < a->k || (a->residual && a->ldr < a->k) || (a->y && a->ldy < a->k)) return MBQ_ERR_SHAPE;
+  if (a->y && a->y == a->residual && a->ldy != a->ldr) return MBQ_ERR_SHAPE;
+  return launched(mbq::launch_block_norm(*a, stream));
+}
+
+namespace {
+mbq_status logprobs_shape(int32_t t, int32_t v, int32_t top) {
+  if (!valid_rows(t) || v < 1 || v > (1 << 28)) return MBQ_ERR_SHAPE;
+  return top < 0 || top > MBQ_MAX_TOP || top > v ? MBQ_ERR_SHAPE : MBQ_OK;
+}
+}  // namespace
+
+mbq_status mbq_token_logprobs_workspace(int32_t t, int32_t v, int32_t top, size_t* bytes) {
+  if (!bytes) return MBQ_ERR_ARG;
+  const mbq_status st = logprobs_shape(t, v, top);
+  if (st == MBQ_OK) *bytes = mbq::token_logprobs_workspace(t, v, top);
+  return st;
+}
+
+mbq_status mbq_token_logprobs(int32_t t, int32_t v, const void* logits, mbq_dtype dtype, int64_t ld,
+                              const void* targets, int32_t target_bits, float inv_temperature, int32_t top,
+                              float* logprob, float* entropy, int32_t* rank, int32_t* top_ids, float* top_logprobs,
+                              void* workspace, size_t ws_bytes, hipStream_t stream) {
+  const mbq_status st = logprobs_shape(t, v, top);
+  if (st != MBQ_OK) return st;
+  if (!valid_dtype(dtype) || (target_bits != 32 && target_bits != 64)) return MBQ_ERR_ARG;
+  if (!(inv_temperature > 0.f) || !std::isfinite(inv_temperature)) return MBQ_ERR_RANGE;
+  if (t == 0) return MBQ_OK;
+  if (ld < v) return MBQ_ERR_SHAPE;
+  if (!logits || !targets || !logprob || !entropy || !rank || (top > 0 && (!top_ids || !top_logprobs))) return MBQ_ERR_ARG;
+  if (!aligned(logits, element(dtype)) || !aligned(targets, uintptr_t(target_bits / 8)) || !aligned(logprob, 4) ||
+      !aligned(entropy, 4) || !aligned(rank, 4) || !aligned(top_ids, 4) || !aligned(top_logprobs, 4))
+    return MBQ_ERR_ARG;
+  const size_t need = mbq::token_logprobs_workspace(t, v, top);
+  if (need && (!workspace || ws_bytes < need || !aligned(workspace, 256))) return MBQ_ERR_WORKSPACE;
+  return launched(mbq::launch_token_logprobs(t, v, logits, dtype == MBQ_BF16, ld, targets, target_bits == 64,
+                                             inv_temperature, top, logprob, entropy, rank, top_ids, top_logprobs,
+                                             workspace, stream));
+}
+
 }  // extern "C"

@@ -1,0 +1,182 @@
+// Device helpers of the 8-bit (e4m3) operators.
+#pragma once
+
+#include "mbq_internal.h"
+
+namespace mbq {
+
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+
+// Loads and stores of rows at any element alignment (gfx950 takes wide accesses at any
+// address; the attribute keeps the compiler from assuming more).
+typedef uint32_t u32x4_a2 __attribute__((__vector_size__(16), aligned(2)));
+typedef uint32_t u32x2_a2 __attribute__((__vector_size__(8), aligned(2)));
+typedef float f32x4_a4 __attribute__((__vector_size__(16), aligned(4)));
+typedef uint32_t u32x2_a1 __attribute__((__vector_size__(8), aligned(1)));
+
+// Elements i .. i + 7 of a row of n elements (those at n and after are 0).
+template <bool BF16>
+__device__ __forceinline__ void load8(const void* row, int64_t i, int64_t n, float (&v)[8]) {
+  if constexpr (BF16) {
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(row) + i;
+    if (i + 8 <= n) {
+      const u32x4_t w = *reinterpret_cast<const u32x4_a2*>(p);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[2 * e] = __uint_as_float(w[e] << 16);
+        v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = i + e < n ? bf16_bits_to_float(p[e]) : 0.f;
+    }
+  } else {
+    const float* p = reinterpret_cast<const float*>(row) + i;
+    if (i + 8 <= n) {
+      const f32x4_t a = *reinterpret_cast<const f32x4_a4*>(p), b = *reinterpret_cast<const f32x4_a4*>(p + 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = a[e];
+        v[4 + e] = b[e];
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = i + e < n ? p[e] : 0.f;
+    }
+  }
+}
+
+// bfloat16 pair, round to nearest even, NaN kept.
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  typedef __bf16 pair_t __attribute__((ext_vector_type(2)));
+  const pair_t p = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(uint32_t, p);
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store8(void* row, int64_t i, int64_t n, const float (&v)[8]) {
+  if constexpr (BF16) {
+    uint16_t* p = reinterpret_cast<uint16_t*>(row) + i;
+    const u32x4_t w = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]), bf16_pair(v[6], v[7])};
+    if (i + 8 <= n) {
+      *reinterpret_cast<u32x4_a2*>(p) = w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (i + e < n) p[e] = uint16_t(w[e / 2] >> (16 * (e & 1)));
+    }
+  } else {
+    float* p = reinterpret_cast<float*>(row) + i;
+    if (i + 8 <= n) {
+      *reinterpret_cast<f32x4_a4*>(p) = f32x4_t{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<f32x4_a4*>(p + 4) = f32x4_t{v[4], v[5], v[6], v[7]};
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (i + e < n) p[e] = v[e];
+    }
+  }
+}
+
+// Largest of the 16 lanes of a row, in all of them.
+__device__ __forceinline__ uint32_t max16(uint32_t m) {
+  m = max(m, uint32_t(__builtin_amdgcn_update_dpp(0, int(m), 0x128, 0xF, 0xF, true)));  // row_ror 8
+  m = max(m, uint32_t(__builtin_amdgcn_update_dpp(0, int(m), 0x124, 0xF, 0xF, true)));  // row_ror 4
+  m = max(m, uint32_t(__builtin_amdgcn_update_dpp(0, int(m), 0x122, 0xF, 0xF, true)));  // row_ror 2
+  m = max(m, uint32_t(__builtin_amdgcn_update_dpp(0, int(m), 0x121, 0xF, 0xF, true)));  // row_ror 1
+  return m;
+}
+
+// Largest magnitude as float bits: an integer maximum, exact, and above every number for
+// infinities and NaN, so they reach the scale.
+__device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) m = max(m, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+  return m;
+}
+
+// Factor that takes a block to codes and the scale that takes codes back, from the bits of
+// the block's largest magnitude (at least 2^-96, so that both are finite numbers).
+__device__ __forceinline__ float fp8_factor(uint32_t amax) { return 448.f / __uint_as_float(max(amax, 0x0F800000u)); }
+__device__ __forceinline__ float fp8_scale(uint32_t amax) { return __uint_as_float(max(amax, 0x0F800000u)) / 448.f; }
+
+// Four e4m3 codes, round to nearest even (|v| <= 448 up to a rounding, so nothing
+// saturates; NaN stays NaN).
+__device__ __forceinline__ uint32_t fp8x4(float a, float b, float c, float d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
+  return uint32_t(__builtin_amdgcn_cvt_pk_fp8_f32(c, d, w, true));
+}
+
+__device__ __forceinline__ void store_codes8(uint8_t* row, int64_t i, int64_t n, const float (&v)[8], float f) {
+  const u32x2_a1 w = {fp8x4(v[0] * f, v[1] * f, v[2] * f, v[3] * f), fp8x4(v[4] * f, v[5] * f, v[6] * f, v[7] * f)};
+  if (i + 8 <= n) {
+    *reinterpret_cast<u32x2_a1*>(row + i) = w;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (i + e < n) row[i + e] = uint8_t(w[e / 4] >> (8 * (e & 3)));
+  }
+}
+
+// 16 rows x 16 columns over 128 inputs, both operands e4m3.  Operand lane 16 c + r holds
+// row (column) r and 32 inputs; which 32 is free as long as both sides agree (here 16 c ..
+// + 15 of each half of 64).  Result lane 16 c + r holds column r, rows 4 c .. 4 c + 3.
+// The instruction's own sum over the 128 products is coarser than float32: off by 2^-16 of
+// the result on normal operands and by up to 1e-4 of the products' magnitudes where a few
+// products tower over the rest (measured; the narrower fp8 forms sum alike).  That is far
+// below the rounding of a bfloat16 output, and too much for a float32 one.
+__device__ __forceinline__ f32x4_t mfma_fp8(i32x8_t a, i32x8_t b) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+
+// Operands of a block for the two sums: the codes as they are, or (EXACT) widened to
+// bfloat16, which holds every e4m3 value, for the bfloat16 instruction, whose products are
+// exact and summed in float32 at half the rate.
+template <bool EXACT>
+struct Frag {
+  i32x8_t v;
+  __device__ __forceinline__ Frag(i32x8_t codes) : v(codes) {}
+};
+template <>
+struct Frag<true> {
+  bf16x8_t v[4];
+  __device__ __forceinline__ Frag(i32x8_t codes) {
+    typedef __bf16 pair_t __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const pair_t lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(uint32_t(codes[2 * i + e]), 1.f, false);
+        const pair_t hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(uint32_t(codes[2 * i + e]), 1.f, true);
+        v[i][4 * e] = lo[0];
+        v[i][4 * e + 1] = lo[1];
+        v[i][4 * e + 2] = hi[0];
+        v[i][4 * e + 3] = hi[1];
+      }
+  }
+};
+
+template <bool EXACT>
+__device__ __forceinline__ f32x4_t block_product(const Frag<EXACT>& a, const Frag<EXACT>& b) {
+  if constexpr (EXACT) {
+    f32x4_t d = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], d, 0, 0, 0);
+    return d;
+  } else {
+    return mfma_fp8(a.v, b.v);
+  }
+}
+
+__device__ __forceinline__ i32x8_t join(u32x4_t lo, u32x4_t hi) {
+  i32x8_t v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = int(lo[i]);
+    v[4 + i] = int(hi[i]);
+  }
+  return v;
+}
+
+}  // namespace mbq

@@ -1,0 +1,129 @@
+// e4m3 operands of the 8-bit linear: activations per token and 128 inputs, weights per
+// 128 x 128 block, laid out in the order the matrix instruction takes them.
+#include "fp8.h"
+
+namespace mbq {
+namespace {
+
+// One block of 128 inputs of one token per 16 lanes, 8 inputs a lane.  Bound by traffic
+// (x once, one byte a code); a wave covers four neighbouring blocks, so its loads and
+// stores are whole lines.
+template <bool BF16, bool PAD>
+__global__ __launch_bounds__(256) void quantize_kernel(int32_t t, int32_t k, int32_t kb, const void* __restrict__ x,
+                                                       int64_t ldx, uint8_t* __restrict__ q, int64_t ldq,
+                                                       float* __restrict__ scale) {
+  const int64_t blocks = int64_t(t) * kb;
+  const int lane = threadIdx.x & 15;
+  // whole 16-lane groups stay and leave together
+  for (int64_t b = int64_t(blockIdx.x) * 16 + threadIdx.x / 16; b < blocks; b += int64_t(gridDim.x) * 16) {
+    const int32_t row = int32_t(b / kb), blk = int32_t(b - int64_t(row) * kb);
+    const int64_t i = int64_t(blk) * kFp8Block + lane * 8;
+    float v[8];
+    load8<BF16>(reinterpret_cast<const uint8_t*>(x) + row * ldx * (BF16 ? 2 : 4), i, k, v);
+    const uint32_t m = max16(amax8(v));
+    // with PAD the row has room for whole blocks, and the inputs past k get code 0
+    store_codes8(q + row * ldq, i, PAD ? int64_t(kb) * kFp8Block : k, v, fp8_factor(m));
+    if (lane == 0) scale[int64_t(blk) * t + row] = fp8_scale(m);
+  }
+}
+
+// One 128 x 128 block of one weight per workgroup: thread 2 r + half holds 64 inputs of row
+// r, the block's maximum goes through LDS, and every lane of the packed tiles is written
+// (rows and inputs of the padding as code 0).
+template <int WT>  // 0 float32, 1 bfloat16, 2 e4m3 codes with scales given
+__global__ __launch_bounds__(256) void pack_fp8_kernel(mbq_fp8_desc d, int32_t part, const void* __restrict__ w,
+                                                       const float* __restrict__ w_scale, uint8_t* __restrict__ packed,
+                                                       int32_t* __restrict__ status) {
+  __shared__ uint32_t wmax[4];
+  const int kb = blockIdx.x % d.k_blocks, nb = blockIdx.x / d.k_blocks, tid = threadIdx.x;
+  const int r = tid >> 1, half = tid & 1;
+  const int64_t row = int64_t(nb) * 128 + r;
+  const int64_t col0 = int64_t(kb) * 128 + 64 * half;
+  uint32_t codes[16];
+  uint32_t bad = 0;
+  float s;
+  if constexpr (WT == 2) {
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(w) + row * d.k;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      uint32_t c = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t col = col0 + 4 * i + e;
+        const uint32_t b = row < d.n && col < d.k ? p[col] : 0u;
+        bad |= (b & 0x7Fu) == 0x7Fu;
+        c |= b << (8 * e);
+      }
+      codes[i] = c;
+    }
+    s = w_scale[int64_t(nb) * d.k_blocks + kb];
+    bad |= (__float_as_uint(s) & 0x7F800000u) == 0x7F800000u;
+  } else {
+    float v[64];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float u[8];
+      const uint8_t* base = reinterpret_cast<const uint8_t*>(w) + (row < d.n ? row : 0) * d.k * (WT == 1 ? 2 : 4);
+      load8<WT == 1>(base, col0 + 8 * i, row < d.n ? d.k : 0, u);
+      m = max(m, amax8(u));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[8 * i + e] = u[e];
+    }
+#pragma unroll
+    for (int o = 32; o; o >>= 1) m = max(m, uint32_t(__shfl_xor(int(m), o)));
+    if ((tid & 63) == 0) wmax[tid >> 6] = m;
+    __syncthreads();
+    m = max(max(wmax[0], wmax[1]), max(wmax[2], wmax[3]));
+    bad = m >= 0x7F800000u;
+    const float f = fp8_factor(m);
+    s = fp8_scale(m);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) codes[i] = fp8x4(v[4 * i] * f, v[4 * i + 1] * f, v[4 * i + 2] * f, v[4 * i + 3] * f);
+  }
+  const int step = d.gated ? 2 : 1;
+  const int64_t rb = (row >> 4) * step + part;
+  if (rb < d.row_blocks) {
+    uint8_t* tile = packed + (rb * d.k_blocks + kb) * kFp8TileBytes + 1024 * half + 16 * (r & 15);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {  // inputs 64 half + 16 c .. + 15
+      const u32x4_t o = {codes[4 * c], codes[4 * c + 1], codes[4 * c + 2], codes[4 * c + 3]};
+      *reinterpret_cast<u32x4_t*>(tile + 256 * c) = o;
+    }
+  }
+  const int nblk = (d.n + 127) / 128;
+  if (tid == 0)
+    reinterpret_cast<float*>(packed + d.scales_offset)[(int64_t(part) * nblk + nb) * d.k_blocks + kb] = s;
+  if (kb == 0 && nb == 0 && tid < 64) reinterpret_cast<uint32_t*>(packed + d.zeros_offset)[tid] = 0;
+  if (bad && status) atomicOr(status, 1);
+}
+
+}  // namespace
+
+hipError_t launch_fp8_quantize(int32_t t, int32_t k, const void* x, bool x_bf16, int64_t ldx, void* q, int64_t ldq,
+                               bool pad, float* scale, hipStream_t stream) {
+  if (t == 0) return hipSuccess;
+  const int32_t kb = (k + kFp8Block - 1) / kFp8Block;
+  const dim3 grid(uint32_t(std::min<int64_t>((int64_t(t) * kb + 15) / 16, 1 << 20)));
+  uint8_t* out = static_cast<uint8_t*>(q);
+  if (x_bf16) {
+    if (pad) quantize_kernel<true, true><<<grid, 256, 0, stream>>>(t, k, kb, x, ldx, out, ldq, scale);
+    else quantize_kernel<true, false><<<grid, 256, 0, stream>>>(t, k, kb, x, ldx, out, ldq, scale);
+  } else {
+    if (pad) quantize_kernel<false, true><<<grid, 256, 0, stream>>>(t, k, kb, x, ldx, out, ldq, scale);
+    else quantize_kernel<false, false><<<grid, 256, 0, stream>>>(t, k, kb, x, ldx, out, ldq, scale);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_pack(const mbq_fp8_desc& d, int32_t part, const void* w, mbq_dtype w_dtype, const float* w_scale,
+                           void* packed, int32_t* dev_status, hipStream_t stream) {
+  const dim3 grid(uint32_t(d.k_blocks) * uint32_t((d.n + 127) / 128));
+  uint8_t* out = static_cast<uint8_t*>(packed);
+  if (w_dtype == MBQ_F32) pack_fp8_kernel<0><<<grid, 256, 0, stream>>>(d, part, w, w_scale, out, dev_status);
+  else if (w_dtype == MBQ_BF16) pack_fp8_kernel<1><<<grid, 256, 0, stream>>>(d, part, w, w_scale, out, dev_status);
+  else pack_fp8_kernel<2><<<grid, 256, 0, stream>>>(d, part, w, w_scale, out, dev_status);
+  return hipGetLastError();
+}
+
+}  // namespace mbq

@@ -106,4 +106,24 @@ int lowrank_u_chunks(int32_t t, int32_t k);
 hipError_t launch_lowrank_update(int32_t t, int32_t n, const float* u, int32_t ksu, const uint16_t* b,
                                  int32_t rank, void* y, bool y_bf16, hipStream_t stream);
 
+// Dense operators (fp8_quant.hip, fp8_linear.hip, block_norm.hip, token_logprobs.hip).
+constexpr int kFp8Block = 128;      // inputs per scale
+constexpr int kFp8TileBytes = 2048; // 16 rows x 128 inputs, one byte each
+hipError_t launch_fp8_pack(const mbq_fp8_desc& d, int32_t part, const void* w, mbq_dtype w_dtype,
+                           const float* w_scale, void* packed, int32_t* dev_status, hipStream_t stream);
+hipError_t launch_fp8_quantize(int32_t t, int32_t k, const void* x, bool x_bf16, int64_t ldx, void* q,
+                               int64_t ldq, bool pad, float* scale, hipStream_t stream);
+// Bytes of the quantized activations (codes, then scales) the linear keeps in its workspace.
+size_t fp8_linear_workspace(const mbq_fp8_desc& d, int32_t t, mbq_dtype x_dtype);
+// act: -1 for the plain linear, an mbq_act for a gated blob.
+hipError_t launch_fp8_linear(const mbq_fp8_desc& d, const void* packed, int32_t t, const void* x,
+                             mbq_dtype x_dtype, int64_t ldx, const float* x_scale, int act, void* y,
+                             bool y_bf16, void* ws, hipStream_t stream);
+hipError_t launch_block_norm(const mbq_block_norm_args& a, hipStream_t stream);
+size_t token_logprobs_workspace(int32_t t, int32_t v, int32_t top);
+hipError_t launch_token_logprobs(int32_t t, int32_t v, const void* logits, bool bf16, int64_t ld,
+                                 const void* targets, bool wide, float inv_temperature, int32_t top,
+                                 float* logprob, float* entropy, int32_t* rank, int32_t* top_ids,
+                                 float* top_logprobs, void* ws, hipStream_t stream);
+
 }  // namespace mbq
