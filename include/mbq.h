@@ -480,7 +480,8 @@ mbq_status mbq_fp8_linear_workspace(const mbq_fp8_desc* desc, int32_t t, mbq_dty
  *   x:       [t x k], rows ldx elements apart (ldx >= k): float32 or bfloat16, or e4m3
  *            codes (MBQ_E4M3) of mbq_fp8_quantize or mbq_block_norm with
  *   x_scale: their scales [ceil(k / 128) x t] (NULL for the other types).  Codes need
- *            k % 16 == 0, ldx % 16 == 0 and 16-byte alignment (MBQ_ERR_SHAPE, MBQ_ERR_ARG).
+ *            k % 16 == 0, ldx % 16 == 0, ldx <= 2^24 and 16-byte alignment (MBQ_ERR_SHAPE,
+ *            MBQ_ERR_ARG).
  *   y:       [t x n] row-major, float32 or bfloat16.
  *   workspace: mbq_fp8_linear_workspace() bytes, 256-byte aligned, scratch (no state is
  *            kept; calls that overlap in time must not share one).

@@ -105,6 +105,13 @@ def test_linear_refuses(gated):
         assert call(act=2) == ARG and call(act=-1) == ARG
 
 
+def test_packed_arguments_match_the_struct():
+    """The binding packs the arguments of mbq_block_norm itself: every field where the struct has it."""
+    a = _lib.MbqBlockNormArgs.from_buffer_copy(_lib.BLOCK_NORM_ARGS.pack(*range(1, 26)))
+    got = [getattr(a, name) for name, _ in _lib.MbqBlockNormArgs._fields_]
+    assert got == list(range(1, 26)) and _lib.BLOCK_NORM_ARGS.size == ctypes.sizeof(_lib.MbqBlockNormArgs)
+
+
 def norm_call(**kw):
     a = _lib.MbqBlockNormArgs(t=4, k=100, kind=0, gate_kind=0, x_dtype=BF16, r_dtype=BF16, h_dtype=BF16, post=1, x=FAKE,
                               residual=FAKE, post_weight=FAKE, pre_weight=FAKE, y=FAKE, h=FAKE, ldx=100, ldr=100, ldy=100,
@@ -193,7 +200,7 @@ def D(t):
 def rec(monkeypatch):
     r = Recorder(L)
     monkeypatch.setattr(_lib, "LIB", r)
-    monkeypatch.setattr(api, "_stream", lambda *a: None)
+    monkeypatch.setattr(api, "_stream_of", lambda x: None)
     return r
 
 

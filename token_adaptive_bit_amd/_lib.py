@@ -7,7 +7,9 @@ missing the import of this module raises; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
+import struct
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmbq.so")
@@ -75,6 +77,10 @@ class MbqBlockNormArgs(ctypes.Structure):
                 + [(f, ctypes.c_float) for f in ("residual_scale", "gate_scale", "eps")])
 
 
+# the same arguments packed in one call (field for field as above)
+BLOCK_NORM_ARGS = struct.Struct("@8i10Q4q3f4x")
+
+
 class MbqError(RuntimeError):
     def __init__(self, status: int, what: str):
         self.status = status
@@ -124,7 +130,7 @@ def _load() -> ctypes.CDLL:
     lib.mbq_fp8_linear_workspace.argtypes = [F8, I32, I32, P(ctypes.c_size_t)]
     lib.mbq_fp8_linear.argtypes = [F8, VP, I32, VP, I32, I64, VP, VP, I32, VP, ctypes.c_size_t, VP]
     lib.mbq_fp8_gated.argtypes = [F8, VP, I32, VP, I32, I64, VP, I32, VP, I32, VP, ctypes.c_size_t, VP]
-    lib.mbq_block_norm.argtypes = [P(MbqBlockNormArgs), VP]
+    lib.mbq_block_norm.argtypes = [VP, VP]  # a packed BLOCK_NORM_ARGS, or byref(MbqBlockNormArgs)
     lib.mbq_token_logprobs_workspace.argtypes = [I32, I32, I32, P(ctypes.c_size_t)]
     lib.mbq_token_logprobs.argtypes = [I32, I32, VP, I32, I64, VP, I32, F, I32, VP, VP, VP, VP, VP, VP,
                                        ctypes.c_size_t, VP]
@@ -197,6 +203,7 @@ def fp8_linear_workspace_bytes(desc: MbqFp8Desc, t: int, x_dtype: int) -> int:
     return int(n.value)
 
 
+@functools.lru_cache(maxsize=256)
 def token_logprobs_workspace_bytes(t: int, v: int, top: int) -> int:
     n = ctypes.c_size_t(0)
     check(LIB.mbq_token_logprobs_workspace(t, v, top, ctypes.byref(n)), "mbq_token_logprobs_workspace")

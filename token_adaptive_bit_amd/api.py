@@ -15,7 +15,7 @@ import torch
 
 from . import _lib
 from ._lib import (MBQ_BF16, MBQ_E4M3, MBQ_F32, MBQ_MUL_AUTO, MBQ_MUL_BF16, MBQ_MUL_FP8_FP4, MBQ_PATH_AUTO,
-                   MBQ_PATH_GENERIC, MbqBlockNormArgs, MbqDesc, MbqError, MbqFp8Desc, MbqOpts, check, describe,
+                   MBQ_PATH_GENERIC, MbqDesc, MbqError, MbqFp8Desc, MbqOpts, check, describe,
                    fp8_describe)
 
 __all__ = ["PackedLinear", "pack", "pack_bitplane", "pack_concat", "route", "route_from_logits", "regroup", "linear",
@@ -497,14 +497,30 @@ def linear_lowrank(p: PackedLinear, x: torch.Tensor, perm: torch.Tensor, offsets
 
 
 # --- dense operators: the 8-bit linear, its gated form, the norms around a block and the
-# --- log probabilities of tokens
+# --- log probabilities of tokens.  A decode step makes many of these calls and each runs for
+# --- a few microseconds, so their checks take a short path for the ordinary tensor and name
+# --- what is wrong in a second pass.
 
 _F8 = torch.float8_e4m3fn
 _CODE = {torch.float32: MBQ_F32, torch.bfloat16: MBQ_BF16, _F8: MBQ_E4M3}
+_F32S, _F8S, _IDS = (torch.float32,), (_F8,), (torch.int32, torch.int64)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _rows(t, name: str, dtypes, device=None, shape=None) -> int:
+def _stream_of(x: torch.Tensor):
+    """The current stream of x's device, which has to be the current one."""
+    i = x.get_device()
+    if i != _current_device():
+        raise ValueError(f"x is on cuda:{i}, the current device is cuda:{_current_device()}")
+    return _raw_stream(i)
+
+
+def _rows(t, name: str, dtypes, dev=None, shape=None) -> int:
     """A 2-D tensor whose rows may lie apart but are contiguous inside; returns the row stride."""
+    if type(t) is torch.Tensor and t.is_cuda and t.dim() == 2 and t.dtype in dtypes and t.is_contiguous() \
+            and (dev is None or t.get_device() == dev) and (shape is None or t.shape == shape):
+        return t.shape[1]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if not t.is_cuda:
@@ -513,10 +529,10 @@ def _rows(t, name: str, dtypes, device=None, shape=None) -> int:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
     if t.dim() != 2:
         raise ValueError(f"{name} must be 2-D")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     rows, cols = t.shape
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{name} must have contiguous rows")
@@ -526,11 +542,39 @@ def _rows(t, name: str, dtypes, device=None, shape=None) -> int:
     return ld
 
 
+def _flat(t, name: str, dtypes, dev, shape) -> int:
+    """A contiguous tensor of this shape; returns its address."""
+    if not (type(t) is torch.Tensor and t.is_cuda and t.shape == shape and t.dtype in dtypes and t.get_device() == dev
+            and t.is_contiguous()):
+        _dev(t, name)
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.dtype not in dtypes:
+            raise TypeError(f"{name} has dtype {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    return t.data_ptr()
+
+
+def _scratch(ws, need: int, x: torch.Tensor):
+    """The workspace given, or a new one; returns (tensor to keep until the call, address, bytes)."""
+    if ws is None:
+        if not need:
+            return None, None, 0
+        ws = x.new_empty(need, dtype=torch.uint8)
+    else:
+        _workspace(ws, "workspace", need, x.device)
+    return ws, ws.data_ptr(), ws.numel()
+
+
 @dataclass
 class Fp8Linear:
     """A packed 8-bit weight, or the two of a gated half: geometry plus the blob."""
     desc: MbqFp8Desc
     blob: torch.Tensor
+
+    def __post_init__(self):
+        self._ref, self._sizes = ctypes.byref(self.desc), {}
 
     @property
     def n(self): return self.desc.n
@@ -541,9 +585,16 @@ class Fp8Linear:
     @property
     def gated(self): return bool(self.desc.gated)
 
+    def _workspace_bytes(self, t: int, code: int) -> int:
+        """Sizes already asked for, by tokens and type (they depend on nothing else)."""
+        need = self._sizes.get((t, code))
+        if need is None:
+            need = self._sizes[(t, code)] = _lib.fp8_linear_workspace_bytes(self.desc, t, code)
+        return need
+
 
 def _fp8_pack(ws, scales, status, out) -> Fp8Linear:
-    for i, (w, s) in enumerate(zip(ws, scales)):
+    for w, s in zip(ws, scales):
         _dev(w, "w")
         if w.dim() != 2 or w.dtype not in _CODE:
             raise TypeError("w must be a 2-D float32, bfloat16 or float8_e4m3fn tensor")
@@ -553,7 +604,7 @@ def _fp8_pack(ws, scales, status, out) -> Fp8Linear:
             raise ValueError("both weights must be on one device")
         if (w.dtype == _F8) != (s is not None):
             raise TypeError("a float8_e4m3fn weight needs its scale, and only that")
-        _opt(s, "scale", (-(-w.shape[0] // 128), -(-w.shape[1] // 128)), (torch.float32,), w.device)
+        _opt(s, "scale", (-(-w.shape[0] // 128), -(-w.shape[1] // 128)), _F32S, w.device)
     n, k = ws[0].shape
     dev = ws[0].device
     _opt(status, "status", (1,), (torch.int32,), dev)
@@ -561,9 +612,10 @@ def _fp8_pack(ws, scales, status, out) -> Fp8Linear:
     if out is None:
         out = torch.empty(int(d.total_bytes), dtype=torch.uint8, device=dev)
     _workspace(out, "out", int(d.total_bytes), dev)
+    stream = _stream_of(ws[0])
     for part, (w, s) in enumerate(zip(ws, scales)):
-        check(_lib.LIB.mbq_fp8_pack(ctypes.byref(d), part, _p(w), _CODE[w.dtype], _p(s), _p(out), _p(status),
-                                    _stream()), "mbq_fp8_pack")
+        check(_lib.LIB.mbq_fp8_pack(ctypes.byref(d), part, _p(w), _CODE[w.dtype], _p(s), _p(out), _p(status), stream),
+              "mbq_fp8_pack")
     return Fp8Linear(d, out)
 
 
@@ -586,41 +638,44 @@ def fp8_quantize(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Te
     scale [ceil(k / 128), t] float32): x is about q * scale."""
     ldx = _rows(x, "x", _FLOATS)
     t, k = x.shape
+    dev, kb = x.get_device(), -(-k // 128)
     if q is None:
-        q = torch.empty((t, k), dtype=_F8, device=x.device)
-    ldq = _rows(q, "q", (_F8,), x.device, (t, k))
+        q = x.new_empty((t, k), dtype=_F8)
+    ldq = _rows(q, "q", _F8S, dev, (t, k))
     if scale is None:
-        scale = torch.empty((-(-k // 128), t), dtype=torch.float32, device=x.device)
-    _arg(scale, "scale", (-(-k // 128), t), (torch.float32,), x.device)
-    check(_lib.LIB.mbq_fp8_quantize(t, k, _p(x), _dtype(x), ldx, _p(q), ldq, _p(scale), _stream()),
-          "mbq_fp8_quantize")
+        scale = x.new_empty((kb, t), dtype=torch.float32)
+    check(_lib.LIB.mbq_fp8_quantize(t, k, x.data_ptr(), _CODE[x.dtype], ldx, q.data_ptr(), ldq,
+                                    _flat(scale, "scale", _F32S, dev, (kb, t)), _stream_of(x)), "mbq_fp8_quantize")
     return q, scale
 
 
 def fp8_linear_workspace(p: Fp8Linear, t: int, x_dtype=torch.bfloat16) -> int:
-    return _lib.fp8_linear_workspace_bytes(p.desc, t, _CODE[x_dtype])
+    return p._workspace_bytes(t, _CODE[x_dtype])
 
 
-def _fp8_args(p, x, scale, out_dtype, y, workspace):
-    """Checks the 8-bit linear's tensors; returns (t, ldx, y, workspace, its bytes)."""
-    ldx = _rows(x, "x", tuple(_CODE))
+def _fp8_run(p, x, scale, act, out_dtype, y, workspace):
+    ldx = _rows(x, "x", _CODE)
     t, k = x.shape
-    dev = x.device
-    if k != p.k:
-        raise ValueError(f"x has {k} inputs, the weight {p.k}")
-    _blob(p, dev)
-    if x.dtype == _F8:
-        _arg(scale, "scale", (p.desc.k_blocks, t), (torch.float32,), dev)
+    dev, code, n, blob = x.get_device(), _CODE[x.dtype], p.desc.n, p.blob
+    if k != p.desc.k:
+        raise ValueError(f"x has {k} inputs, the weight {p.desc.k}")
+    if blob.dtype != torch.uint8 or blob.get_device() != dev or blob.numel() < p.desc.total_bytes:
+        raise ValueError(f"packed blob must be uint8 on cuda:{dev} holding at least desc.total_bytes")
+    if code == MBQ_E4M3:
+        scale = _flat(scale, "scale", _F32S, dev, (p.desc.k_blocks, t))
     elif scale is not None:
         raise TypeError("scale belongs to float8_e4m3fn activations")
     if y is None:
-        y = torch.empty((t, p.n), dtype=out_dtype or (torch.bfloat16 if x.dtype == _F8 else x.dtype), device=dev)
-    _arg(y, "y", (t, p.n), _FLOATS, dev)
-    need = _lib.fp8_linear_workspace_bytes(p.desc, t, _CODE[x.dtype])
-    _workspace(workspace, "workspace", need, dev)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    return t, ldx, y, workspace, 0 if workspace is None else workspace.numel()
+        y = x.new_empty((t, n), dtype=out_dtype or (torch.bfloat16 if code == MBQ_E4M3 else x.dtype))
+    y_ptr, y_code = _flat(y, "y", _FLOATS, dev, (t, n)), _CODE[y.dtype]
+    _ws, ws_ptr, ws_bytes = _scratch(workspace, p._workspace_bytes(t, code), x)
+    if act is None:
+        check(_lib.LIB.mbq_fp8_linear(p._ref, blob.data_ptr(), t, x.data_ptr(), code, ldx, scale, y_ptr, y_code, ws_ptr,
+                                      ws_bytes, _stream_of(x)), "mbq_fp8_linear")
+    else:
+        check(_lib.LIB.mbq_fp8_gated(p._ref, blob.data_ptr(), t, x.data_ptr(), code, ldx, scale, act, y_ptr, y_code,
+                                     ws_ptr, ws_bytes, _stream_of(x)), "mbq_fp8_gated")
+    return y
 
 
 def fp8_linear(p: Fp8Linear, x: torch.Tensor, scale: torch.Tensor | None = None,
@@ -628,12 +683,9 @@ def fp8_linear(p: Fp8Linear, x: torch.Tensor, scale: torch.Tensor | None = None,
                workspace: torch.Tensor | None = None) -> torch.Tensor:
     """8-bit linear y = x . W^T: x [t, k] float32 or bfloat16 (quantized per token and 128
     inputs within the call), or the codes and scale of fp8_quantize / block_norm."""
-    if p.gated:
+    if p.desc.gated:
         raise ValueError("a gated blob needs fp8_gated")
-    t, ldx, y, workspace, ws_bytes = _fp8_args(p, x, scale, out_dtype, y, workspace)
-    check(_lib.LIB.mbq_fp8_linear(ctypes.byref(p.desc), _p(p.blob), t, _p(x), _CODE[x.dtype], ldx, _p(scale), _p(y),
-                                  _dtype(y), _p(workspace), ws_bytes, _stream()), "mbq_fp8_linear")
-    return y
+    return _fp8_run(p, x, scale, None, out_dtype, y, workspace)
 
 
 _ACTS = {"silu": _lib.MBQ_ACT_SILU, "gelu_tanh": _lib.MBQ_ACT_GELU_TANH}
@@ -643,14 +695,11 @@ def fp8_gated(p: Fp8Linear, x: torch.Tensor, scale: torch.Tensor | None = None, 
               out_dtype: torch.dtype | None = None, y: torch.Tensor | None = None,
               workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Gated half of a feed-forward block: act(x . Wg^T) * (x . Wu^T) on a gated blob."""
-    if not p.gated:
+    if not p.desc.gated:
         raise ValueError("fp8_gated needs a blob of fp8_pack_gated")
     if act not in _ACTS:
         raise ValueError(f"act must be one of {sorted(_ACTS)}")
-    t, ldx, y, workspace, ws_bytes = _fp8_args(p, x, scale, out_dtype, y, workspace)
-    check(_lib.LIB.mbq_fp8_gated(ctypes.byref(p.desc), _p(p.blob), t, _p(x), _CODE[x.dtype], ldx, _p(scale),
-                                 _ACTS[act], _p(y), _dtype(y), _p(workspace), ws_bytes, _stream()), "mbq_fp8_gated")
-    return y
+    return _fp8_run(p, x, scale, _ACTS[act], out_dtype, y, workspace)
 
 
 _KINDS = {"rms": _lib.MBQ_NORM_RMS, "layer": _lib.MBQ_NORM_LAYER}
@@ -672,45 +721,47 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor | None = None, pre: torch
     if kind not in _KINDS:
         raise ValueError(f"kind must be one of {sorted(_KINDS)}")
     ldx = _rows(x, "x", _FLOATS)
-    t, k = shape = tuple(x.shape)
-    dev, f32 = x.device, (torch.float32,)
-    a = MbqBlockNormArgs(t=t, k=k, kind=_KINDS[kind], x_dtype=_CODE[x.dtype], post=int(post is not None), x=x.data_ptr(),
-                         ldx=ldx, residual_scale=residual_scale, gate_scale=gate_scale, eps=eps)
+    shape = x.shape
+    t, k = shape
+    dev = x.get_device()
+    r_dtype, r_ptr, ldr = x.dtype, 0, 0
     if residual is not None:
-        a.ldr = _rows(residual, "residual", _FLOATS, dev, shape)
-        a.residual = residual.data_ptr()
-    for name, v in (("pre_weight", pre), ("post_weight", post), ("pre_bias", pre_bias), ("post_bias", post_bias)):
-        if v is not None:
-            _arg(v, name, (k,), f32, dev)
-            setattr(a, name, v.data_ptr())
+        ldr = _rows(residual, "residual", _FLOATS, dev, shape)
+        r_dtype, r_ptr = residual.dtype, residual.data_ptr()
+    pre_ptr = 0 if pre is None else _flat(pre, "pre", _F32S, dev, (k,))
+    post_ptr = 0 if post is None else _flat(post, "post", _F32S, dev, (k,))
+    preb_ptr = 0 if pre_bias is None else _flat(pre_bias, "pre_bias", _F32S, dev, (k,))
+    postb_ptr = 0 if post_bias is None else _flat(post_bias, "post_bias", _F32S, dev, (k,))
+    gate_kind = gate_ptr = 0
     if gate is not None:
         if gate.dim() == 2:
-            _arg(gate, "gate", shape, (x.dtype,), dev)
-            a.gate_kind = _lib.MBQ_GATE_FULL
+            gate_kind, gate_ptr = _lib.MBQ_GATE_FULL, _flat(gate, "gate", (x.dtype,), dev, shape)
         elif gate.shape == (k,):
-            _arg(gate, "gate", (k,), f32, dev)
-            a.gate_kind = _lib.MBQ_GATE_CHANNEL
+            gate_kind, gate_ptr = _lib.MBQ_GATE_CHANNEL, _flat(gate, "gate", _F32S, dev, (k,))
         else:
-            _arg(gate, "gate", (t,), f32, dev)
-            a.gate_kind = _lib.MBQ_GATE_TOKEN
-        a.gate = gate.data_ptr()
-    r_dtype = x.dtype if residual is None else residual.dtype
+            gate_kind, gate_ptr = _lib.MBQ_GATE_TOKEN, _flat(gate, "gate", _F32S, dev, (t,))
     if y is None:
-        y = torch.empty(shape, dtype=r_dtype, device=dev)
-    a.ldy = _rows(y, "y", (r_dtype,), dev, shape)
-    h_dtype = _F8 if quantized else out_dtype or (x.dtype if h is None else h.dtype)
+        y, ldy = x.new_empty(shape, dtype=r_dtype), k
+    else:
+        ldy = _rows(y, "y", (r_dtype,), dev, shape)
     if h is None:
-        h = torch.empty(shape, dtype=h_dtype, device=dev)
-    a.ldh = _rows(h, "h", (_F8,) if quantized else _FLOATS, dev, shape)
+        h, ldh = x.new_empty(shape, dtype=_F8 if quantized else out_dtype or x.dtype), k
+    else:
+        ldh = _rows(h, "h", _F8S if quantized else _FLOATS if out_dtype is None else (out_dtype,), dev, shape)
+    s_ptr = 0
     if quantized:
         if scale is None:
-            scale = torch.empty((-(-k // 128), t), dtype=torch.float32, device=dev)
-        _arg(scale, "scale", (-(-k // 128), t), f32, dev)
-        a.scale = scale.data_ptr()
+            scale = x.new_empty((-(-k // 128), t), dtype=torch.float32)
+        s_ptr = _flat(scale, "scale", _F32S, dev, (-(-k // 128), t))
     elif scale is not None:
         raise TypeError("scale belongs to quantized=True")
-    a.r_dtype, a.h_dtype, a.y, a.h = _CODE[r_dtype], _CODE[h.dtype], y.data_ptr(), h.data_ptr()
-    check(_lib.LIB.mbq_block_norm(ctypes.byref(a), _stream()), "mbq_block_norm")
+    if h.dtype not in _CODE:
+        raise TypeError(f"out_dtype {h.dtype}, expected float32 or bfloat16")
+    args = _lib.BLOCK_NORM_ARGS.pack(t, k, _KINDS[kind], gate_kind, _CODE[x.dtype], _CODE[r_dtype], _CODE[h.dtype],
+                                     post is not None, x.data_ptr(), r_ptr, post_ptr, postb_ptr, pre_ptr, preb_ptr,
+                                     gate_ptr, y.data_ptr(), h.data_ptr(), s_ptr, ldx, ldr, ldy, ldh, residual_scale,
+                                     gate_scale, eps)
+    check(_lib.LIB.mbq_block_norm(args, _stream_of(x)), "mbq_block_norm")
     return (y, h, scale) if quantized else (y, h)
 
 
@@ -735,21 +786,19 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0, in
     alternatives, equal logits by ascending token."""
     ld = _rows(logits, "logits", _FLOATS)
     t, v = logits.shape
-    dev = logits.device
-    _arg(targets, "targets", (t,), (torch.int32, torch.int64), dev)
+    dev = logits.get_device()
+    tg_ptr = _flat(targets, "targets", _IDS, dev, (t,))
     if not 0 <= top <= min(v, _lib.MBQ_MAX_TOP):
         raise ValueError(f"top must lie in 0 .. {min(v, _lib.MBQ_MAX_TOP)}")
-    logprob = torch.empty(t, dtype=torch.float32, device=dev)
-    entropy = torch.empty(t, dtype=torch.float32, device=dev)
-    rank = torch.empty(t, dtype=torch.int32, device=dev)
-    ids = torch.empty((t, top), dtype=torch.int32, device=dev) if top else None
-    best = torch.empty((t, top), dtype=torch.float32, device=dev) if top else None
-    need = _lib.token_logprobs_workspace_bytes(t, v, top)
-    _workspace(workspace, "workspace", need, dev)
-    if need and workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    check(_lib.LIB.mbq_token_logprobs(t, v, _p(logits), _dtype(logits), ld, _p(targets), targets.element_size() * 8,
-                                      float(inv_temperature), top, _p(logprob), _p(entropy), _p(rank), _p(ids), _p(best),
-                                      _p(workspace), 0 if workspace is None else workspace.numel(), _stream()),
-          "mbq_token_logprobs")
+    logprob, entropy = logits.new_empty(t, dtype=torch.float32), logits.new_empty(t, dtype=torch.float32)
+    rank = logits.new_empty(t, dtype=torch.int32)
+    ids = best = ids_ptr = best_ptr = None
+    if top:
+        ids, best = logits.new_empty((t, top), dtype=torch.int32), logits.new_empty((t, top), dtype=torch.float32)
+        ids_ptr, best_ptr = ids.data_ptr(), best.data_ptr()
+    _ws, ws_ptr, ws_bytes = _scratch(workspace, _lib.token_logprobs_workspace_bytes(t, v, top), logits)
+    check(_lib.LIB.mbq_token_logprobs(t, v, logits.data_ptr(), _CODE[logits.dtype], ld, tg_ptr,
+                                      32 if targets.dtype == torch.int32 else 64, inv_temperature, top,
+                                      logprob.data_ptr(), entropy.data_ptr(), rank.data_ptr(), ids_ptr, best_ptr, ws_ptr,
+                                      ws_bytes, _stream_of(logits)), "mbq_token_logprobs")
     return TokenLogprobs(logprob, entropy, rank, ids, best)

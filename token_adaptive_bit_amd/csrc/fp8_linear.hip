@@ -21,6 +21,7 @@ struct LinArgs {
 };
 
 constexpr int kPlain = -1;
+typedef __attribute__((address_space(4))) float ConstFloat;  // read by scalar loads
 
 template <int ACT>
 __device__ __forceinline__ float gated(float g, float u) {
@@ -49,41 +50,83 @@ __device__ __forceinline__ void store4(void* y, int64_t row, int32_t n, int32_t 
   }
 }
 
-__device__ __forceinline__ void to_lds(const uint8_t* g, uint8_t* l) {
-  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)g,
-                                   (__attribute__((address_space(3))) void*)l, 16, 0, 0);
+// 16 (or 4) bytes a lane from memory to LDS, the lanes side by side at l.  Written in
+// assembly because the compiler waits for every copy in flight before any LDS read that
+// follows one of its own (it cannot tell the buffers apart).  The instruction has no
+// register outputs; to_lds_wait() before the barrier completes it.
+template <int BYTES>
+__device__ __forceinline__ void to_lds(const void* base, uint32_t offset, const uint8_t* l) {  // base, l: the wave's
+  const uint32_t at = uint32_t(uintptr_t((const __attribute__((address_space(3))) uint8_t*)l));
+  if constexpr (BYTES == 16)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 ::"s"(at), "v"(offset), "s"(base) : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
+                 ::"s"(at), "v"(offset), "s"(base) : "memory", "m0");
 }
+__device__ __forceinline__ void to_lds_from(const uint8_t* g, const uint8_t* l) {  // 16 bytes at each lane's own g
+  const uint32_t at = uint32_t(uintptr_t((const __attribute__((address_space(3))) uint8_t*)l));
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(g) : "memory", "m0");
+}
+__device__ __forceinline__ void to_lds_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// Tiles of 16 RN WN packed rows x 16 RT WT tokens on WN WT waves, both operands through
-// two LDS buffers.
+// Tiles of 16 RN WN packed rows x 16 RT WT tokens on WN WT = 8 waves; both operands and the
+// tokens' scales of a block go through LDS in two buffers, one block ahead.
 template <int RN, int RT, int WN, int WT, int ACT, bool YBF>
-__global__ __launch_bounds__(64 * WN * WT) void gemm_kernel(LinArgs a) {
-  constexpr int kWaves = WN * WT, kRb = RN * WN, kTb = RT * WT;
-  __shared__ __align__(1024) uint8_t lds[2][(kRb + kTb) * kFp8TileBytes];
+__global__ __launch_bounds__(64 * WN * WT, 2) void gemm_kernel(LinArgs a) {
+  constexpr int kWaves = WN * WT, kRb = RN * WN, kTb = RT * WT, kTok = 16 * kTb;
+  constexpr int kStage = (kRb + kTb) * kFp8TileBytes + kTok * 4;
+  constexpr int kCopiesW = 2 * kRb / kWaves, kCopiesX = 2 * kTb / kWaves;  // a wave's copies to LDS a block
+  static_assert(2 * kRb % kWaves == 0 && 2 * kTb % kWaves == 0 && kTok % 64 == 0, "whole copies");
+  __shared__ __align__(1024) uint8_t lds[2][kStage];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, c = lane >> 4;
   const int wn = wave % WN, wt = wave / WN;
-  const int tiles_t = (a.t + 16 * kTb - 1) / (16 * kTb);
-  const int tn = blockIdx.x / tiles_t, tt = blockIdx.x % tiles_t;
-  const int rb0 = tn * kRb, tok0 = tt * kTb * 16;
+  // neighbouring tiles (four token tiles by as many row tiles as it takes) on one XCD
+  const int tiles_t = (a.t + kTok - 1) / kTok, tiles_n = (a.rbs + kRb - 1) / kRb;
+  const int per = gridDim.x / 8, rest = gridDim.x % 8, xcd = blockIdx.x % 8;
+  const int id = blockIdx.x / 8 + xcd * per + min(xcd, rest);
+  const int group = id / (4 * tiles_n), gt = min(4, tiles_t - 4 * group), in = id - group * 4 * tiles_n;
+  const int rb0 = in / gt * kRb, tok0 = (4 * group + in % gt) * kTok;
 
-  auto issue = [&](int kb, int buf) {
+  // a wave's rows lie in one 128-row block of each weight
+  const int rbw = min(rb0 + wn * RN, a.rbs - 1);
+  const ConstFloat* wsp = (const ConstFloat*)a.ws + int64_t(ACT == kPlain ? rbw / 8 : rbw / 16) * a.kb;
+  const ConstFloat* wsu = wsp + int64_t(a.nblk) * a.kb;
+
+  const uint8_t* wp[kCopiesW];
 #pragma unroll
-    for (int i = 0; i < (kRb + kTb + kWaves - 1) / kWaves; ++i) {
-      const int tile = i * kWaves + wave;
-      if (tile < kRb) {
-        const int rb = min(rb0 + tile, a.rbs - 1);
-        const uint8_t* g = a.codes + (int64_t(rb) * a.kb + kb) * kFp8TileBytes + lane * 16;
-        to_lds(g, &lds[buf][tile * kFp8TileBytes]);
-        to_lds(g + 1024, &lds[buf][tile * kFp8TileBytes + 1024]);
-      } else if (tile < kRb + kTb) {
-        const int tok = min(tok0 + (tile - kRb) * 16 + r, a.t - 1);
-        const int col = kb * kFp8Block + 16 * c;
-        const uint8_t* g = a.xq + tok * a.ldq + col;
-        to_lds(col < a.xlim ? g : a.zeros, &lds[buf][tile * kFp8TileBytes]);
-        to_lds(col + 64 < a.xlim ? g + 64 : a.zeros, &lds[buf][tile * kFp8TileBytes + 1024]);
+  for (int i = 0; i < kCopiesW; ++i) {
+    const int half = i * kWaves + wave;
+    wp[i] = a.codes + int64_t(min(rb0 + (half >> 1), a.rbs - 1)) * a.kb * kFp8TileBytes + (half & 1) * 1024;
+  }
+  const uint8_t* xb = a.xq + tok0 * a.ldq;
+  uint32_t xo[kCopiesX];  // this lane's 16 bytes from there: 256 rows of at most 2^24 bytes
+#pragma unroll
+  for (int i = 0; i < kCopiesX; ++i) {
+    const int half = i * kWaves + wave;
+    xo[i] = uint32_t(min((half >> 1) * 16 + r, a.t - 1 - tok0)) * uint32_t(a.ldq) + 64 * (half & 1) + 16 * c;
+  }
+  const int xchunk = wave % (kTok / 64);
+  const uint32_t so = uint32_t(min(tok0 + xchunk * 64 + lane, a.t - 1));
+
+  auto copy = [&](int kb, int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kCopiesW; ++i)
+      to_lds<16>(wp[i] + int64_t(kb) * kFp8TileBytes, uint32_t(lane) * 16, &lds[buf][(i * kWaves + wave) * 1024]);
+    if (kb * kFp8Block + kFp8Block <= a.xlim) {
+#pragma unroll
+      for (int i = 0; i < kCopiesX; ++i)
+        to_lds<16>(xb + int64_t(kb) * kFp8Block, xo[i], &lds[buf][(2 * kRb + i * kWaves + wave) * 1024]);
+    } else {  // the end of a row of codes that is no whole block: zeros after it
+#pragma unroll
+      for (int i = 0; i < kCopiesX; ++i) {
+        const int half = i * kWaves + wave;
+        const bool in_row = kb * kFp8Block + 64 * (half & 1) + 16 * c < a.xlim;
+        to_lds_from(in_row ? xb + int64_t(kb) * kFp8Block + xo[i] : a.zeros, &lds[buf][(2 * kRb + half) * 1024]);
       }
     }
+    to_lds<4>(a.xs + int64_t(kb) * a.t, so * 4, &lds[buf][(kRb + kTb) * kFp8TileBytes + xchunk * 256]);
   };
 
   f32x4_t acc[RN][RT];
@@ -92,45 +135,44 @@ __global__ __launch_bounds__(64 * WN * WT) void gemm_kernel(LinArgs a) {
 #pragma unroll
     for (int j = 0; j < RT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  // a wave's rows lie in one 128-row block of each weight
-  const int rbw = min(rb0 + wn * RN, a.rbs - 1);
-  const float* wsp = a.ws + int64_t(ACT == kPlain ? rbw / 8 : rbw / 16) * a.kb;
-  const float* wsu = wsp + int64_t(a.nblk) * a.kb;
-  int tok[RT];
-#pragma unroll
-  for (int j = 0; j < RT; ++j) tok[j] = min(tok0 + (wt * RT + j) * 16 + r, a.t - 1);
-
-  issue(0, 0);
+  copy(0, 0);
   for (int kb = 0; kb < a.kb; ++kb) {
-    const int buf = kb & 1;
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-    if (kb + 1 < a.kb) issue(kb + 1, buf ^ 1);
-    float s[ACT == kPlain ? 1 : 2][RT];
+    const uint8_t* buf = lds[kb & 1];
+    to_lds_wait();
+    __syncthreads();  // block kb is in, and every wave has left the other buffer
+    if (kb + 1 < a.kb) copy(kb + 1, (kb & 1) ^ 1);
+    auto frag = [&](int tile) __attribute__((always_inline)) {
+      const u32x4_t* p = reinterpret_cast<const u32x4_t*>(buf + tile * kFp8TileBytes) + lane;
+      return join(p[0], p[64]);
+    };
+    i32x8_t x[RT];
+    float xs[RT];
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
-      const float xs = a.xs[int64_t(kb) * a.t + tok[j]];
-      s[0][j] = xs * wsp[kb];
-      if constexpr (ACT != kPlain) s[1][j] = xs * wsu[kb];
+      const int tile = wt * RT + j;
+      x[j] = frag(kRb + tile);
+      xs[j] = reinterpret_cast<const float*>(buf + (kRb + kTb) * kFp8TileBytes)[tile * 16 + r];
     }
-    auto frag = [&](int tile) {
-      const uint8_t* p = &lds[buf][tile * kFp8TileBytes + lane * 16];
-      return join(*reinterpret_cast<const u32x4_t*>(p), *reinterpret_cast<const u32x4_t*>(p + 1024));
-    };
-    i32x8_t xf[RT];
+    constexpr int P = ACT == kPlain ? 1 : 2;
 #pragma unroll
-    for (int j = 0; j < RT; ++j) xf[j] = frag(kRb + wt * RT + j);
+    for (int part = 0; part < P; ++part) {  // gated: all gate tiles, then all up tiles
+      const float w_scale = (part ? wsu : wsp)[kb];
+      float s[RT];
 #pragma unroll
-    for (int i = 0; i < RN; ++i) {
-      const Frag<!YBF> wf = frag(wn * RN + i);
+      for (int j = 0; j < RT; ++j) s[j] = xs[j] * w_scale;
 #pragma unroll
-      for (int j = 0; j < RT; ++j) {
-        const f32x4_t d = block_product<!YBF>(wf, xf[j]);
+      for (int i = part; i < RN; i += P) {
+        const Frag<!YBF> w = frag(wn * RN + i);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[e], s[ACT == kPlain ? 0 : i & 1][j], acc[i][j][e]);
+        for (int j = 0; j < RT; ++j) {
+          const f32x4_t d = block_product<!YBF>(w, x[j]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[e], s[j], acc[i][j][e]);
+        }
       }
     }
   }
+
 #pragma unroll
   for (int j = 0; j < RT; ++j) {
     const int token = tok0 + (wt * RT + j) * 16 + r;
