@@ -428,7 +428,6 @@ mbq_status mbq_linear_lowrank(const mbq_desc* desc, const void* packed, int32_t 
  *          Rows >= n and inputs >= k are padding (code 0).
  *   scales at +scales_offset: float32 [gated + 1][ceil(n / 128)][k_blocks], one per
  *          128 x 128 block of each weight.
- *   zeros  at +zeros_offset: 256 bytes of 0.
  */
 typedef struct {
   int32_t abi;             /* MBQ_ABI_VERSION */
@@ -437,8 +436,7 @@ typedef struct {
   int32_t row_blocks;      /* ceil(n / 16) * (gated + 1) */
   int32_t k_blocks;        /* ceil(k / 128) */
   uint64_t scales_offset;  /* row_blocks * k_blocks * 2048 */
-  uint64_t zeros_offset;   /* scales_offset + the scales, rounded up to 256 */
-  uint64_t total_bytes;    /* zeros_offset + 256 */
+  uint64_t total_bytes;    /* scales_offset + the scales, rounded up to 256 */
 } mbq_fp8_desc;
 
 /* Host only: validates the shape (1 <= n, k <= 2^24, codes below 64 GiB) and fills *out.

@@ -28,7 +28,7 @@ def test_describe(n, k, gated, rbs, kbs, scales):
     st, d = desc(n, k, gated)
     assert st == OK and (d.row_blocks, d.k_blocks) == (rbs, kbs)
     assert d.scales_offset == rbs * kbs * 2048
-    assert d.zeros_offset == d.scales_offset + (scales * 4 + 255) // 256 * 256 and d.total_bytes == d.zeros_offset + 256
+    assert d.total_bytes == d.scales_offset + (scales * 4 + 255) // 256 * 256
 
 
 def test_describe_refuses():
@@ -52,7 +52,7 @@ def test_pack_refuses():
     assert call(dp, 0, P(FAKE + 2), F32, None, f, None, None) == ARG
     assert call(dp, 0, P(FAKE + 1), BF16, None, f, None, None) == ARG
     assert call(dp, 0, f, F32, None, f, P(FAKE + 2), None) == ARG
-    for field, st in (("abi", UNSUP), ("k_blocks", SHAPE), ("total_bytes", SHAPE), ("zeros_offset", SHAPE)):
+    for field, st in (("abi", UNSUP), ("k_blocks", SHAPE), ("total_bytes", SHAPE)):
         bad = _lib.MbqFp8Desc.from_buffer_copy(d)
         setattr(bad, field, getattr(bad, field) + 1)
         assert call(ctypes.byref(bad), 0, f, F32, None, f, None, None) == st

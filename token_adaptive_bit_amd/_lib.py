@@ -64,8 +64,7 @@ class MbqFp8Desc(ctypes.Structure):
     """Geometry of a packed 8-bit weight (mbq_fp8_desc in include/mbq.h)."""
     _fields_ = [("abi", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
                 ("gated", ctypes.c_int32), ("row_blocks", ctypes.c_int32), ("k_blocks", ctypes.c_int32),
-                ("scales_offset", ctypes.c_uint64), ("zeros_offset", ctypes.c_uint64),
-                ("total_bytes", ctypes.c_uint64)]
+                ("scales_offset", ctypes.c_uint64), ("total_bytes", ctypes.c_uint64)]
 
 
 class MbqBlockNormArgs(ctypes.Structure):

@@ -467,8 +467,7 @@ mbq_status mbq_fp8_describe(int32_t n, int32_t k, int32_t gated, mbq_fp8_desc* o
   d.k_blocks = (k + mbq::kFp8Block - 1) / mbq::kFp8Block;
   d.scales_offset = uint64_t(d.row_blocks) * d.k_blocks * mbq::kFp8TileBytes;
   if (d.scales_offset >= (uint64_t(1) << 36)) return MBQ_ERR_SHAPE;  // 64 GiB: grids stay in range
-  d.zeros_offset = d.scales_offset + align256(uint64_t(gated + 1) * ((n + 127) / 128) * d.k_blocks * 4);
-  d.total_bytes = d.zeros_offset + 256;
+  d.total_bytes = d.scales_offset + align256(uint64_t(gated + 1) * ((n + 127) / 128) * d.k_blocks * 4);
   *out = d;
   return MBQ_OK;
 }
@@ -482,7 +481,7 @@ mbq_status check_fp8_desc(const mbq_fp8_desc* d) {
   const mbq_status st = mbq_fp8_describe(d->n, d->k, d->gated, &ref);
   if (st != MBQ_OK) return st;
   if (ref.row_blocks != d->row_blocks || ref.k_blocks != d->k_blocks || ref.scales_offset != d->scales_offset ||
-      ref.zeros_offset != d->zeros_offset || ref.total_bytes != d->total_bytes)
+      ref.total_bytes != d->total_bytes)
     return MBQ_ERR_SHAPE;
   return MBQ_OK;
 }

@@ -13,11 +13,13 @@ struct LinArgs {
   const uint8_t* codes;  // packed tiles
   const float* ws;       // weight scales [parts][nblk][kb]
   const uint8_t* xq;     // activation codes, rows of ldq bytes, xlim of them readable
-  const uint8_t* zeros;  // 16 or more bytes of 0
   const float* xs;       // activation scales [kb][t]
   void* y;
-  int64_t ldq;
-  int32_t t, n, kb, rbs, nblk, xlim;
+  float* part;           // split K: sums [chunks][t][16 rbs], joined by a second launch
+  const void* x;         // float activations, rows of ldx elements (quantized in the kernel)
+  int64_t ldq, ldx;
+  int32_t t, n, k, kb, rbs, nblk, xlim;
+  int32_t chunks, chunk_kb;  // chunks of the blocks, chunk_kb each (the last one less)
 };
 
 constexpr int kPlain = -1;
@@ -55,8 +57,8 @@ __device__ __forceinline__ void store4(void* y, int64_t row, int32_t n, int32_t 
 // follows one of its own (it cannot tell the buffers apart).  The instruction has no
 // register outputs; to_lds_wait() before the barrier completes it.
 template <int BYTES>
-__device__ __forceinline__ void to_lds(const void* base, uint32_t offset, const uint8_t* l) {  // base, l: the wave's
-  const uint32_t at = uint32_t(uintptr_t((const __attribute__((address_space(3))) uint8_t*)l));
+__device__ __forceinline__ void to_lds(const void* base, uint32_t offset, const void* l) {  // base, l: the wave's
+  const uint32_t at = uint32_t(uintptr_t((const __attribute__((address_space(3))) void*)l));
   if constexpr (BYTES == 16)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                  ::"s"(at), "v"(offset), "s"(base) : "memory", "m0");
@@ -64,70 +66,81 @@ __device__ __forceinline__ void to_lds(const void* base, uint32_t offset, const 
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
                  ::"s"(at), "v"(offset), "s"(base) : "memory", "m0");
 }
-__device__ __forceinline__ void to_lds_from(const uint8_t* g, const uint8_t* l) {  // 16 bytes at each lane's own g
-  const uint32_t at = uint32_t(uintptr_t((const __attribute__((address_space(3))) uint8_t*)l));
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(at), "v"(g) : "memory", "m0");
+// Waits until at most N of the wave's copies are on their way (nothing else of it may be).
+template <int N>
+__device__ __forceinline__ void to_lds_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ void to_lds_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
-// Tiles of 16 RN WN packed rows x 16 RT WT tokens on WN WT = 8 waves; both operands and the
-// tokens' scales of a block go through LDS in two buffers, one block ahead.
-template <int RN, int RT, int WN, int WT, int ACT, bool YBF>
-__global__ __launch_bounds__(64 * WN * WT, 2) void gemm_kernel(LinArgs a) {
-  constexpr int kWaves = WN * WT, kRb = RN * WN, kTb = RT * WT, kTok = 16 * kTb;
-  constexpr int kStage = (kRb + kTb) * kFp8TileBytes + kTok * 4;
-  constexpr int kCopiesW = 2 * kRb / kWaves, kCopiesX = 2 * kTb / kWaves;  // a wave's copies to LDS a block
-  static_assert(2 * kRb % kWaves == 0 && 2 * kTb % kWaves == 0 && kTok % 64 == 0, "whole copies");
-  __shared__ __align__(1024) uint8_t lds[2][kStage];
+// Tiles of 32 RN packed rows x 64 RT tokens on 2 x 4 waves (16 RN rows x 16 RT tokens each);
+// both operands and the tokens' scales of a block go through NS LDS buffers, NS - 1 blocks
+// ahead.  With few tiles K is split into chunks, one workgroup each.
+template <int RN, int RT, int NS, int ACT, bool YBF>
+__global__ __launch_bounds__(512, 2) void gemm_kernel(LinArgs a) {
+  constexpr int kRb = 2 * RN, kTb = 4 * RT, kTok = 16 * kTb;
+  constexpr int kCopiesW = 2 * kRb / 8, kCopiesX = RT;  // a wave's 1 KiB copies to LDS a block
+  constexpr int kCopies = kCopiesW + kCopiesX + 1;
+  static_assert(ACT == kPlain || RN % 2 == 0, "a gate tile and its up tile in one wave");
+  static_assert(2 * kRb % 8 == 0, "every wave makes as many copies as the waits count");
+  __shared__ __align__(1024) uint8_t lds[NS][(kRb + kTb) * kFp8TileBytes];
+  __shared__ float lxs[NS][kTok];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, c = lane >> 4;
-  const int wn = wave % WN, wt = wave / WN;
+  const int wn = wave & 1, wt = wave >> 1;
   // neighbouring tiles (four token tiles by as many row tiles as it takes) on one XCD
   const int tiles_t = (a.t + kTok - 1) / kTok, tiles_n = (a.rbs + kRb - 1) / kRb;
   const int per = gridDim.x / 8, rest = gridDim.x % 8, xcd = blockIdx.x % 8;
-  const int id = blockIdx.x / 8 + xcd * per + min(xcd, rest);
+  const int wg = blockIdx.x / 8 + xcd * per + min(xcd, rest);
+  const int chunk = wg % a.chunks, id = wg / a.chunks;
+  const int kb0 = chunk * a.chunk_kb, kb1 = min(kb0 + a.chunk_kb, a.kb);
   const int group = id / (4 * tiles_n), gt = min(4, tiles_t - 4 * group), in = id - group * 4 * tiles_n;
   const int rb0 = in / gt * kRb, tok0 = (4 * group + in % gt) * kTok;
 
   // a wave's rows lie in one 128-row block of each weight
-  const int rbw = min(rb0 + wn * RN, a.rbs - 1);
-  const ConstFloat* wsp = (const ConstFloat*)a.ws + int64_t(ACT == kPlain ? rbw / 8 : rbw / 16) * a.kb;
-  const ConstFloat* wsu = wsp + int64_t(a.nblk) * a.kb;
+  static_assert(ACT == kPlain ? 8 % RN == 0 : 16 % RN == 0, "one scale a weight");
+  const int rbw = rb0 + wn * RN, rbl = min(rbw, a.rbs - 1);
+  constexpr int P = ACT == kPlain ? 1 : 2;
+  const ConstFloat* wsp = (const ConstFloat*)a.ws + int64_t(rbl / (8 * P)) * a.kb;
+  auto scale_at = [&](int part, int kb) __attribute__((always_inline)) { return wsp[int64_t(part) * a.nblk * a.kb + kb]; };
 
   const uint8_t* wp[kCopiesW];
 #pragma unroll
   for (int i = 0; i < kCopiesW; ++i) {
-    const int half = i * kWaves + wave;
+    const int half = i * 8 + wave;
     wp[i] = a.codes + int64_t(min(rb0 + (half >> 1), a.rbs - 1)) * a.kb * kFp8TileBytes + (half & 1) * 1024;
   }
   const uint8_t* xb = a.xq + tok0 * a.ldq;
-  uint32_t xo[kCopiesX];  // this lane's 16 bytes from there: 256 rows of at most 2^24 bytes
+  const int col = 64 * (wave & 1) + 16 * c;  // of this lane's 16 bytes in a block (the same in all its copies)
+  uint32_t xo[kCopiesX];  // their place from xb: 256 rows of at most 2^24 bytes
 #pragma unroll
-  for (int i = 0; i < kCopiesX; ++i) {
-    const int half = i * kWaves + wave;
-    xo[i] = uint32_t(min((half >> 1) * 16 + r, a.t - 1 - tok0)) * uint32_t(a.ldq) + 64 * (half & 1) + 16 * c;
-  }
-  const int xchunk = wave % (kTok / 64);
-  const uint32_t so = uint32_t(min(tok0 + xchunk * 64 + lane, a.t - 1));
+  for (int i = 0; i < kCopiesX; ++i)
+    xo[i] = uint32_t(min((i * 8 + wave) / 2 * 16 + r, a.t - 1 - tok0)) * uint32_t(a.ldq) + col;
+  const int xchunk = wave % RT;
+  const uint32_t so = uint32_t(min(tok0 + xchunk * 64 + lane, a.t - 1)) * 4;
 
-  auto copy = [&](int kb, int buf) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < kCopiesW; ++i)
-      to_lds<16>(wp[i] + int64_t(kb) * kFp8TileBytes, uint32_t(lane) * 16, &lds[buf][(i * kWaves + wave) * 1024]);
+  auto copy_x = [&](int kb, int buf) __attribute__((always_inline)) {
+    // Past the end of a row of codes (k no multiple of 128) the lane copies the row's first
+    // bytes: they meet weight codes of 0, and a NaN among them has its token's row already.
     if (kb * kFp8Block + kFp8Block <= a.xlim) {
 #pragma unroll
       for (int i = 0; i < kCopiesX; ++i)
-        to_lds<16>(xb + int64_t(kb) * kFp8Block, xo[i], &lds[buf][(2 * kRb + i * kWaves + wave) * 1024]);
-    } else {  // the end of a row of codes that is no whole block: zeros after it
+        to_lds<16>(xb + int64_t(kb) * kFp8Block, xo[i], &lds[buf][(2 * kRb + i * 8 + wave) * 1024]);
+    } else {
+      const uint32_t at = kb * kFp8Block + col < a.xlim ? uint32_t(kb) * kFp8Block : 0u - uint32_t(col);
 #pragma unroll
-      for (int i = 0; i < kCopiesX; ++i) {
-        const int half = i * kWaves + wave;
-        const bool in_row = kb * kFp8Block + 64 * (half & 1) + 16 * c < a.xlim;
-        to_lds_from(in_row ? xb + int64_t(kb) * kFp8Block + xo[i] : a.zeros, &lds[buf][(2 * kRb + half) * 1024]);
-      }
+      for (int i = 0; i < kCopiesX; ++i) to_lds<16>(xb, xo[i] + at, &lds[buf][(2 * kRb + i * 8 + wave) * 1024]);
     }
-    to_lds<4>(a.xs + int64_t(kb) * a.t, so * 4, &lds[buf][(kRb + kTb) * kFp8TileBytes + xchunk * 256]);
+    to_lds<4>(a.xs + int64_t(kb) * a.t, so, &lxs[buf][xchunk * 64]);
   };
+  auto copy_w = [&](int kb, int buf) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < kCopiesW; ++i)
+      to_lds<16>(wp[i] + int64_t(kb) * kFp8TileBytes, uint32_t(lane) * 16, &lds[buf][(i * 8 + wave) * 1024]);
+  };
+
+  float ws[P];  // the block's weight scales, loaded a block ahead
+#pragma unroll
+  for (int i = 0; i < P; ++i) ws[i] = scale_at(i, kb0);
 
   f32x4_t acc[RN][RT];
 #pragma unroll
@@ -135,51 +148,80 @@ __global__ __launch_bounds__(64 * WN * WT, 2) void gemm_kernel(LinArgs a) {
 #pragma unroll
     for (int j = 0; j < RT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 
-  copy(0, 0);
-  for (int kb = 0; kb < a.kb; ++kb) {
-    const uint8_t* buf = lds[kb & 1];
-    to_lds_wait();
-    __syncthreads();  // block kb is in, and every wave has left the other buffer
-    if (kb + 1 < a.kb) copy(kb + 1, (kb & 1) ^ 1);
+#pragma unroll
+  for (int i = 0; i < NS - 1; ++i)
+    if (kb0 + i < kb1) {
+      copy_x(kb0 + i, i);
+      copy_w(kb0 + i, i);
+    }
+  int buf = 0;
+  for (int kb = kb0; kb < kb1; ++kb) {
+    const int next = kb + NS - 1, free = buf == 0 ? NS - 1 : buf - 1;
+    // block kb is in (the copies of the blocks after it may be on their way), and every wave
+    // has left the buffer of block kb - 1
+    if (next <= kb1) to_lds_wait<(NS - 2) * kCopies>();
+    else to_lds_wait<0>();
+    __syncthreads();
+    // a block's copies in two parts: all at once hold up the reads of this block
+    if (next < kb1) copy_x(next, free);
+    float ws_now[P];
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      ws_now[i] = ws[i];
+      ws[i] = scale_at(i, min(kb + 1, kb1 - 1));
+    }
     auto frag = [&](int tile) __attribute__((always_inline)) {
-      const u32x4_t* p = reinterpret_cast<const u32x4_t*>(buf + tile * kFp8TileBytes) + lane;
+      const u32x4_t* p = reinterpret_cast<const u32x4_t*>(&lds[buf][tile * kFp8TileBytes]) + lane;
       return join(p[0], p[64]);
     };
     i32x8_t x[RT];
-    float xs[RT];
+    float xs[RT], s[RT];
 #pragma unroll
     for (int j = 0; j < RT; ++j) {
-      const int tile = wt * RT + j;
-      x[j] = frag(kRb + tile);
-      xs[j] = reinterpret_cast<const float*>(buf + (kRb + kTb) * kFp8TileBytes)[tile * 16 + r];
+      x[j] = frag(kRb + wt * RT + j);
+      xs[j] = lxs[buf][(wt * RT + j) * 16 + r];
     }
-    constexpr int P = ACT == kPlain ? 1 : 2;
+    // row tiles in the order 0 .. RN - 1; gated: all gate tiles, then all up tiles
+    constexpr auto tile_of = [](int q) { return ACT == kPlain ? q : q < RN / 2 ? 2 * q : 2 * q - RN + 1; };
+    // A product is added four products later, so that no wave waits for its own instruction.
+    constexpr int M = RN * RT, D = M < 4 ? M : 4;
+    f32x4_t d[D];
+    i32x8_t w[2] = {frag(wn * RN + tile_of(0)), {}};
 #pragma unroll
-    for (int part = 0; part < P; ++part) {  // gated: all gate tiles, then all up tiles
-      const float w_scale = (part ? wsu : wsp)[kb];
-      float s[RT];
+    for (int m = 0; m < M + D - 1; ++m) {
+      if (m == M / 2 && next < kb1) copy_w(next, free);
+      if (m < M) {
+        const int q = m / RT;
+        if (m % RT == 0 && q + 1 < RN) w[(q + 1) & 1] = frag(wn * RN + tile_of(q + 1));
+        d[m % D] = block_product<!YBF>(w[q & 1], x[m % RT]);
+      }
+      if (m >= D - 1) {
+        const int f = m - (D - 1), i = tile_of(f / RT), j = f % RT;
+        if (f % (M / P) == 0) {
 #pragma unroll
-      for (int j = 0; j < RT; ++j) s[j] = xs[j] * w_scale;
-#pragma unroll
-      for (int i = part; i < RN; i += P) {
-        const Frag<!YBF> w = frag(wn * RN + i);
-#pragma unroll
-        for (int j = 0; j < RT; ++j) {
-          const f32x4_t d = block_product<!YBF>(w, x[j]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[e], s[j], acc[i][j][e]);
+          for (int e = 0; e < RT; ++e) s[e] = xs[e] * ws_now[f / (M / P)];
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[f % D][e], s[j], acc[i][j][e]);
       }
     }
+    buf = buf == NS - 1 ? 0 : buf + 1;
   }
 
 #pragma unroll
   for (int j = 0; j < RT; ++j) {
     const int token = tok0 + (wt * RT + j) * 16 + r;
     if (token >= a.t) continue;
+    if (a.chunks > 1) {
+      float* row = a.part + (int64_t(chunk) * a.t + token) * a.rbs * 16 + 4 * c;
+#pragma unroll
+      for (int i = 0; i < RN; ++i)
+        if (rbw + i < a.rbs) *reinterpret_cast<f32x4_t*>(row + (rbw + i) * 16) = acc[i][j];
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < RN; i += ACT == kPlain ? 1 : 2) {
-      const int rb = rb0 + wn * RN + i;
+      const int rb = rbw + i;
       float v[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -191,28 +233,60 @@ __global__ __launch_bounds__(64 * WN * WT, 2) void gemm_kernel(LinArgs a) {
   }
 }
 
+// Joins the chunks of a split K in their order: four outputs of one token a thread.
+template <int ACT, bool YBF>
+__global__ __launch_bounds__(256) void join_kernel(LinArgs a) {
+  constexpr int R = ACT == kPlain ? 1 : 2;
+  const int quads = a.rbs / R * 4;
+  const int64_t stride = int64_t(a.t) * a.rbs * 16;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < int64_t(a.t) * quads; i += int64_t(gridDim.x) * 256) {
+    const int token = int(i / quads), q = int(i - int64_t(token) * quads);
+    const float* p = a.part + int64_t(token) * a.rbs * 16 + (q >> 2) * 16 * R + (q & 3) * 4;
+    f32x4_t sum[R];
+#pragma unroll
+    for (int e = 0; e < R; ++e) sum[e] = *reinterpret_cast<const f32x4_t*>(p + 16 * e);
+    for (int s = 1; s < a.chunks; ++s)
+#pragma unroll
+      for (int e = 0; e < R; ++e) {
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(p + s * stride + 16 * e);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum[e][k] += v[k];
+      }
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (ACT == kPlain) v[e] = sum[0][e];
+      else v[e] = gated<ACT>(sum[0][e], sum[R - 1][e]);
+    }
+    store4<YBF>(a.y, token, a.n, q * 4, v);
+  }
+}
+
 // Up to 16 TT tokens: every workgroup streams one row block (gated: the pair), its eight
 // waves take every eighth 128-input block, and their sums meet in LDS in a fixed order.
+// XT: the type of x.  Codes (MBQ_E4M3) are read from memory, with every block of the weight;
+// a few float tokens are quantized here, once a workgroup into LDS, while the first weight
+// tiles are on their way, which saves the quantizing launch.
 constexpr int kStreamWaves = 8;
+constexpr int kInlineBlocks = 160;  // quantized in the kernel: at most 5 blocks for each 16 lanes
 
-template <int TT, int ACT, bool YBF>
+template <int TT, int XT, int ACT, bool YBF>
 __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(LinArgs a) {
   constexpr int R = ACT == kPlain ? 1 : 2, U = TT == 1 ? 4 : 2;
+  constexpr bool kInline = XT != MBQ_E4M3;
+  static_assert(!kInline || TT == 1, "a few tokens");
   __shared__ f32x4_t red[kStreamWaves][R * TT][64];
+  __shared__ __align__(16) uint8_t lx[kInline ? kInlineBlocks * kFp8Block + 16 * 16 : 16];  // rows 16 bytes apart in banks
+  __shared__ float ls[kInline ? kInlineBlocks : 1];                                         // [kb][t]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, c = lane >> 4;
   const int rb0 = blockIdx.x * R;
-  const float* wsp = a.ws + int64_t(rb0 / (8 * R)) * a.kb;
-  const float* wsu = wsp + int64_t(a.nblk) * a.kb;
+  const ConstFloat* wsp = (const ConstFloat*)a.ws + int64_t(rb0 / (8 * R)) * a.kb;
+  const ConstFloat* wsu = wsp + int64_t(a.nblk) * a.kb;
   const uint8_t* wp = a.codes + int64_t(rb0) * a.kb * kFp8TileBytes + lane * 16;
-  f32x4_t acc[R][TT];
-#pragma unroll
-  for (int i = 0; i < R; ++i)
-#pragma unroll
-    for (int j = 0; j < TT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int k0 = wave; k0 < a.kb; k0 += kStreamWaves * U) {
-    u32x4_t wf[U][R][2], xf[U][TT][2];
-    float xs[U][TT];
+  const int row = a.kb * kFp8Block + 16;
+  u32x4_t wf[U][R][2];
+  auto load_w = [&](int k0) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int kb = min(k0 + u * kStreamWaves, a.kb - 1);
@@ -223,16 +297,46 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(LinArgs a) {
         wf[u][i][1] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p + 1024));
       }
     }
+  };
+  load_w(wave);
+  if constexpr (kInline) {
+    const int g = threadIdx.x & 15;
+    for (int b = threadIdx.x >> 4; b < a.t * a.kb; b += 4 * kStreamWaves) {  // block b / t of token b % t
+      const int blk = b / a.t, tok = b - blk * a.t, i = blk * kFp8Block + g * 8;
+      float v[8];
+      load8<XT == MBQ_BF16>(static_cast<const uint8_t*>(a.x) + tok * a.ldx * (XT == MBQ_BF16 ? 2 : 4), i, a.k, v);
+      const uint32_t m = max16(amax8(v));
+      store_codes8(lx + tok * row, i, row, v, fp8_factor(m));
+      if (g == 0) ls[b] = fp8_scale(m);
+    }
+    __syncthreads();
+  }
+  f32x4_t acc[R][TT];
+#pragma unroll
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int j = 0; j < TT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  for (int k0 = wave; k0 < a.kb; k0 += kStreamWaves * U) {
+    if (k0 != wave) load_w(k0);
+    u32x4_t xf[U][TT][2];
+    float xs[U][TT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int kb = min(k0 + u * kStreamWaves, a.kb - 1);
 #pragma unroll
       for (int j = 0; j < TT; ++j) {
         const int tok = min(j * 16 + r, a.t - 1), col = kb * kFp8Block + 16 * c;
-        const uint8_t* p = a.xq + tok * a.ldq + col;
-        xf[u][j][0] = *reinterpret_cast<const u32x4_t*>(col < a.xlim ? p : a.zeros);
-        xf[u][j][1] = *reinterpret_cast<const u32x4_t*>(col + 64 < a.xlim ? p + 64 : a.zeros);
-        xs[u][j] = a.xs[int64_t(kb) * a.t + tok];
+        if constexpr (kInline) {
+          const uint8_t* p = lx + tok * row + col;
+          xf[u][j][0] = *reinterpret_cast<const u32x4_t*>(p);
+          xf[u][j][1] = *reinterpret_cast<const u32x4_t*>(p + 64);
+          xs[u][j] = ls[kb * a.t + tok];
+        } else {
+          const uint8_t* p = a.xq + tok * a.ldq;  // past the end of a row: see gemm_kernel
+          xf[u][j][0] = *reinterpret_cast<const u32x4_t*>(p + (col < a.xlim ? col : 0));
+          xf[u][j][1] = *reinterpret_cast<const u32x4_t*>(p + (col + 64 < a.xlim ? col + 64 : 0));
+          xs[u][j] = a.xs[int64_t(kb) * a.t + tok];
+        }
       }
     }
 #pragma unroll
@@ -278,28 +382,102 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(LinArgs a) {
   store4<YBF>(a.y, token, a.n, int32_t(blockIdx.x) * 16 + 4 * c, v);
 }
 
-template <int ACT, bool YBF>
-hipError_t launch(const LinArgs& a, hipStream_t stream) {
-  constexpr int R = ACT == kPlain ? 1 : 2;
-  if (a.t <= 64) {
-    const dim3 grid(a.rbs / R), block(64 * kStreamWaves);
-    if (a.t <= 16) stream_kernel<1, ACT, YBF><<<grid, block, 0, stream>>>(a);
-    else if (a.t <= 32) stream_kernel<2, ACT, YBF><<<grid, block, 0, stream>>>(a);
-    else stream_kernel<4, ACT, YBF><<<grid, block, 0, stream>>>(a);
-  } else {
-    const dim3 grid(uint32_t((a.rbs + 15) / 16) * uint32_t((a.t + 255) / 256));
-    gemm_kernel<8, 4, 2, 4, ACT, YBF><<<grid, 512, 0, stream>>>(a);
+// The tile and the chunks of K for a shape.  A workgroup's time is its blocks times the
+// tile's time a block, and workgroups run in rounds of one on each of the 256 compute units
+// (two on a unit take twice as long).  Times a block measured on one box, alone and with
+// every unit busy: 256 x 256 1.46-1.86 us, 128 x 128 0.64, 64 x 128 0.52, 64 x 64 0.40
+// (the smaller, the more of it is the wait of a block).
+// Splitting K costs a second launch and the partial sums' traffic.  For instance (us, tiles
+// in this order without the second): 1024 x 4096 x 4096 60 / 27 / 38 / 44; 512 x 3584 x 3584
+// 53 / 23 / 19 / 22; 1024 x 1024 x 8192 105 / 44 / 36 / 27.
+struct Tile {
+  int rn, rt;
+  float us;
+};
+constexpr Tile kTiles[] = {{8, 4, 1.8f}, {4, 2, 0.64f}, {2, 2, 0.52f}, {2, 1, 0.40f}};
+struct Plan {
+  int tile, chunks;
+};
+
+Plan plan_gemm(int32_t t, int32_t rbs, int32_t kb, bool exact) {
+  Plan best{3, 1};
+  float best_us = 1e30f;
+  for (int i = exact ? 1 : 0; i < 4; ++i) {  // float32 outputs: the smaller tiles only (registers)
+    const int64_t tiles = int64_t((rbs + 2 * kTiles[i].rn - 1) / (2 * kTiles[i].rn)) * ((t + 64 * kTiles[i].rt - 1) / (64 * kTiles[i].rt));
+    for (int s = 1; s <= 16 && s <= kb; s *= 2) {
+      if (s > 1 && tiles * s > 512) break;
+      const int per = (kb + s - 1) / s;
+      const float join = s == 1 ? 0.f : 4.f + float(s) * t * rbs * 64.f * 2.f / 4e6f;
+      const float us = float((tiles * s + 255) / 256) * per * kTiles[i].us + join;
+      if (us < best_us) {
+        best_us = us;
+        best = {i, (kb + per - 1) / per};
+      }
+    }
   }
+  return best;
+}
+
+template <int RN, int RT, int NS, int ACT, bool YBF>
+void launch_gemm(const LinArgs& a, hipStream_t stream) {
+  const int64_t tiles = int64_t((a.rbs + 2 * RN - 1) / (2 * RN)) * ((a.t + 64 * RT - 1) / (64 * RT));
+  gemm_kernel<RN, RT, NS, ACT, YBF><<<uint32_t(tiles * a.chunks), 512, 0, stream>>>(a);
+}
+
+constexpr int kStreamTokens = 64;
+
+template <int ACT, bool YBF>
+hipError_t launch(LinArgs& a, mbq_dtype x_dtype, hipStream_t stream) {
+  constexpr int R = ACT == kPlain ? 1 : 2;
+  if (a.t <= kStreamTokens) {
+    const dim3 grid(a.rbs / R), block(64 * kStreamWaves);
+    if (a.x && x_dtype == MBQ_BF16) stream_kernel<1, MBQ_BF16, ACT, YBF><<<grid, block, 0, stream>>>(a);
+    else if (a.x) stream_kernel<1, MBQ_F32, ACT, YBF><<<grid, block, 0, stream>>>(a);
+    else if (a.t <= 16) stream_kernel<1, MBQ_E4M3, ACT, YBF><<<grid, block, 0, stream>>>(a);
+    else if (a.t <= 32) stream_kernel<2, MBQ_E4M3, ACT, YBF><<<grid, block, 0, stream>>>(a);
+    else stream_kernel<4, MBQ_E4M3, ACT, YBF><<<grid, block, 0, stream>>>(a);
+    return hipGetLastError();
+  }
+  const Plan p = plan_gemm(a.t, a.rbs, a.kb, !YBF);
+  a.chunks = p.chunks;
+  a.chunk_kb = (a.kb + p.chunks - 1) / p.chunks;
+  switch (p.tile) {
+    case 0:
+      if constexpr (YBF) launch_gemm<8, 4, 2, ACT, YBF>(a, stream);
+      break;
+    case 1: launch_gemm<4, 2, 3, ACT, YBF>(a, stream); break;
+    case 2: launch_gemm<2, 2, 3, ACT, YBF>(a, stream); break;
+    default: launch_gemm<2, 1, 3, ACT, YBF>(a, stream); break;
+  }
+  if (a.chunks > 1)
+    join_kernel<ACT, YBF><<<uint32_t(std::min<int64_t>((int64_t(a.t) * (a.rbs / R) * 4 + 255) / 256, 4096)), 256, 0, stream>>>(a);
   return hipGetLastError();
 }
 
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 size_t codes_bytes(const mbq_fp8_desc& d, int32_t t) { return size_t(t) * d.k_blocks * kFp8Block; }
 
 }  // namespace
 
+// Float activations quantized inside the streaming kernel: its workgroups each do all of it,
+// so a few blocks only.  One token of 5120 x 5120 (40 blocks): 8.1 us in one launch against
+// 2.5 + 6.8 us and the gap between two.
+bool quantize_inline(const mbq_fp8_desc& d, int32_t t, mbq_dtype x_dtype) {
+  return x_dtype != MBQ_E4M3 && t <= 16 && int64_t(t) * d.k_blocks <= kInlineBlocks;
+}
+
+// Workspace: the activations' codes and scales, then the partial sums of a split K.
 size_t fp8_linear_workspace(const mbq_fp8_desc& d, int32_t t, mbq_dtype x_dtype) {
-  if (x_dtype == MBQ_E4M3 || t == 0) return 0;
-  return codes_bytes(d, t) + (size_t(d.k_blocks) * t * 4 + 255) / 256 * 256;
+  size_t bytes = 0;
+  if (quantize_inline(d, t, x_dtype)) return 0;
+  if (x_dtype != MBQ_E4M3) bytes = codes_bytes(d, t) + align256(size_t(d.k_blocks) * t * 4);
+  size_t part = 0;
+  if (t > kStreamTokens)
+    for (bool exact : {false, true}) {  // y's type is not known here
+      const int chunks = plan_gemm(t, d.row_blocks, d.k_blocks, exact).chunks;
+      if (chunks > 1) part = std::max(part, size_t(chunks) * t * d.row_blocks * 64);
+    }
+  return bytes + part;
 }
 
 hipError_t launch_fp8_linear(const mbq_fp8_desc& d, const void* packed, int32_t t, const void* x, mbq_dtype x_dtype,
@@ -310,31 +488,36 @@ hipError_t launch_fp8_linear(const mbq_fp8_desc& d, const void* packed, int32_t 
   LinArgs a{};
   a.codes = base;
   a.ws = reinterpret_cast<const float*>(base + d.scales_offset);
-  a.zeros = base + d.zeros_offset;
   a.y = y;
   a.t = t;
   a.n = d.n;
+  a.k = d.k;
   a.kb = d.k_blocks;
   a.rbs = d.row_blocks;
   a.nblk = (d.n + 127) / 128;
   if (x_dtype == MBQ_E4M3) {
+    a.part = static_cast<float*>(ws);
     a.xq = static_cast<const uint8_t*>(x);
     a.ldq = ldx;
     a.xs = x_scale;
     a.xlim = d.k;
+  } else if (quantize_inline(d, t, x_dtype)) {
+    a.x = x;
+    a.ldx = ldx;
   } else {
     uint8_t* q = static_cast<uint8_t*>(ws);
     float* s = reinterpret_cast<float*>(q + codes_bytes(d, t));
+    a.part = reinterpret_cast<float*>(q + codes_bytes(d, t) + align256(size_t(d.k_blocks) * t * 4));
     a.ldq = a.xlim = d.k_blocks * kFp8Block;
     const hipError_t e = launch_fp8_quantize(t, d.k, x, x_dtype == MBQ_BF16, ldx, q, a.ldq, true, s, stream);
     if (e != hipSuccess) return e;
     a.xq = q;
     a.xs = s;
   }
-  if (act == kPlain) return y_bf16 ? launch<kPlain, true>(a, stream) : launch<kPlain, false>(a, stream);
+  if (act == kPlain) return y_bf16 ? launch<kPlain, true>(a, x_dtype, stream) : launch<kPlain, false>(a, x_dtype, stream);
   if (act == MBQ_ACT_SILU)
-    return y_bf16 ? launch<MBQ_ACT_SILU, true>(a, stream) : launch<MBQ_ACT_SILU, false>(a, stream);
-  return y_bf16 ? launch<MBQ_ACT_GELU_TANH, true>(a, stream) : launch<MBQ_ACT_GELU_TANH, false>(a, stream);
+    return y_bf16 ? launch<MBQ_ACT_SILU, true>(a, x_dtype, stream) : launch<MBQ_ACT_SILU, false>(a, x_dtype, stream);
+  return y_bf16 ? launch<MBQ_ACT_GELU_TANH, true>(a, x_dtype, stream) : launch<MBQ_ACT_GELU_TANH, false>(a, x_dtype, stream);
 }
 
 }  // namespace mbq

@@ -94,7 +94,6 @@ __global__ __launch_bounds__(256) void pack_fp8_kernel(mbq_fp8_desc d, int32_t p
   const int nblk = (d.n + 127) / 128;
   if (tid == 0)
     reinterpret_cast<float*>(packed + d.scales_offset)[(int64_t(part) * nblk + nb) * d.k_blocks + kb] = s;
-  if (kb == 0 && nb == 0 && tid < 64) reinterpret_cast<uint32_t*>(packed + d.zeros_offset)[tid] = 0;
   if (bad && status) atomicOr(status, 1);
 }
 
