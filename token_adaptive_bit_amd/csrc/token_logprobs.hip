@@ -1,15 +1,13 @@
 // Log probabilities of given tokens, entropy, rank and the top alternatives, in one pass
-// over the logits.  With c = inv_temperature log2 e and a running maximum m,
-//   s = sum 2^(c (x - m)),  q = sum 2^(c (x - m)) c (x - m)
-// give lse = m / T + ln s and the entropy ln s - ln 2 q / s; both are kept per lane in
-// float32 and rescaled when m grows.  The rank counts lanes' comparisons on the scalar
-// unit.  The top list is a sorted list of 64-bit keys (value, then lower index first), one
-// entry a lane; a vector of logits is looked at only if it reaches the list's last entry,
-// which after a short start happens about top / i times in vector i.
-// A row is split over several workgroups when there are few rows, and a second launch joins
-// the parts.
-#include <cfloat>
-
+// over the logits.  With c = inv_temperature log2 e, a running reference r and d = c (x - r),
+//   s = sum 2^d,  q = sum 2^d d
+// give the log probability ln 2 d - ln s of x and the entropy ln s - ln 2 q / s; both sums
+// are kept per lane in float32 and rescaled when the values outgrow r.  The rank counts
+// lanes' comparisons on the scalar unit.  The top list is a sorted list of 64-bit keys
+// (value, then lower index first), one entry a lane; a vector of logits is looked at only if
+// it reaches the list's last entry.
+// A row is split over several waves when there are few rows; beyond one workgroup's waves a
+// second launch joins the parts.
 #include "fp8.h"
 
 namespace mbq {
@@ -23,10 +21,10 @@ struct LpArgs {
   float *logprob, *entropy;
   int32_t *rank, *top_ids;
   float* top_logprobs;
-  float4* part;    // [t][chunks] m, s, q, rank count
-  uint64_t* keys;  // [t][chunks][top]
+  struct Part* part;  // [t][parts]
+  uint64_t* keys;     // [t][parts][top]
   int64_t ld;
-  int32_t t, v, top, chunks, per;  // per: logits a chunk, a multiple of 8
+  int32_t t, v, top, parts, per;  // parts a row, one wave each; per: logits a part, a multiple of 8
   float inv_temperature;
   bool wide;
 };
@@ -48,8 +46,13 @@ __device__ __forceinline__ uint64_t lane_key(uint64_t k, int lane) {
 struct TopList {
   uint64_t mine = 0;  // this lane's entry
   uint64_t last = 0;  // entry top - 1
-  float floor = -__builtin_inff();  // its value
+  float floor = -__builtin_inff();  // no value below it can enter
+  float gate = -__builtin_inff();   // nor, from a vector of higher indexes, one below this
 
+  // A full list takes no equal value of a higher index: from the next vector on.
+  __device__ __forceinline__ void close_vector() {
+    gate = last ? from_ordered(uint32_t(last >> 32) + 1) : floor;
+  }
   __device__ __forceinline__ void insert(uint64_t k, int lane, int top) {
     const int pos = __popcll(__ballot(mine > k));
     const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(mine)), 0x138, 0xF, 0xF, true);  // wave_shr 1
@@ -57,7 +60,7 @@ struct TopList {
     if (lane == pos) mine = k;
     else if (lane > pos) mine = uint64_t(hi) << 32 | lo;
     last = lane_key(mine, top - 1);
-    floor = last ? from_ordered(uint32_t(last >> 32)) : -__builtin_inff();
+    if (last) floor = from_ordered(uint32_t(last >> 32));
   }
   // Offers one key a lane (0: none).
   __device__ __forceinline__ void offer(uint64_t k, int lane, int top) {
@@ -68,26 +71,91 @@ struct TopList {
       m &= __ballot(k > last);
     }
   }
+  // Fills an empty list with one key a lane: a bitonic sort of the wave.
+  __device__ __forceinline__ void fill(uint64_t k, int lane, int top) {
+#pragma unroll
+    for (int size = 2; size <= 64; size *= 2)
+#pragma unroll
+      for (int step = size / 2; step; step /= 2) {
+        const uint64_t o = uint64_t(__shfl_xor((long long)k, step));
+        const bool larger = ((lane & step) == 0) == ((lane & size) == 0 || size == 64);  // lane keeps the larger key
+        if ((o > k) == larger) k = o;
+      }
+    mine = k;
+    last = lane_key(mine, top - 1);
+    if (last) floor = from_ordered(uint32_t(last >> 32));
+  }
+  // Raises the floor of a list without real values yet to one that at least `top` lanes' x reach: found
+  // bit by bit over the upper half of the ordered value, so that the list fills with about
+  // `top` insertions and not with top (1 + ln(n / top)).  (NaN sorts above all; its row has
+  // no list.)
+  __device__ __forceinline__ void start(float x, int top) {
+    const uint32_t o = ordered(x);
+    uint32_t t = 0;
+#pragma unroll
+    for (int b = 31; b >= 16; --b)
+      if (__popcll(__ballot(o >= (t | 1u << b))) >= top) t |= 1u << b;
+    floor = fmaxf(floor, from_ordered(t));  // t == 0 maps to a NaN, which fmaxf drops
+    gate = fmaxf(gate, floor);
+  }
 };
 
-// Joins (m, s, q) of two sets; an empty set has s = q = 0 and any finite m.
-__device__ __forceinline__ void join_sums(float c, float& m, float& s, float& q, float m2, float s2, float q2) {
-  const float mn = fmaxf(m, m2);
-  // -1e4: far below the range of 2^x, and finite, so that an empty set's 0 stays 0
-  const float d1 = fmaxf((m - mn) * c, -1e4f), d2 = fmaxf((m2 - mn) * c, -1e4f);
-  const float f1 = __builtin_amdgcn_exp2f(d1), f2 = __builtin_amdgcn_exp2f(d2);
-  q = f1 * fmaf(d1, s, q) + f2 * fmaf(d2, s2, q2);
-  s = f1 * s + f2 * s2;
-  m = mn;
-}
+constexpr float kLn2 = 0.69314718f;
 
-__device__ __forceinline__ void wave_join(float c, float& m, float& s, float& q) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) {
-    const float m2 = __shfl_xor(m, o), s2 = __shfl_xor(s, o), q2 = __shfl_xor(q, o);
-    join_sums(c, m, s, q, m2, s2, q2);
+// The sums of a set of logits.  The reference of the exponents is one of two: a whole
+// number M in units of ln 2 (m = 0), so that c x - M is a single FMA and rounds once; or,
+// for values that c x would overflow or blur, a logit m (M = 0).
+struct Sums {
+  float m, M, s, q;
+  static constexpr float kNone = -3e38f;  // M while nothing above -infinity has been seen
+
+  __device__ __forceinline__ float exponent(float x, float c) const { return fmaf(x - m, c, -M); }
+  // ln of 2^exponent, without its overflow far from the reference.
+  __device__ __forceinline__ float natural(float x, float c, float inv_t) const {
+    const float d = exponent(x, c);
+    return fabsf(d) < 1e6f ? d * kLn2 : fmaf(x - m, inv_t, -M * kLn2);
   }
-}
+  // Moves the reference up; terms further than 2^-10000 below it are 0 (finite, and at most
+  // 0 from the empty set's reference too, so that an empty sum stays 0).
+  __device__ __forceinline__ void move(float m2, float M2, float c) {
+    const float d = fminf(fmaxf(fmaf(m - m2, c, M - M2), -1e4f), 0.f), f = __builtin_amdgcn_exp2f(d);
+    q = f * fmaf(d, s, q);
+    s *= f;
+    m = m2;
+    M = M2;
+  }
+  __device__ __forceinline__ void refer(float x, float c) {
+    const bool plain = fabsf(x * c) < 1e6f;
+    move(plain ? 0.f : x, plain ? rintf(x * c) : 0.f, c);
+  }
+  __device__ __forceinline__ void join(Sums o, float c) {
+    if (o.s == 0.f) return;
+    if (s == 0.f || m + M / c < o.m + o.M / c) {
+      const Sums t = *this;
+      *this = o;
+      o = t;
+    }
+    o.move(m, M, c);
+    s += o.s;
+    q += o.q;
+  }
+  __device__ __forceinline__ void join_wave(float c) {
+#pragma unroll
+    for (int o = 32; o; o >>= 1) {
+      Sums t;
+      t.m = __shfl_xor(m, o);
+      t.M = __shfl_xor(M, o);
+      t.s = __shfl_xor(s, o);
+      t.q = __shfl_xor(q, o);
+      join(t, c);
+    }
+  }
+};
+
+struct Part {
+  Sums sums;
+  int count, unused[3];
+};
 
 __device__ __forceinline__ int64_t target_of(const LpArgs& a, int row) {
   return a.wide ? static_cast<const int64_t*>(a.targets)[row] : static_cast<const int32_t*>(a.targets)[row];
@@ -100,149 +168,223 @@ __device__ __forceinline__ float logit(const LpArgs& a, int row, int64_t i) {
 
 // Writes a row's results from its sums and its top list (one wave).
 template <bool BF16>
-__device__ __forceinline__ void finish(const LpArgs& a, int row, float m, float s, float q, int count,
-                                       const TopList& list, int lane) {
+__device__ __forceinline__ void finish(const LpArgs& a, int row, const Sums& sums, int count, const TopList& list,
+                                       float c, int lane) {
+  const float s = sums.s;
   const int64_t target = target_of(a, row);
   const bool valid = target >= 0 && target < a.v;
   const bool none = s == 0.f, bad = s != s;  // nothing but -infinity; a NaN or +infinity
   const float log_s = logf(s), inf = __builtin_inff();
   if (lane == 0) {
     const float xt = valid ? logit<BF16>(a, row, target) : 0.f;
-    a.logprob[row] = !valid ? 0.f : none ? -inf : (xt - m) * a.inv_temperature - log_s;
-    a.entropy[row] = none ? 0.f : log_s - 0.69314718f * (q / s);
+    a.logprob[row] = !valid ? 0.f : none ? -inf : sums.natural(xt, c, a.inv_temperature) - log_s;
+    a.entropy[row] = none ? 0.f : log_s - kLn2 * (sums.q / s);
     a.rank[row] = valid && !bad ? count + 1 : 0;
   }
   if (lane < a.top) {
     const float x = from_ordered(uint32_t(list.mine >> 32));
     a.top_ids[int64_t(row) * a.top + lane] = bad ? -1 : int32_t(~uint32_t(list.mine));
-    a.top_logprobs[int64_t(row) * a.top + lane] = none ? -inf : bad ? s : (x - m) * a.inv_temperature - log_s;
+    a.top_logprobs[int64_t(row) * a.top + lane] = none ? -inf : bad ? s : sums.natural(x, c, a.inv_temperature) - log_s;
   }
 }
 
-template <bool BF16, bool TOP>
-__global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
-  __shared__ float4 sums[kWaves];
-  __shared__ uint64_t lists[TOP ? kWaves : 1][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int row = blockIdx.x / a.chunks, chunk = blockIdx.x % a.chunks;
-  const uint8_t* base = static_cast<const uint8_t*>(a.logits) + int64_t(row) * a.ld * (BF16 ? 2 : 4);
-  const int begin = chunk * a.per, end = min(begin + a.per, a.v);
-  const float c = a.inv_temperature * 1.4426950408889634f;
-  const int64_t tg = target_of(a, row);
-  const int target = tg >= 0 && tg < a.v ? int(tg) : -1;
-  const float xt = target >= 0 ? logit<BF16>(a, row, target) : __builtin_inff();
-  // x > xt as x >= the next value above it
-  const float above = target >= 0 ? from_ordered(ordered(xt) + 1) : __builtin_inff();
-
-  float m = -FLT_MAX, s = 0.f, q = 0.f;
-  int count = 0, tied = 0;
-  TopList list;
-  constexpr int U = 4;
-  for (int i0 = begin; i0 < end; i0 += kThreads * 8 * U) {
-    float v[U][8];
+// Eight logits as they lie in memory.
+template <bool BF16>
+struct Raw {
+  u32x4_t w[BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const uint8_t* row, int i, int end) {  // from i; -infinity from end on
+    if (i + 8 <= end) {
+      const uint8_t* p = row + int64_t(i) * (BF16 ? 2 : 4);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + (u * kThreads + int(threadIdx.x)) * 8;
-      if (i + 8 <= end) {
-        load8<BF16>(base, i, end, v[u]);
-      } else {
+      for (int h = 0; h < (BF16 ? 1 : 2); ++h) w[h] = *reinterpret_cast<const u32x4_a2*>(p + 16 * h);
+    } else {
+      float x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          v[u][e] = i + e < end ? load_x(base, size_t(i + e), BF16) : -__builtin_inff();
-      }
-    }
+      for (int e = 0; e < 8; ++e) x[e] = i + e < end ? load_x(row, size_t(i + e), BF16) : -__builtin_inff();
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + (u * kThreads + int(threadIdx.x)) * 8;
-      const float (&x)[8] = v[u];
-      const float best = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-      const float mn = fmaxf(m, best);
-      const float shift = fmaxf((m - mn) * c, -1e4f), f = __builtin_amdgcn_exp2f(shift);
-      q = f * fmaf(shift, s, q);
-      s *= f;
-      m = mn;
-      // a chunk ends on a vector; what is read past it counts for nothing
-      const float bound = i >= end ? __builtin_inff() : i + 8 <= target ? xt : above;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = (x[e] - mn) * c, p = __builtin_amdgcn_exp2f(d);
-        s += p;
-        q = fmaf(p, fmaxf(d, -1e4f), q);  // finite, so that p = 0 adds 0
-        count += __popcll(__ballot(x[e] >= bound));
-      }
-      if (target >= i && target < i + 8) {  // the vector that holds the target: equal logits before it
-#pragma unroll
-        for (int e = 0; e < 8; ++e) tied += i + e < target && x[e] == xt;
-      }
-      if constexpr (TOP) {
-        if (__ballot(best >= list.floor && i < end)) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) list.offer(i + e < end && x[e] == x[e] ? key_of(x[e], uint32_t(i + e)) : 0, lane, a.top);
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (BF16) {
+          w[0][e] = __float_as_uint(x[2 * e]) >> 16 | (__float_as_uint(x[2 * e + 1]) & 0xFFFF0000u);
+        } else {
+          w[0][e] = __float_as_uint(x[e]);
+          w[BF16 ? 0 : 1][e] = __float_as_uint(x[4 + e]);
         }
       }
     }
   }
-  wave_join(c, m, s, q);
+  __device__ __forceinline__ void get(float (&x)[8]) const {
 #pragma unroll
-  for (int o = 32; o; o >>= 1) tied += __shfl_xor(tied, o);
-  count += tied;
-  if (lane == 0) sums[wave] = make_float4(m, s, q, __int_as_float(count));
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (BF16) {
+        x[2 * e] = __uint_as_float(w[0][e] << 16);
+        x[2 * e + 1] = __uint_as_float(w[0][e] & 0xFFFF0000u);
+      } else {
+        x[e] = __uint_as_float(w[0][e]);
+        x[4 + e] = __uint_as_float(w[BF16 ? 0 : 1][e]);
+      }
+    }
+  }
+};
+
+// One part of a row a wave.  The waves of a row meet in LDS when they fit one workgroup
+// (1, 2 or 4 parts), else their results go to memory for the merging launch.
+template <bool BF16, bool TOP>
+__global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
+  __shared__ Part parts[kWaves];
+  __shared__ uint64_t lists[TOP ? kWaves : 1][64];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t id = int64_t(blockIdx.x) * kWaves + wave;
+  const int row = __builtin_amdgcn_readfirstlane(int(min(id / a.parts, int64_t(a.t - 1)))), part = int(id - int64_t(row) * a.parts);
+  const uint8_t* base = static_cast<const uint8_t*>(a.logits) + int64_t(row) * a.ld * (BF16 ? 2 : 4);
+  const float c = a.inv_temperature * 1.4426950408889634f;
+  Sums sums = {0.f, Sums::kNone, 0.f, 0.f};
+  int count = 0;
+  TopList list;
+  if (part < a.parts) {  // else the last workgroup's spare waves, with nothing to add
+    const int begin = min(part * a.per, a.v), end = min(begin + a.per, a.v);
+    const int64_t tg = target_of(a, row);
+    const int target = tg >= 0 && tg < a.v ? int(tg) : -1;
+    const float xt = target >= 0 ? logit<BF16>(a, row, target) : __builtin_inff();
+    // x > xt as x >= the next value above it
+    const float above = target >= 0 ? from_ordered(ordered(xt) + 1) : __builtin_inff();
+    int tied = 0;
+    constexpr int U = 4, kStep = 64 * 8 * U;
+    Raw<BF16> next[U];
+    auto load = [&](int i0) __attribute__((always_inline)) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) next[u].load(base, i0 + (u * 64 + lane) * 8, end);
+    };
+    load(begin);
+    for (int i0 = begin; i0 < end; i0 += kStep) {
+      Raw<BF16> raw[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) raw[u] = next[u];
+      if (i0 + kStep < end) load(i0 + kStep);
+      float best[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        float x[8];
+        raw[u].get(x);
+        best[u] = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
+      }
+      if constexpr (TOP) {
+        if (list.floor == -__builtin_inff()) list.start(fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])), a.top);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int i = i0 + (u * 64 + lane) * 8;
+        float x[8];
+        raw[u].get(x);
+        // The reference follows the largest value with a lead of up to 2^16 in the terms, so
+        // that the sums are rescaled rarely.
+        const bool far = best[u] > -__builtin_inff() && (sums.M == Sums::kNone || sums.exponent(best[u], c) > 16.f);
+        if (__ballot(far)) {
+          if (far) sums.refer(best[u], c);
+        }
+        if (__ballot(sums.m != 0.f)) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float d = sums.exponent(x[e], c), p = __builtin_amdgcn_exp2f(d);
+            sums.s += p;
+            sums.q = fmaf(p, fmaxf(d, -1e4f), sums.q);  // finite, so that p = 0 adds 0
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float d = fmaf(x[e], c, -sums.M), p = __builtin_amdgcn_exp2f(d);
+            sums.s += p;
+            sums.q = fmaf(p, fmaxf(d, -1e4f), sums.q);
+          }
+        }
+        // a part ends on a vector; what is read past it counts for nothing
+        const float bound = i >= end ? __builtin_inff() : i + 8 <= target ? xt : above;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) count += __popcll(__ballot(x[e] >= bound));
+        if (target >= i && target < i + 8) {  // the vector that holds the target: equal logits before it
+#pragma unroll
+          for (int e = 0; e < 8; ++e) tied += i + e < target && x[e] == xt;
+        }
+        if constexpr (TOP) {
+          if (__ballot(best[u] >= list.gate && i < end)) {
+            int at = i;
+            asm("" : "+v"(at));  // the indexes are computed here and not in every step
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (__ballot(x[e] >= list.floor && at + e < end))
+                list.offer(at + e < end && x[e] >= list.floor ? key_of(x[e], uint32_t(at + e)) : 0, lane, a.top);
+            list.close_vector();
+          }
+        }
+      }
+    }
+    sums.join_wave(c);
+#pragma unroll
+    for (int o = 32; o; o >>= 1) tied += __shfl_xor(tied, o);
+    count += tied;
+    if (a.parts > kWaves) {
+      const int64_t at = int64_t(row) * a.parts + part;
+      if (lane == 0) a.part[at] = {sums, count, {}};
+      if (TOP && lane < a.top) a.keys[at * a.top + lane] = list.mine;
+    } else if (a.parts == 1) {
+      finish<BF16>(a, row, sums, count, list, c, lane);
+    }
+  }
+  if (a.parts == 1 || a.parts > kWaves) return;
+  if (lane == 0) parts[wave] = {sums, count, {}};
   if constexpr (TOP) lists[wave][lane] = list.mine;
   __syncthreads();
-  if (wave) return;
-#pragma unroll
-  for (int w = 1; w < kWaves; ++w) {
-    join_sums(c, m, s, q, sums[w].x, sums[w].y, sums[w].z);
-    count += __float_as_int(sums[w].w);
-    if constexpr (TOP) list.offer(lane < a.top ? lists[w][lane] : 0, lane, a.top);
+  if (part) return;
+  for (int w = 1; w < a.parts; ++w) {
+    sums.join(parts[wave + w].sums, c);
+    count += parts[wave + w].count;
+    if constexpr (TOP) list.offer(lane < a.top ? lists[wave + w][lane] : 0, lane, a.top);
   }
-  if (a.chunks == 1) {
-    finish<BF16>(a, row, m, s, q, count, list, lane);
-  } else {
-    const int64_t at = int64_t(row) * a.chunks + chunk;
-    if (lane == 0) a.part[at] = make_float4(m, s, q, __int_as_float(count));
-    if (TOP && lane < a.top) a.keys[at * a.top + lane] = list.mine;
-  }
+  finish<BF16>(a, row, sums, count, list, c, lane);
 }
 
+constexpr int kMaxParts = 64;
+
+// Joins the parts of a row (more than four), one lane each.
 template <bool BF16>
-__global__ __launch_bounds__(64) void merge_kernel(LpArgs a) {
-  const int row = blockIdx.x, lane = threadIdx.x;
+__global__ __launch_bounds__(kThreads) void merge_kernel(LpArgs a) {
+  __shared__ uint64_t keys[kMaxParts * MBQ_MAX_TOP];
+  const int row = blockIdx.x, lane = threadIdx.x & 63, all = a.parts * a.top;
+  for (int i = threadIdx.x; i < all; i += kThreads) keys[i] = a.keys[int64_t(row) * all + i];
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
   const float c = a.inv_temperature * 1.4426950408889634f;
-  float m = -FLT_MAX, s = 0.f, q = 0.f;
+  Sums sums = {0.f, Sums::kNone, 0.f, 0.f};
   int count = 0;
-  if (lane < a.chunks) {  // chunks <= 64
-    const float4 p = a.part[int64_t(row) * a.chunks + lane];
-    m = p.x;
-    s = p.y;
-    q = p.z;
-    count = __float_as_int(p.w);
+  if (lane < a.parts) {
+    sums = a.part[int64_t(row) * a.parts + lane].sums;
+    count = a.part[int64_t(row) * a.parts + lane].count;
   }
-  wave_join(c, m, s, q);
+  sums.join_wave(c);
 #pragma unroll
   for (int o = 32; o; o >>= 1) count += __shfl_xor(count, o);
   TopList list;
-  const int all = a.chunks * a.top;
-  for (int i = 0; i < all; i += 64)
-    list.offer(i + lane < all ? a.keys[int64_t(row) * all + i + lane] : 0, lane, a.top);
-  finish<BF16>(a, row, m, s, q, count, list, lane);
+  for (int j = 0; j < a.top; ++j) {  // the parts' best, then their second ...: descending, so the first round without an entry is the last
+    const uint64_t k = lane < a.parts ? keys[lane * a.top + j] : 0;
+    if (j == 0) list.fill(k, lane, a.top);
+    else if (__ballot(k > list.last)) list.offer(k, lane, a.top);
+    else break;
+  }
+  finish<BF16>(a, row, sums, count, list, c, lane);
 }
 
-constexpr int kMaxChunks = 64;
-
-// Parts of a row: enough workgroups for four on every compute unit, each with at least one
-// full step of its loop.
-int chunks_of(int32_t t, int32_t v) {
-  const int64_t want = (1024 + int64_t(t) - 1) / std::max(t, 1);
-  const int64_t most = (int64_t(v) + kThreads * 32 - 1) / (kThreads * 32);
-  return int(std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), kMaxChunks)));
+// Parts of a row: at least 4096 waves (four a SIMD), each with at least one full step of its
+// loop.  Fewer, longer parts mean fewer lists to fill: NNN.
+int parts_of(int32_t t, int32_t v) {
+  const int64_t want = (4096 + int64_t(t) - 1) / std::max(t, 1), most = (int64_t(v) + 2047) / 2048;
+  const int p = int(std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), kMaxParts)));
+  return p == 3 ? 4 : p;  // up to four parts share a workgroup, which holds whole rows
 }
 
 }  // namespace
 
 size_t token_logprobs_workspace(int32_t t, int32_t v, int32_t top) {
-  const int c = chunks_of(t, v);
-  return t == 0 || c == 1 ? 0 : size_t(t) * c * (16 + 8 * size_t(top));
+  const int p = parts_of(t, v);
+  return t == 0 || p <= kWaves ? 0 : size_t(t) * p * (sizeof(Part) + 8 * size_t(top));
 }
 
 hipError_t launch_token_logprobs(int32_t t, int32_t v, const void* logits, bool bf16, int64_t ld, const void* targets,
@@ -261,21 +403,21 @@ hipError_t launch_token_logprobs(int32_t t, int32_t v, const void* logits, bool 
   a.t = t;
   a.v = v;
   a.top = top;
-  a.chunks = chunks_of(t, v);
-  a.per = ((v + a.chunks - 1) / a.chunks + 7) / 8 * 8;
-  a.part = static_cast<float4*>(ws);
-  a.keys = reinterpret_cast<uint64_t*>(a.part + int64_t(t) * a.chunks);
+  a.parts = parts_of(t, v);
+  a.per = ((v + a.parts - 1) / a.parts + 7) / 8 * 8;
+  a.part = static_cast<Part*>(ws);
+  a.keys = reinterpret_cast<uint64_t*>(a.part + int64_t(t) * a.parts);
   a.inv_temperature = inv_temperature;
   a.wide = wide;
-  const dim3 grid(uint32_t(t) * uint32_t(a.chunks));
+  const dim3 grid(uint32_t((int64_t(t) * a.parts + kWaves - 1) / kWaves));
   if (bf16) {
     if (top) part_kernel<true, true><<<grid, kThreads, 0, stream>>>(a);
     else part_kernel<true, false><<<grid, kThreads, 0, stream>>>(a);
-    if (a.chunks > 1) merge_kernel<true><<<t, 64, 0, stream>>>(a);
+    if (a.parts > kWaves) merge_kernel<true><<<t, kThreads, 0, stream>>>(a);
   } else {
     if (top) part_kernel<false, true><<<grid, kThreads, 0, stream>>>(a);
     else part_kernel<false, false><<<grid, kThreads, 0, stream>>>(a);
-    if (a.chunks > 1) merge_kernel<false><<<t, 64, 0, stream>>>(a);
+    if (a.parts > kWaves) merge_kernel<false><<<t, kThreads, 0, stream>>>(a);
   }
   return hipGetLastError();
 }
