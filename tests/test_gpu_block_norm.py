@@ -85,8 +85,8 @@ def check(api, t, k, xd=F32, rd=F32, hd=F32, kind="rms", post=True, gate="none",
         assert worst <= 1, f"h: {worst:.2f} of the tolerance"
 
 
-WIDTHS = [1, 2, 7, 8, 64, 127, 128, 129, 500, 512, 513, 1000, 1531, 2048, 2056, 4096, 4100, 5120, 8192, 8200, 13824, 16384,
-          18944, 33000]
+WIDTHS = [1, 2, 7, 8, 64, 127, 128, 129, 250, 256, 257, 500, 512, 513, 1000, 1531, 2048, 2056, 4096, 4100, 5120, 8192, 8200, 13824, 16384,
+          17000, 18944, 25000, 32768, 33000]
 
 
 @pytest.mark.parametrize("k", WIDTHS)
@@ -112,7 +112,7 @@ def test_parts(api, gate, post, residual, k):
 
 
 @pytest.mark.parametrize("t", [0, 1, 2, 3, 4, 5, 63, 1000])
-@pytest.mark.parametrize("k", [96, 640])
+@pytest.mark.parametrize("k", [40, 96, 200, 640, 1500])
 def test_rows(api, t, k):
     if t == 0:
         y, h = api.block_norm(torch.empty(0, k, device=DEV), None)

@@ -561,7 +561,7 @@ def _scratch(ws, need: int, x: torch.Tensor):
     if ws is None:
         if not need:
             return None, None, 0
-        ws = x.new_empty(need, dtype=torch.uint8)
+        ws = torch.empty(need, dtype=torch.uint8, device=x.device)
     else:
         _workspace(ws, "workspace", need, x.device)
     return ws, ws.data_ptr(), ws.numel()
@@ -640,10 +640,10 @@ def fp8_quantize(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Te
     t, k = x.shape
     dev, kb = x.get_device(), -(-k // 128)
     if q is None:
-        q = x.new_empty((t, k), dtype=_F8)
+        q = torch.empty_like(x, dtype=_F8)
     ldq = _rows(q, "q", _F8S, dev, (t, k))
     if scale is None:
-        scale = x.new_empty((kb, t), dtype=torch.float32)
+        scale = torch.empty(kb, t, dtype=torch.float32, device=x.device)
     check(_lib.LIB.mbq_fp8_quantize(t, k, x.data_ptr(), _CODE[x.dtype], ldx, q.data_ptr(), ldq,
                                     _flat(scale, "scale", _F32S, dev, (kb, t)), _stream_of(x)), "mbq_fp8_quantize")
     return q, scale
@@ -666,7 +666,7 @@ def _fp8_run(p, x, scale, act, out_dtype, y, workspace):
     elif scale is not None:
         raise TypeError("scale belongs to float8_e4m3fn activations")
     if y is None:
-        y = x.new_empty((t, n), dtype=out_dtype or (torch.bfloat16 if code == MBQ_E4M3 else x.dtype))
+        y = torch.empty(t, n, dtype=out_dtype or (torch.bfloat16 if code == MBQ_E4M3 else x.dtype), device=x.device)
     y_ptr, y_code = _flat(y, "y", _FLOATS, dev, (t, n)), _CODE[y.dtype]
     _ws, ws_ptr, ws_bytes = _scratch(workspace, p._workspace_bytes(t, code), x)
     if act is None:
@@ -741,17 +741,17 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor | None = None, pre: torch
         else:
             gate_kind, gate_ptr = _lib.MBQ_GATE_TOKEN, _flat(gate, "gate", _F32S, dev, (t,))
     if y is None:
-        y, ldy = x.new_empty(shape, dtype=r_dtype), k
+        y, ldy = torch.empty_like(x, dtype=r_dtype), k
     else:
         ldy = _rows(y, "y", (r_dtype,), dev, shape)
     if h is None:
-        h, ldh = x.new_empty(shape, dtype=_F8 if quantized else out_dtype or x.dtype), k
+        h, ldh = torch.empty_like(x, dtype=_F8 if quantized else out_dtype or x.dtype), k
     else:
         ldh = _rows(h, "h", _F8S if quantized else _FLOATS if out_dtype is None else (out_dtype,), dev, shape)
     s_ptr = 0
     if quantized:
         if scale is None:
-            scale = x.new_empty((-(-k // 128), t), dtype=torch.float32)
+            scale = torch.empty(-(-k // 128), t, dtype=torch.float32, device=x.device)
         s_ptr = _flat(scale, "scale", _F32S, dev, (-(-k // 128), t))
     elif scale is not None:
         raise TypeError("scale belongs to quantized=True")
@@ -790,11 +790,14 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0, in
     tg_ptr = _flat(targets, "targets", _IDS, dev, (t,))
     if not 0 <= top <= min(v, _lib.MBQ_MAX_TOP):
         raise ValueError(f"top must lie in 0 .. {min(v, _lib.MBQ_MAX_TOP)}")
-    logprob, entropy = logits.new_empty(t, dtype=torch.float32), logits.new_empty(t, dtype=torch.float32)
-    rank = logits.new_empty(t, dtype=torch.int32)
+    device = logits.device
+    logprob = torch.empty(t, dtype=torch.float32, device=device)
+    entropy = torch.empty_like(logprob)
+    rank = torch.empty_like(logprob, dtype=torch.int32)
     ids = best = ids_ptr = best_ptr = None
     if top:
-        ids, best = logits.new_empty((t, top), dtype=torch.int32), logits.new_empty((t, top), dtype=torch.float32)
+        best = torch.empty(t, top, dtype=torch.float32, device=device)
+        ids = torch.empty_like(best, dtype=torch.int32)
         ids_ptr, best_ptr = ids.data_ptr(), best.data_ptr()
     _ws, ws_ptr, ws_bytes = _scratch(workspace, _lib.token_logprobs_workspace_bytes(t, v, top), logits)
     check(_lib.LIB.mbq_token_logprobs(t, v, logits.data_ptr(), _CODE[logits.dtype], ld, tg_ptr,

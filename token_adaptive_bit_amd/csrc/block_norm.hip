@@ -10,23 +10,18 @@ namespace {
 
 typedef mbq_block_norm_args Args;
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
+constexpr int kMaxWaves = 16;
 
-// Sum over the W waves that share a row, the same in every lane; `slot` alternates between
-// consecutive sums so that one barrier a sum is enough.
-template <int W>
-__device__ __forceinline__ float row_sum(float v, float (*red)[W], int slot) {
-  v = wave_sum(v);
-  if constexpr (W == 1) return v;
-  if ((threadIdx.x & 63) == 0) red[slot][(threadIdx.x >> 6) % W] = v;
+// Sum over the threads that share a row (16, 32 or whole waves), the same in all of them;
+// `slot` alternates between consecutive sums so that one barrier a sum is enough.
+__device__ __forceinline__ float row_sum(float v, float (*red)[kMaxWaves], int slot, int threads) {
+  for (int o = min(threads, 64) / 2; o; o >>= 1) v += __shfl_xor(v, o);
+  if (threads <= 64) return v;
+  const int wave = threadIdx.x >> 6, waves = threads >> 6;
+  if ((threadIdx.x & 63) == 0) red[slot][wave] = v;
   __syncthreads();
   float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < W; ++i) s += red[slot][i];
+  for (int i = 0; i < waves; ++i) s += red[slot][i];
   return s;
 }
 
@@ -81,67 +76,84 @@ __device__ __forceinline__ void store_h(const Args& a, int64_t row, int64_t i, c
   }
 }
 
-// W waves a row, V groups of 8 elements a thread (element 8 (tid + 64 W j) + e); RPB rows
-// a workgroup.
-template <int W, int V, int RPB, bool XB, bool RB, int HT>
-__global__ __launch_bounds__(64 * W * RPB) void norm_kernel(Args a) {
-  __shared__ float red[RPB][2][W];
-  const int tid = threadIdx.x % (64 * W), sub = threadIdx.x / (64 * W);
-  const int64_t row = int64_t(blockIdx.x) * RPB + sub;
-  if (row >= a.t) return;  // W == 1 wherever RPB > 1: no barrier is left behind
-  const int64_t k = a.k;
+// blockDim.x threads a row, V groups of 8 elements a thread (element 8 (tid + threads j) + e),
+// blockDim.y rows a workgroup.
+template <int V, bool XB, bool RB, int HT>
+__global__ __launch_bounds__(1024) void norm_kernel(Args a) {
+  __shared__ float reds[2][2][kMaxWaves];  // of at most two rows of several waves
+  const int tid = threadIdx.x, threads = blockDim.x;
+  float (*red)[kMaxWaves] = reds[threads > 64 ? threadIdx.y : 0];
+  const int64_t asked = int64_t(blockIdx.x) * blockDim.y + threadIdx.y;
+  const bool spare = asked >= a.t;  // the last workgroup's rows past the end take part in its barriers
+  const int64_t row = spare ? a.t - 1 : asked;
+  const int k = a.k;
   const float inv_k = 1.f / float(a.k);
   const bool layer = a.kind == MBQ_NORM_LAYER;
   float v[V][8];
 #pragma unroll
   for (int j = 0; j < V; ++j)
-    load8<XB>(static_cast<const uint8_t*>(a.x) + row * a.ldx * (XB ? 2 : 4), 8 * (tid + 64 * W * j), k, v[j]);
+    load8<XB>(static_cast<const uint8_t*>(a.x) + row * a.ldx * (XB ? 2 : 4), 8 * (tid + threads * j), k, v[j]);
 
+  // Elements past the row are 0 before and after (their weights and biases read as 0).
   auto norm = [&](const float* weight, const float* bias) {
-    float mean = 0.f;
     if (layer) {
       float s = 0.f;
 #pragma unroll
       for (int j = 0; j < V; ++j)
 #pragma unroll
         for (int e = 0; e < 8; ++e) s += v[j][e];
-      mean = row_sum<W>(s, red[sub], 0) * inv_k;
+      const float mean = row_sum(s, red, 0, threads) * inv_k;
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const int i = 8 * (tid + threads * j);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] -= mean;
+        if (i + 8 > k) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[j][e] = i + e < k ? v[j][e] : 0.f;
+        }
+      }
     }
     float s = 0.f;
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int64_t i = 8 * (tid + 64 * W * j) + e;
-        const float d = layer ? (i < k ? v[j][e] - mean : 0.f) : v[j][e];
-        v[j][e] = d;
-        s = fmaf(d, d, s);
-      }
-    const float rstd = 1.f / sqrtf(row_sum<W>(s, red[sub], 1) * inv_k + a.eps);
+      for (int e = 0; e < 8; ++e) s = fmaf(v[j][e], v[j][e], s);
+    const float rstd = 1.f / sqrtf(row_sum(s, red, 1, threads) * inv_k + a.eps);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-      float w[8], b[8];
-      const int64_t i = 8 * (tid + 64 * W * j);
-      load_or(weight, i, k, 1.f, w);
-      load_or(bias, i, k, 0.f, b);
+      const int i = 8 * (tid + threads * j);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[j][e] = i + e < k ? fmaf(v[j][e] * rstd, w[e], b[e]) : 0.f;
+      for (int e = 0; e < 8; ++e) v[j][e] *= rstd;
+      if (weight) {
+        float w[8];
+        load8<false>(weight, i, k, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] *= w[e];
+      }
+      if (bias) {
+        float b[8];
+        load8<false>(bias, i, k, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[j][e] += b[e];
+      }
     }
   };
 
   if (a.post) norm(a.post_weight, a.post_bias);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
-    const int64_t i = 8 * (tid + 64 * W * j);
+    const int i = 8 * (tid + threads * j);
     if (i < k) {
       join_residual<XB, RB>(a, row, i, v[j]);
-      if (a.y) store8<RB>(static_cast<uint8_t*>(a.y) + row * a.ldy * (RB ? 2 : 4), i, k, v[j]);
+      if (a.y && !spare) store8<RB>(static_cast<uint8_t*>(a.y) + row * a.ldy * (RB ? 2 : 4), i, k, v[j]);
     }
   }
-  if (W > 1 && a.post) __syncthreads();  // the first norm's sums are read before the second's are written
+  if (threads > 64 && a.post) __syncthreads();  // the first norm's sums are read before the second's are written
   norm(a.pre_weight, a.pre_bias);
+  if (spare) return;
 #pragma unroll
-  for (int j = 0; j < V; ++j) store_h<HT>(a, row, 8 * (tid + 64 * W * j), v[j]);
+  for (int j = 0; j < V; ++j) store_h<HT>(a, row, 8 * (tid + threads * j), v[j]);
 }
 
 // Rows too long for registers: 1024 threads walk the row once for each statistic and once
@@ -149,8 +161,7 @@ __global__ __launch_bounds__(64 * W * RPB) void norm_kernel(Args a) {
 // the last walk only, by the thread that read it).
 template <bool XB, bool RB, int HT>
 __global__ __launch_bounds__(1024) void norm_long_kernel(Args a) {
-  constexpr int W = 16;
-  __shared__ float red[2][W];
+  __shared__ float red[2][kMaxWaves];
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x, k = a.k, step = 8 * 1024;
   const int64_t kr = (k + step - 1) / step * step;  // whole walks: every lane takes part in the sums
@@ -183,7 +194,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(Args a) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) s += i + e < k ? v[e] : 0.f;
       }
-      mean = row_sum<W>(s, red, slot) * inv_k;
+      mean = row_sum(s, red, slot, 1024) * inv_k;
       slot ^= 1;
     }
     float s = 0.f;
@@ -195,7 +206,7 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(Args a) {
         s = fmaf(d, d, s);
       }
     }
-    rstd = 1.f / sqrtf(row_sum<W>(s, red, slot) * inv_k + a.eps);
+    rstd = 1.f / sqrtf(row_sum(s, red, slot, 1024) * inv_k + a.eps);
     slot ^= 1;
     __syncthreads();
   };
@@ -217,15 +228,31 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(Args a) {
   }
 }
 
+// Threads for a row are bought in waves of 512 elements: as many waves as fit the row with
+// two groups of 8 elements a thread (enough loads in flight; a thread's slots past the row
+// cost its issue time), three where that takes fewer waves for the same slots (3 and 5
+// times 512), more only where 16 waves are not enough; 16 or 32 lanes for rows of up to 128
+// or 256.  GB/s at 2^26 elements, bfloat16, both norms and a gate, with 1 / 2 / 3 / 4 groups:
+// 1024 5299 / 5559 / 5381 / 4743; 1531 3029 / 3344 / 4025 / 3753; 5120 3574 / 4630 / 4737 /
+// 4583; 8192 4534 / 4952 / 4273 / 4516; 16384 two: 4670, three: 4245.
 template <bool XB, bool RB, int HT>
 hipError_t launch(const Args& a, hipStream_t s) {
-  const uint32_t t = uint32_t(a.t);
-  if (a.k <= 512) norm_kernel<1, 1, 4, XB, RB, HT><<<(t + 3) / 4, 256, 0, s>>>(a);
-  else if (a.k <= 2048) norm_kernel<4, 1, 1, XB, RB, HT><<<t, 256, 0, s>>>(a);
-  else if (a.k <= 4096) norm_kernel<4, 2, 1, XB, RB, HT><<<t, 256, 0, s>>>(a);
-  else if (a.k <= 8192) norm_kernel<8, 2, 1, XB, RB, HT><<<t, 512, 0, s>>>(a);
-  else if (a.k <= 16384) norm_kernel<16, 2, 1, XB, RB, HT><<<t, 1024, 0, s>>>(a);
-  else norm_long_kernel<XB, RB, HT><<<t, 1024, 0, s>>>(a);
+  const int units = (a.k + 511) / 512;
+  if (units > 4 * kMaxWaves) {
+    norm_long_kernel<XB, RB, HT><<<uint32_t(a.t), 1024, 0, s>>>(a);
+    return hipGetLastError();
+  }
+  int v = units == 1 ? 1 : units == 3 || units == 5 ? 3 : 2;
+  while ((units + v - 1) / v > kMaxWaves) ++v;
+  const int threads = a.k <= 128 ? 16 : a.k <= 256 ? 32 : 64 * ((units + v - 1) / v);
+  const int rows = threads <= 64 ? 256 / threads : threads == 128 ? 2 : 1;
+  const dim3 grid((uint32_t(a.t) + rows - 1) / rows), block(threads, rows);
+  switch (v) {
+    case 1: norm_kernel<1, XB, RB, HT><<<grid, block, 0, s>>>(a); break;
+    case 2: norm_kernel<2, XB, RB, HT><<<grid, block, 0, s>>>(a); break;
+    case 3: norm_kernel<3, XB, RB, HT><<<grid, block, 0, s>>>(a); break;
+    default: norm_kernel<4, XB, RB, HT><<<grid, block, 0, s>>>(a); break;
+  }
   return hipGetLastError();
 }
 

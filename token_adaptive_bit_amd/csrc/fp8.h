@@ -96,10 +96,27 @@ __device__ __forceinline__ uint32_t amax8(const float (&v)[8]) {
   return m;
 }
 
-// Factor that takes a block to codes and the scale that takes codes back, from the bits of
-// the block's largest magnitude (at least 2^-96, so that both are finite numbers).
-__device__ __forceinline__ float fp8_factor(uint32_t amax) { return 448.f / __uint_as_float(max(amax, 0x0F800000u)); }
-__device__ __forceinline__ float fp8_scale(uint32_t amax) { return __uint_as_float(max(amax, 0x0F800000u)) / 448.f; }
+// Factor that takes a block to codes, 448 / a, and the scale that takes codes back, a / 448,
+// from the bits of the block's largest magnitude (a is at least 2^-96, so that both are
+// finite numbers).  Both are correctly rounded by Markstein's method, a product with the
+// reciprocal and one correction by the exact remainder: a few instructions where the
+// general division, which also serves subnormal numbers, takes a dozen each.  Infinity and
+// NaN have no remainder: the factor 0 or NaN and the scale itself.
+__device__ __forceinline__ float fp8_factor(uint32_t amax) {
+  const float a = __uint_as_float(max(amax, 0x0F800000u));
+  const float b = a * 0x1p-16f;  // 2^-112 .. 2^112: its reciprocal is a normal number
+  float y = __builtin_amdgcn_rcpf(b);
+  y = fmaf(fmaf(-b, y, 1.f), y, y);
+  const float n = 448.f * 0x1p-16f, q = n * y;
+  const float f = fmaf(fmaf(-b, q, n), y, q);
+  return amax < 0x7F800000u ? f : amax == 0x7F800000u ? 0.f : a;
+}
+__device__ __forceinline__ float fp8_scale(uint32_t amax) {
+  const float a = __uint_as_float(max(amax, 0x0F800000u));
+  const float y = 1.f / 448.f, q = a * y;
+  const float s = fmaf(fmaf(-448.f, q, a), y, q);
+  return amax < 0x7F800000u ? s : a;
+}
 
 // Four e4m3 codes, round to nearest even (|v| <= 448 up to a rounding, so nothing
 // saturates; NaN stays NaN).

@@ -85,10 +85,10 @@ struct TopList {
     last = lane_key(mine, top - 1);
     if (last) floor = from_ordered(uint32_t(last >> 32));
   }
-  // Raises the floor of a list without real values yet to one that at least `top` lanes' x reach: found
-  // bit by bit over the upper half of the ordered value, so that the list fills with about
-  // `top` insertions and not with top (1 + ln(n / top)).  (NaN sorts above all; its row has
-  // no list.)
+  // Raises the floor of a list without real values yet to one that at least `top` lanes' x
+  // reach, found bit by bit over the upper half of the ordered value: the list then fills
+  // with little more than `top` entries, not with top (1 + ln(n / top)).  (NaN sorts above
+  // all; its row has no list.)
   __device__ __forceinline__ void start(float x, int top) {
     const uint32_t o = ordered(x);
     uint32_t t = 0;
@@ -267,8 +267,37 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
         raw[u].get(x);
         best[u] = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
       }
+      bool listed = false;  // this step's entries are in the list already
       if constexpr (TOP) {
-        if (list.floor == -__builtin_inff()) list.start(fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])), a.top);
+        if (list.floor == -__builtin_inff()) {
+          list.start(fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])), a.top);
+          if (a.top > 8 && __ballot(list.mine != 0) == 0) {
+            // an empty list: what reaches the floor, side by side in LDS, sorted at once (one
+            // row of 131072, top 20: 16.8 us against 18.1; 2048 x 128000, top 8: 147 against 143)
+            int n = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const int i = i0 + (u * 64 + lane) * 8;
+              float x[8];
+              raw[u].get(x);
+              if (__ballot(best[u] >= list.floor && i < end)) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const bool in = x[e] >= list.floor && i + e < end;
+                  const uint64_t m = __ballot(in);
+                  const int at = n + __builtin_amdgcn_mbcnt_hi(uint32_t(m >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(m), 0));
+                  if (in && at < 64) lists[wave][at] = key_of(x[e], uint32_t(i + e));
+                  n += __popcll(m);
+                }
+              }
+            }
+            if (n <= 64) {
+              list.fill(lane < n ? lists[wave][lane] : 0, lane, a.top);
+              list.close_vector();
+              listed = true;
+            }
+          }
+        }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -305,7 +334,7 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
           for (int e = 0; e < 8; ++e) tied += i + e < target && x[e] == xt;
         }
         if constexpr (TOP) {
-          if (__ballot(best[u] >= list.gate && i < end)) {
+          if (!listed && __ballot(best[u] >= list.gate && i < end)) {
             int at = i;
             asm("" : "+v"(at));  // the indexes are computed here and not in every step
 #pragma unroll
@@ -373,7 +402,8 @@ __global__ __launch_bounds__(kThreads) void merge_kernel(LpArgs a) {
 }
 
 // Parts of a row: at least 4096 waves (four a SIMD), each with at least one full step of its
-// loop.  Fewer, longer parts mean fewer lists to fill: NNN.
+// loop.  (2048 x 128000 bfloat16, top 8: 143 us with two parts a row, 162 with one; 300 x
+// 100000, top 20: 53 with 14 parts, 59 with 4.)
 int parts_of(int32_t t, int32_t v) {
   const int64_t want = (4096 + int64_t(t) - 1) / std::max(t, 1), most = (int64_t(v) + 2047) / 2048;
   const int p = int(std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), kMaxParts)));
