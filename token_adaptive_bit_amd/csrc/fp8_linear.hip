@@ -262,20 +262,21 @@ __global__ __launch_bounds__(256) void join_kernel(LinArgs a) {
   }
 }
 
-// Up to 16 TT tokens: every workgroup streams one row block (gated: the pair), its eight
-// waves take every eighth 128-input block, and their sums meet in LDS in a fixed order.
+// Up to 16 TT tokens: every workgroup streams one row block (gated: the pair), its W
+// waves take every W-th 128-input block, and their sums meet in LDS in a fixed order.  What
+// keeps memory busy is the number of waves on a unit: a set of loads one step ahead in
+// registers was slower (18944 x 3584, 16 tokens: 23.0 us against 17.6).
 // XT: the type of x.  Codes (MBQ_E4M3) are read from memory, with every block of the weight;
 // a few float tokens are quantized here, once a workgroup into LDS, while the first weight
 // tiles are on their way, which saves the quantizing launch.
-constexpr int kStreamWaves = 8;
-constexpr int kInlineBlocks = 160;  // quantized in the kernel: at most 5 blocks for each 16 lanes
+constexpr int kInlineBlocks = 148;  // quantized in the kernel: at most 5 blocks for each 16 lanes
 
-template <int TT, int XT, int ACT, bool YBF>
-__global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(LinArgs a) {
+template <int W, int TT, int XT, int ACT, bool YBF>
+__global__ __launch_bounds__(64 * W) void stream_kernel(LinArgs a) {
   constexpr int R = ACT == kPlain ? 1 : 2, U = TT == 1 ? 4 : 2;
   constexpr bool kInline = XT != MBQ_E4M3;
   static_assert(!kInline || TT == 1, "a few tokens");
-  __shared__ f32x4_t red[kStreamWaves][R * TT][64];
+  __shared__ f32x4_t red[W][R * TT][64];
   __shared__ __align__(16) uint8_t lx[kInline ? kInlineBlocks * kFp8Block + 16 * 16 : 16];  // rows 16 bytes apart in banks
   __shared__ float ls[kInline ? kInlineBlocks : 1];                                         // [kb][t]
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -289,7 +290,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(LinArgs a) {
   auto load_w = [&](int k0) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int kb = min(k0 + u * kStreamWaves, a.kb - 1);
+      const int kb = min(k0 + u * W, a.kb - 1);
 #pragma unroll
       for (int i = 0; i < R; ++i) {
         const uint8_t* p = wp + (int64_t(i) * a.kb + kb) * kFp8TileBytes;
@@ -301,7 +302,7 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(LinArgs a) {
   load_w(wave);
   if constexpr (kInline) {
     const int g = threadIdx.x & 15;
-    for (int b = threadIdx.x >> 4; b < a.t * a.kb; b += 4 * kStreamWaves) {  // block b / t of token b % t
+    for (int b = threadIdx.x >> 4; b < a.t * a.kb; b += 4 * W) {  // block b / t of token b % t
       const int blk = b / a.t, tok = b - blk * a.t, i = blk * kFp8Block + g * 8;
       float v[8];
       load8<XT == MBQ_BF16>(static_cast<const uint8_t*>(a.x) + tok * a.ldx * (XT == MBQ_BF16 ? 2 : 4), i, a.k, v);
@@ -316,13 +317,13 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(LinArgs a) {
   for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int j = 0; j < TT; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  for (int k0 = wave; k0 < a.kb; k0 += kStreamWaves * U) {
+  for (int k0 = wave; k0 < a.kb; k0 += W * U) {
     if (k0 != wave) load_w(k0);
     u32x4_t xf[U][TT][2];
     float xs[U][TT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int kb = min(k0 + u * kStreamWaves, a.kb - 1);
+      const int kb = min(k0 + u * W, a.kb - 1);
 #pragma unroll
       for (int j = 0; j < TT; ++j) {
         const int tok = min(j * 16 + r, a.t - 1), col = kb * kFp8Block + 16 * c;
@@ -341,15 +342,15 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(LinArgs a) {
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int kb = k0 + u * kStreamWaves;
+      const int kb = k0 + u * W;
       if (kb >= a.kb) break;
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        const float w = i == 0 ? wsp[kb] : wsu[kb];
+        const float ws = i == 0 ? wsp[kb] : wsu[kb];
 #pragma unroll
         for (int j = 0; j < TT; ++j) {
           const f32x4_t d = block_product<!YBF>(join(wf[u][i][0], wf[u][i][1]), join(xf[u][j][0], xf[u][j][1]));
-          const float s = xs[u][j] * w;
+          const float s = xs[u][j] * ws;
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[i][j][e] = fmaf(d[e], s, acc[i][j][e]);
         }
@@ -367,8 +368,8 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(LinArgs a) {
 #pragma unroll
   for (int i = 0; i < R; ++i) {
     sum[i] = red[0][i * TT + j][lane];
-#pragma unroll
-    for (int w = 1; w < kStreamWaves; ++w)
+#pragma unroll 5
+    for (int w = 1; w < W; ++w)
 #pragma unroll
       for (int e = 0; e < 4; ++e) sum[i][e] += red[w][i * TT + j][lane][e];
   }
@@ -385,8 +386,8 @@ __global__ __launch_bounds__(64 * kStreamWaves) void stream_kernel(LinArgs a) {
 // The tile and the chunks of K for a shape.  A workgroup's time is its blocks times the
 // tile's time a block, and workgroups run in rounds of one on each of the 256 compute units
 // (two on a unit take twice as long).  Times a block measured on one box, alone and with
-// every unit busy: 256 x 256 1.46-1.86 us, 128 x 128 0.64, 64 x 128 0.52, 64 x 64 0.40
-// (the smaller, the more of it is the wait of a block).
+// every unit busy: 256 x 256 1.46-1.86 us, 128 x 128 0.64, 64 x 128 0.52, 128 x 64 0.48,
+// 64 x 64 0.40 (the smaller, the more of it is the wait of a block).
 // Splitting K costs a second launch and the partial sums' traffic.  For instance (us, tiles
 // in this order without the second): 1024 x 4096 x 4096 60 / 27 / 38 / 44; 512 x 3584 x 3584
 // 53 / 23 / 19 / 22; 1024 x 1024 x 8192 105 / 44 / 36 / 27.
@@ -394,15 +395,15 @@ struct Tile {
   int rn, rt;
   float us;
 };
-constexpr Tile kTiles[] = {{8, 4, 1.8f}, {4, 2, 0.64f}, {2, 2, 0.52f}, {2, 1, 0.40f}};
+constexpr Tile kTiles[] = {{8, 4, 1.8f}, {4, 2, 0.64f}, {2, 2, 0.52f}, {4, 1, 0.48f}, {2, 1, 0.40f}};
 struct Plan {
   int tile, chunks;
 };
 
 Plan plan_gemm(int32_t t, int32_t rbs, int32_t kb, bool exact) {
-  Plan best{3, 1};
+  Plan best{4, 1};
   float best_us = 1e30f;
-  for (int i = exact ? 1 : 0; i < 4; ++i) {  // float32 outputs: the smaller tiles only (registers)
+  for (int i = exact ? 1 : 0; i < 5; ++i) {  // float32 outputs: the smaller tiles only (registers)
     const int64_t tiles = int64_t((rbs + 2 * kTiles[i].rn - 1) / (2 * kTiles[i].rn)) * ((t + 64 * kTiles[i].rt - 1) / (64 * kTiles[i].rt));
     for (int s = 1; s <= 16 && s <= kb; s *= 2) {
       if (s > 1 && tiles * s > 512) break;
@@ -424,18 +425,38 @@ void launch_gemm(const LinArgs& a, hipStream_t stream) {
   gemm_kernel<RN, RT, NS, ACT, YBF><<<uint32_t(tiles * a.chunks), 512, 0, stream>>>(a);
 }
 
-constexpr int kStreamTokens = 64;
+// Up to 16 tokens the streaming kernel serves every weight; up to 64 those of few row blocks
+// (us with it / in tiles: 32 tokens 1024 x 4096 9.2 / 12.6, 5120 x 5120 17.0 / 14.4; 64
+// tokens 18944 x 3584 41.1 / 21.6).
+bool streams(int32_t t, int32_t row_groups) { return t <= 16 || (t <= 64 && (t + 15) / 16 * row_groups <= 256); }
+
+
+template <int W, int TT, int ACT, bool YBF>
+void launch_stream(const LinArgs& a, mbq_dtype x_dtype, hipStream_t stream) {
+  const dim3 grid(a.rbs / (ACT == kPlain ? 1 : 2)), block(64 * W);
+  if constexpr (TT == 1) {
+    if (a.x && x_dtype == MBQ_BF16) {
+      stream_kernel<W, 1, MBQ_BF16, ACT, YBF><<<grid, block, 0, stream>>>(a);
+      return;
+    }
+    if (a.x) {
+      stream_kernel<W, 1, MBQ_F32, ACT, YBF><<<grid, block, 0, stream>>>(a);
+      return;
+    }
+  }
+  stream_kernel<W, TT, MBQ_E4M3, ACT, YBF><<<grid, block, 0, stream>>>(a);
+}
 
 template <int ACT, bool YBF>
 hipError_t launch(LinArgs& a, mbq_dtype x_dtype, hipStream_t stream) {
   constexpr int R = ACT == kPlain ? 1 : 2;
-  if (a.t <= kStreamTokens) {
-    const dim3 grid(a.rbs / R), block(64 * kStreamWaves);
-    if (a.x && x_dtype == MBQ_BF16) stream_kernel<1, MBQ_BF16, ACT, YBF><<<grid, block, 0, stream>>>(a);
-    else if (a.x) stream_kernel<1, MBQ_F32, ACT, YBF><<<grid, block, 0, stream>>>(a);
-    else if (a.t <= 16) stream_kernel<1, MBQ_E4M3, ACT, YBF><<<grid, block, 0, stream>>>(a);
-    else if (a.t <= 32) stream_kernel<2, MBQ_E4M3, ACT, YBF><<<grid, block, 0, stream>>>(a);
-    else stream_kernel<4, MBQ_E4M3, ACT, YBF><<<grid, block, 0, stream>>>(a);
+  if (streams(a.t, a.rbs / R)) {
+    // sixteen waves for long rows of few row groups, which leave the units half empty with
+    // eight (one token, 8 / 16 waves: 3584 x 18944 17.9 / 14.2 us, 5120 x 5120 7.8 / 8.3)
+    if (a.t <= 16 && a.rbs / R <= 256 && a.kb >= 64) launch_stream<16, 1, ACT, YBF>(a, x_dtype, stream);
+    else if (a.t <= 16) launch_stream<8, 1, ACT, YBF>(a, x_dtype, stream);
+    else if (a.t <= 32) launch_stream<8, 2, ACT, YBF>(a, x_dtype, stream);
+    else launch_stream<8, 4, ACT, YBF>(a, x_dtype, stream);
     return hipGetLastError();
   }
   const Plan p = plan_gemm(a.t, a.rbs, a.kb, !YBF);
@@ -447,6 +468,7 @@ hipError_t launch(LinArgs& a, mbq_dtype x_dtype, hipStream_t stream) {
       break;
     case 1: launch_gemm<4, 2, 3, ACT, YBF>(a, stream); break;
     case 2: launch_gemm<2, 2, 3, ACT, YBF>(a, stream); break;
+    case 3: launch_gemm<4, 1, 3, ACT, YBF>(a, stream); break;
     default: launch_gemm<2, 1, 3, ACT, YBF>(a, stream); break;
   }
   if (a.chunks > 1)
@@ -472,7 +494,7 @@ size_t fp8_linear_workspace(const mbq_fp8_desc& d, int32_t t, mbq_dtype x_dtype)
   if (quantize_inline(d, t, x_dtype)) return 0;
   if (x_dtype != MBQ_E4M3) bytes = codes_bytes(d, t) + align256(size_t(d.k_blocks) * t * 4);
   size_t part = 0;
-  if (t > kStreamTokens)
+  if (!streams(t, d.row_blocks / (d.gated + 1)))
     for (bool exact : {false, true}) {  // y's type is not known here
       const int chunks = plan_gemm(t, d.row_blocks, d.k_blocks, exact).chunks;
       if (chunks > 1) part = std::max(part, size_t(chunks) * t * d.row_blocks * 64);
