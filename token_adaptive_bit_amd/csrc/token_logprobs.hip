@@ -166,6 +166,9 @@ __device__ __forceinline__ float logit(const LpArgs& a, int row, int64_t i) {
   return load_x(a.logits, size_t(row) * size_t(a.ld) + size_t(i), BF16);
 }
 
+// The last rounding takes no probability above 1 and no entropy below 0 (NaN stays).
+__device__ __forceinline__ float at_most_0(float v) { return v > 0.f ? 0.f : v; }
+
 // Writes a row's results from its sums and its top list (one wave).
 template <bool BF16>
 __device__ __forceinline__ void finish(const LpArgs& a, int row, const Sums& sums, int count, const TopList& list,
@@ -177,14 +180,14 @@ __device__ __forceinline__ void finish(const LpArgs& a, int row, const Sums& sum
   const float log_s = logf(s), inf = __builtin_inff();
   if (lane == 0) {
     const float xt = valid ? logit<BF16>(a, row, target) : 0.f;
-    a.logprob[row] = !valid ? 0.f : none ? -inf : sums.natural(xt, c, a.inv_temperature) - log_s;
-    a.entropy[row] = none ? 0.f : log_s - kLn2 * (sums.q / s);
+    a.logprob[row] = !valid ? 0.f : none ? -inf : at_most_0(sums.natural(xt, c, a.inv_temperature) - log_s);
+    a.entropy[row] = none ? 0.f : -at_most_0(kLn2 * (sums.q / s) - log_s);
     a.rank[row] = valid && !bad ? count + 1 : 0;
   }
   if (lane < a.top) {
     const float x = from_ordered(uint32_t(list.mine >> 32));
     a.top_ids[int64_t(row) * a.top + lane] = bad ? -1 : int32_t(~uint32_t(list.mine));
-    a.top_logprobs[int64_t(row) * a.top + lane] = none ? -inf : bad ? s : sums.natural(x, c, a.inv_temperature) - log_s;
+    a.top_logprobs[int64_t(row) * a.top + lane] = none ? -inf : bad ? s : at_most_0(sums.natural(x, c, a.inv_temperature) - log_s);
   }
 }
 
@@ -310,21 +313,26 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
         if (__ballot(far)) {
           if (far) sums.refer(best[u], c);
         }
+        // A vector's terms are summed apart and then added: the lane's long chain has an
+        // eighth of the roundings.
+        float ps = 0.f, pq = 0.f;
         if (__ballot(sums.m != 0.f)) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float d = sums.exponent(x[e], c), p = __builtin_amdgcn_exp2f(d);
-            sums.s += p;
-            sums.q = fmaf(p, fmaxf(d, -1e4f), sums.q);  // finite, so that p = 0 adds 0
+            ps += p;
+            pq = fmaf(p, fmaxf(d, -1e4f), pq);  // finite, so that p = 0 adds 0
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const float d = fmaf(x[e], c, -sums.M), p = __builtin_amdgcn_exp2f(d);
-            sums.s += p;
-            sums.q = fmaf(p, fmaxf(d, -1e4f), sums.q);
+            ps += p;
+            pq = fmaf(p, fmaxf(d, -1e4f), pq);
           }
         }
+        sums.s += ps;
+        sums.q += pq;
         // a part ends on a vector; what is read past it counts for nothing
         const float bound = i >= end ? __builtin_inff() : i + 8 <= target ? xt : above;
 #pragma unroll
