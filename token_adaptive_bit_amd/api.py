@@ -14,6 +14,7 @@ from typing import NamedTuple
 import torch
 
 from . import _lib
+from . import _bind  # after _lib: the library and torch's runtime are loaded
 from ._lib import (MBQ_BF16, MBQ_E4M3, MBQ_F32, MBQ_MUL_AUTO, MBQ_MUL_BF16, MBQ_MUL_FP8_FP4, MBQ_PATH_AUTO,
                    MBQ_PATH_GENERIC, MbqDesc, MbqError, MbqFp8Desc, MbqOpts, check, describe,
                    fp8_describe)
@@ -498,8 +499,9 @@ def linear_lowrank(p: PackedLinear, x: torch.Tensor, perm: torch.Tensor, offsets
 
 # --- dense operators: the 8-bit linear, its gated form, the norms around a block and the
 # --- log probabilities of tokens.  A decode step makes many of these calls and each runs for
-# --- a few microseconds, so their checks take a short path for the ordinary tensor and name
-# --- what is wrong in a second pass.
+# --- a few microseconds, so ordinary calls (plain contiguous tensors, no buffers given) are
+# --- checked and made by _bind; what it leaves alone comes back here, where the checks name
+# --- what is wrong.
 
 _F8 = torch.float8_e4m3fn
 _CODE = {torch.float32: MBQ_F32, torch.bfloat16: MBQ_BF16, _F8: MBQ_E4M3}
@@ -514,6 +516,10 @@ def _stream_of(x: torch.Tensor):
     if i != _current_device():
         raise ValueError(f"x is on cuda:{i}, the current device is cuda:{_current_device()}")
     return _raw_stream(i)
+
+
+def _bound(x) -> bool:
+    return type(x) is torch.Tensor and x.is_cuda
 
 
 def _rows(t, name: str, dtypes, dev=None, shape=None) -> int:
@@ -574,7 +580,7 @@ class Fp8Linear:
     blob: torch.Tensor
 
     def __post_init__(self):
-        self._ref, self._sizes = ctypes.byref(self.desc), {}
+        self._ref, self._addr, self._sizes = ctypes.byref(self.desc), ctypes.addressof(self.desc), {}
 
     @property
     def n(self): return self.desc.n
@@ -636,6 +642,10 @@ def fp8_pack_gated(w_gate: torch.Tensor, w_up: torch.Tensor, scale_gate: torch.T
 def fp8_quantize(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None):
     """e4m3 codes of x [t, k] per token and 128 inputs.  Returns (q [t, k] float8_e4m3fn,
     scale [ceil(k / 128), t] float32): x is about q * scale."""
+    if q is None and scale is None and _bound(x):
+        r = _bind.fp8_quantize(x, dev := _current_device(), _raw_stream(dev))
+        if r is not None:
+            return r
     ldx = _rows(x, "x", _FLOATS)
     t, k = x.shape
     dev, kb = x.get_device(), -(-k // 128)
@@ -654,6 +664,11 @@ def fp8_linear_workspace(p: Fp8Linear, t: int, x_dtype=torch.bfloat16) -> int:
 
 
 def _fp8_run(p, x, scale, act, out_dtype, y, workspace):
+    if y is None and workspace is None and _bound(x):
+        r = _bind.fp8(p._addr, p.blob, x, scale, -1 if act is None else act, out_dtype, dev := _current_device(),
+                      _raw_stream(dev))
+        if r is not None:
+            return r
     ldx = _rows(x, "x", _CODE)
     t, k = x.shape
     dev, code, n, blob = x.get_device(), _CODE[x.dtype], p.desc.n, p.blob
@@ -720,6 +735,11 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor | None = None, pre: torch
     float8_e4m3fn, scale [ceil(k / 128), t] float32), which fp8_linear takes."""
     if kind not in _KINDS:
         raise ValueError(f"kind must be one of {sorted(_KINDS)}")
+    if y is None and h is None and scale is None and _bound(x):
+        r = _bind.block_norm(x, residual, pre, post, gate, residual_scale, gate_scale, eps, _KINDS[kind], pre_bias,
+                             post_bias, quantized, out_dtype, dev := _current_device(), _raw_stream(dev))
+        if r is not None:
+            return r
     ldx = _rows(x, "x", _FLOATS)
     shape = x.shape
     t, k = shape
@@ -784,6 +804,10 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0, in
     """Log probabilities of targets [t] (int32 or int64; outside [0, v): a padded position)
     under softmax(inv_temperature * logits [t, v]), with entropy, rank and the top (<= 64)
     alternatives, equal logits by ascending token."""
+    if workspace is None and _bound(logits):
+        r = _bind.token_logprobs(logits, targets, top, inv_temperature, dev := _current_device(), _raw_stream(dev))
+        if r is not None:
+            return TokenLogprobs._make(r)
     ld = _rows(logits, "logits", _FLOATS)
     t, v = logits.shape
     dev = logits.get_device()

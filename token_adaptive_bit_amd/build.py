@@ -1,4 +1,5 @@
-"""Build libmbq.so (gfx950) in the package directory with hipcc.
+"""Build libmbq.so (gfx950) in the package directory with hipcc, and the native binding of
+the dense operators (_bind.so, host code) with the C++ compiler.
 
 Every translation unit is compiled for gfx950 only, with packed FP32 instructions
 disabled (-packed-fp32-ops) and IEEE-correct float32 division.  The pack kernel is also
@@ -10,16 +11,19 @@ Usage:  python -m token_adaptive_bit_amd.build   (or __graft_entry__.build())
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import re
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libmbq.so")
+BIND = os.path.join(PKG, "_bind.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = {
@@ -99,19 +103,51 @@ def _compile(src: str, extra: list, verbose: bool) -> str:
     return obj
 
 
-def build(verbose: bool = False, jobs: int | None = None) -> str:
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    jobs = jobs or min(len(SOURCES), max(1, min(8, os.cpu_count() or 1)))
-    with cf.ThreadPoolExecutor(jobs) as ex:
-        objs = list(ex.map(lambda kv: _compile(kv[0], kv[1], verbose), SOURCES.items()))
-    tmp = OUT + ".tmp"
-    cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.origin:
+        raise RuntimeError("torch not found (the binding is built against it)")
+    return os.path.dirname(spec.origin)
+
+
+def _run(cmd: list, what: str, verbose: bool) -> None:
     if verbose:
         print(" ".join(cmd), flush=True)
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
+        raise RuntimeError(f"{what} failed:\n{res.stdout}\n{res.stderr}")
+
+
+def _compile_bind(verbose: bool) -> str:
+    """csrc/bind.cpp, the native calls of the dense operators (host code only)."""
+    obj, torch = os.path.join(BUILD_DIR, "bind.o"), _torch_dir()
+    cxx = shutil.which("g++") or hipcc()
+    _run([cxx, "-std=c++17", "-O2", "-fPIC", "-D__HIP_PLATFORM_AMD__=1", "-DUSE_ROCM=1", "-c", os.path.join(CSRC, "bind.cpp"),
+          "-I", os.path.join(torch, "include"), "-I", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+          "-I", sysconfig.get_paths()["include"], "-I", "/opt/rocm/include", "-o", obj], "compiling bind.cpp", verbose)
+    return obj
+
+
+def _link_bind(obj: str, verbose: bool) -> None:
+    lib, tmp = os.path.join(_torch_dir(), "lib"), BIND + ".tmp"
+    cxx = shutil.which("g++") or hipcc()
+    _run([cxx, "-shared", "-fPIC", "-o", tmp, obj, "-L", PKG, "-l:libmbq.so", "-L", lib, "-lc10", "-ltorch_cpu", "-ltorch_python",
+          "-Wl,-rpath,$ORIGIN"], "linking the binding", verbose)
+    os.replace(tmp, BIND)
+
+
+def build(verbose: bool = False, jobs: int | None = None) -> str:
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    jobs = jobs or min(len(SOURCES), max(1, min(8, os.cpu_count() or 1)))
+    with cf.ThreadPoolExecutor(jobs) as ex:
+        bind = ex.submit(_compile_bind, verbose)
+        objs = list(ex.map(lambda kv: _compile(kv[0], kv[1], verbose), SOURCES.items()))
+        bind_obj = bind.result()
+    tmp = OUT + ".tmp"
+    cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
+    _run(cmd, "link", verbose)
     os.replace(tmp, OUT)
+    _link_bind(bind_obj, verbose)
     return OUT
 
 

@@ -42,6 +42,25 @@ __device__ __forceinline__ uint64_t lane_key(uint64_t k, int lane) {
   return uint64_t(hi) << 32 | lo;
 }
 
+// The value of lane ^ STEP: by register moves inside 16 lanes, through LDS beyond.
+template <int STEP>
+__device__ __forceinline__ uint32_t across(uint32_t v) {
+  if constexpr (STEP == 1) return __builtin_amdgcn_update_dpp(0, int(v), 0xB1, 0xF, 0xF, true);   // quad 1 0 3 2
+  if constexpr (STEP == 2) return __builtin_amdgcn_update_dpp(0, int(v), 0x4E, 0xF, 0xF, true);   // quad 2 3 0 1
+  if constexpr (STEP == 4) {                                                                      // ^ 7, then ^ 3
+    const int m = __builtin_amdgcn_update_dpp(0, int(v), 0x141, 0xF, 0xF, true);                  // row_half_mirror
+    return __builtin_amdgcn_update_dpp(0, m, 0x1B, 0xF, 0xF, true);                               // quad 3 2 1 0
+  }
+  if constexpr (STEP == 8) return __builtin_amdgcn_update_dpp(0, int(v), 0x128, 0xF, 0xF, true);  // row_ror 8
+  return uint32_t(__shfl_xor(int(v), STEP));
+}
+template <int STEP>
+__device__ __forceinline__ float across(float v) { return __uint_as_float(across<STEP>(__float_as_uint(v))); }
+template <int STEP>
+__device__ __forceinline__ uint64_t across(uint64_t v) {
+  return uint64_t(across<STEP>(uint32_t(v >> 32))) << 32 | across<STEP>(uint32_t(v));
+}
+
 // The wave's best 64 keys, descending by lane (0: no entry).
 struct TopList {
   uint64_t mine = 0;  // this lane's entry
@@ -73,17 +92,22 @@ struct TopList {
   }
   // Fills an empty list with one key a lane: a bitonic sort of the wave.
   __device__ __forceinline__ void fill(uint64_t k, int lane, int top) {
-#pragma unroll
-    for (int size = 2; size <= 64; size *= 2)
-#pragma unroll
-      for (int step = size / 2; step; step /= 2) {
-        const uint64_t o = uint64_t(__shfl_xor((long long)k, step));
-        const bool larger = ((lane & step) == 0) == ((lane & size) == 0 || size == 64);  // lane keeps the larger key
-        if ((o > k) == larger) k = o;
-      }
+    sort<2>(k, lane);
     mine = k;
     last = lane_key(mine, top - 1);
     if (last) floor = from_ordered(uint32_t(last >> 32));
+  }
+  template <int SIZE>
+  static __device__ __forceinline__ void sort(uint64_t& k, int lane) {
+    merge<SIZE, SIZE / 2>(k, lane);
+    if constexpr (SIZE < 64) sort<SIZE * 2>(k, lane);
+  }
+  template <int SIZE, int STEP>
+  static __device__ __forceinline__ void merge(uint64_t& k, int lane) {
+    const uint64_t o = across<STEP>(k);
+    const bool larger = ((lane & STEP) == 0) == ((lane & SIZE) == 0 || SIZE == 64);  // this lane keeps the larger key
+    if ((o > k) == larger) k = o;
+    if constexpr (STEP > 1) merge<SIZE, STEP / 2>(k, lane);
   }
   // Raises the floor of a list without real values yet to one that at least `top` lanes' x
   // reach, found bit by bit over the upper half of the ordered value: the list then fills
@@ -139,16 +163,10 @@ struct Sums {
     s += o.s;
     q += o.q;
   }
+  template <int STEP = 1>
   __device__ __forceinline__ void join_wave(float c) {
-#pragma unroll
-    for (int o = 32; o; o >>= 1) {
-      Sums t;
-      t.m = __shfl_xor(m, o);
-      t.M = __shfl_xor(M, o);
-      t.s = __shfl_xor(s, o);
-      t.q = __shfl_xor(q, o);
-      join(t, c);
-    }
+    join({across<STEP>(m), across<STEP>(M), across<STEP>(s), across<STEP>(q)}, c);
+    if constexpr (STEP < 32) join_wave<STEP * 2>(c);
   }
 };
 
@@ -157,9 +175,12 @@ struct Part {
   int count, unused[3];
 };
 
-__device__ __forceinline__ int64_t target_of(const LpArgs& a, int row) {
-  return a.wide ? static_cast<const int64_t*>(a.targets)[row] : static_cast<const int32_t*>(a.targets)[row];
-}
+// A row's target (-1: none) and its logit.  Two reads that wait for one another, so they are
+// asked for early.
+struct Target {
+  int at;
+  float x;
+};
 
 template <bool BF16>
 __device__ __forceinline__ float logit(const LpArgs& a, int row, int64_t i) {
@@ -169,18 +190,23 @@ __device__ __forceinline__ float logit(const LpArgs& a, int row, int64_t i) {
 // The last rounding takes no probability above 1 and no entropy below 0 (NaN stays).
 __device__ __forceinline__ float at_most_0(float v) { return v > 0.f ? 0.f : v; }
 
-// Writes a row's results from its sums and its top list (one wave).
 template <bool BF16>
+__device__ __forceinline__ Target target_of(const LpArgs& a, int row) {
+  const int64_t t = a.wide ? static_cast<const int64_t*>(a.targets)[row] : static_cast<const int32_t*>(a.targets)[row];
+  Target r = {t >= 0 && t < a.v ? int(t) : -1, 0.f};
+  if (r.at >= 0) r.x = logit<BF16>(a, row, r.at);
+  return r;
+}
+
+// Writes a row's results from its sums and its top list (one wave).
 __device__ __forceinline__ void finish(const LpArgs& a, int row, const Sums& sums, int count, const TopList& list,
-                                       float c, int lane) {
+                                       Target target, float c, int lane) {
   const float s = sums.s;
-  const int64_t target = target_of(a, row);
-  const bool valid = target >= 0 && target < a.v;
+  const bool valid = target.at >= 0;
   const bool none = s == 0.f, bad = s != s;  // nothing but -infinity; a NaN or +infinity
   const float log_s = logf(s), inf = __builtin_inff();
   if (lane == 0) {
-    const float xt = valid ? logit<BF16>(a, row, target) : 0.f;
-    a.logprob[row] = !valid ? 0.f : none ? -inf : at_most_0(sums.natural(xt, c, a.inv_temperature) - log_s);
+    a.logprob[row] = !valid ? 0.f : none ? -inf : at_most_0(sums.natural(target.x, c, a.inv_temperature) - log_s);
     a.entropy[row] = none ? 0.f : -at_most_0(kLn2 * (sums.q / s) - log_s);
     a.rank[row] = valid && !bad ? count + 1 : 0;
   }
@@ -243,13 +269,9 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
   Sums sums = {0.f, Sums::kNone, 0.f, 0.f};
   int count = 0;
   TopList list;
+  Target target = {-1, 0.f};
   if (part < a.parts) {  // else the last workgroup's spare waves, with nothing to add
     const int begin = min(part * a.per, a.v), end = min(begin + a.per, a.v);
-    const int64_t tg = target_of(a, row);
-    const int target = tg >= 0 && tg < a.v ? int(tg) : -1;
-    const float xt = target >= 0 ? logit<BF16>(a, row, target) : __builtin_inff();
-    // x > xt as x >= the next value above it
-    const float above = target >= 0 ? from_ordered(ordered(xt) + 1) : __builtin_inff();
     int tied = 0;
     constexpr int U = 4, kStep = 64 * 8 * U;
     Raw<BF16> next[U];
@@ -258,6 +280,10 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
       for (int u = 0; u < U; ++u) next[u].load(base, i0 + (u * 64 + lane) * 8, end);
     };
     load(begin);
+    target = target_of<BF16>(a, row);
+    const float xt = target.at >= 0 ? target.x : __builtin_inff();
+    // x > xt as x >= the next value above it
+    const float above = target.at >= 0 ? from_ordered(ordered(xt) + 1) : __builtin_inff();
     for (int i0 = begin; i0 < end; i0 += kStep) {
       Raw<BF16> raw[U];
 #pragma unroll
@@ -334,12 +360,12 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
         sums.s += ps;
         sums.q += pq;
         // a part ends on a vector; what is read past it counts for nothing
-        const float bound = i >= end ? __builtin_inff() : i + 8 <= target ? xt : above;
+        const float bound = i >= end ? __builtin_inff() : i + 8 <= target.at ? xt : above;
 #pragma unroll
         for (int e = 0; e < 8; ++e) count += __popcll(__ballot(x[e] >= bound));
-        if (target >= i && target < i + 8) {  // the vector that holds the target: equal logits before it
+        if (target.at >= i && target.at < i + 8) {  // the vector that holds the target: equal logits before it
 #pragma unroll
-          for (int e = 0; e < 8; ++e) tied += i + e < target && x[e] == xt;
+          for (int e = 0; e < 8; ++e) tied += i + e < target.at && x[e] == xt;
         }
         if constexpr (TOP) {
           if (!listed && __ballot(best[u] >= list.gate && i < end)) {
@@ -363,7 +389,7 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
       if (lane == 0) a.part[at] = {sums, count, {}};
       if (TOP && lane < a.top) a.keys[at * a.top + lane] = list.mine;
     } else if (a.parts == 1) {
-      finish<BF16>(a, row, sums, count, list, c, lane);
+      finish(a, row, sums, count, list, target, c, lane);
     }
   }
   if (a.parts == 1 || a.parts > kWaves) return;
@@ -376,7 +402,7 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
     count += parts[wave + w].count;
     if constexpr (TOP) list.offer(lane < a.top ? lists[wave + w][lane] : 0, lane, a.top);
   }
-  finish<BF16>(a, row, sums, count, list, c, lane);
+  finish(a, row, sums, count, list, target, c, lane);
 }
 
 constexpr int kMaxParts = 64;
@@ -386,16 +412,17 @@ template <bool BF16>
 __global__ __launch_bounds__(kThreads) void merge_kernel(LpArgs a) {
   __shared__ uint64_t keys[kMaxParts * MBQ_MAX_TOP];
   const int row = blockIdx.x, lane = threadIdx.x & 63, all = a.parts * a.top;
-  for (int i = threadIdx.x; i < all; i += kThreads) keys[i] = a.keys[int64_t(row) * all + i];
-  __syncthreads();
-  if (threadIdx.x >= 64) return;
-  const float c = a.inv_temperature * 1.4426950408889634f;
+  const Target target = target_of<BF16>(a, row);
   Sums sums = {0.f, Sums::kNone, 0.f, 0.f};
   int count = 0;
   if (lane < a.parts) {
     sums = a.part[int64_t(row) * a.parts + lane].sums;
     count = a.part[int64_t(row) * a.parts + lane].count;
   }
+  for (int i = threadIdx.x; i < all; i += kThreads) keys[i] = a.keys[int64_t(row) * all + i];
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  const float c = a.inv_temperature * 1.4426950408889634f;
   sums.join_wave(c);
 #pragma unroll
   for (int o = 32; o; o >>= 1) count += __shfl_xor(count, o);
@@ -406,7 +433,7 @@ __global__ __launch_bounds__(kThreads) void merge_kernel(LpArgs a) {
     else if (__ballot(k > list.last)) list.offer(k, lane, a.top);
     else break;
   }
-  finish<BF16>(a, row, sums, count, list, c, lane);
+  finish(a, row, sums, count, list, target, c, lane);
 }
 
 // Parts of a row: at least 4096 waves (four a SIMD), each with at least one full step of its
