@@ -564,7 +564,7 @@ mbq_status mbq_block_norm(const mbq_block_norm_args* args, hipStream_t stream);
 #define MBQ_MAX_TOP 64
 
 /* Host only: bytes of device workspace mbq_token_logprobs needs (0 where one workgroup
- * holds a row).  Depends only on t, v and top. */
+ * holds whole rows).  Depends only on t, v and top. */
 mbq_status mbq_token_logprobs_workspace(int32_t t, int32_t v, int32_t top, size_t* bytes);
 
 /*
@@ -579,8 +579,8 @@ mbq_status mbq_token_logprobs_workspace(int32_t t, int32_t v, int32_t top, size_
  * A target outside [0, v) gives logprob 0 and rank 0 (a padded position).  A row of nothing
  * but -infinity gives log probabilities of -infinity and entropy 0.  A row that holds a
  * NaN or +infinity has no distribution: its floats are NaN, its rank 0, its top_ids -1.
- * Sums are float32 about a running maximum, in a fixed order.  inv_temperature > 0 and
- * finite (MBQ_ERR_RANGE).  workspace: 256-byte aligned scratch.
+ * Sums are float32 about a running maximum, in a fixed order.  0 < inv_temperature <=
+ * 1e30 (MBQ_ERR_RANGE).  workspace: 256-byte aligned scratch.
  */
 mbq_status mbq_token_logprobs(int32_t t, int32_t v, const void* logits, mbq_dtype dtype, int64_t ld,
                               const void* targets, int32_t target_bits, float inv_temperature, int32_t top,

@@ -154,7 +154,7 @@ def test_token_logprobs_refuses():
     assert call(t=-1) == SHAPE and call(v=0) == SHAPE and call(v=(1 << 28) + 1) == SHAPE and call(ld=499) == SHAPE
     assert call(top=-1) == SHAPE and call(top=65) == SHAPE and call(v=2, ld=2) == SHAPE
     assert call(dt=E4M3) == ARG and call(dt=8) == ARG and call(bits=16) == ARG
-    for it in (0.0, -1.0, float("nan"), float("inf")):
+    for it in (0.0, -1.0, 1e31, float("nan"), float("inf")):
         assert call(it=it) == RANGE
     for name in ("x", "tg", "lp", "en", "rk", "ids", "best"):
         assert call(**{name: None}) == ARG

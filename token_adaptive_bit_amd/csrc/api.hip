@@ -602,7 +602,7 @@ mbq_status mbq_token_logprobs(int32_t t, int32_t v, const void* logits, mbq_dtyp
   const mbq_status st = logprobs_shape(t, v, top);
   if (st != MBQ_OK) return st;
   if (!valid_dtype(dtype) || (target_bits != 32 && target_bits != 64)) return MBQ_ERR_ARG;
-  if (!(inv_temperature > 0.f) || !std::isfinite(inv_temperature)) return MBQ_ERR_RANGE;
+  if (!(inv_temperature > 0.f) || !(inv_temperature <= 1e30f)) return MBQ_ERR_RANGE;
   if (t == 0) return MBQ_OK;
   if (ld < v) return MBQ_ERR_SHAPE;
   if (!logits || !targets || !logprob || !entropy || !rank || (top > 0 && (!top_ids || !top_logprobs))) return MBQ_ERR_ARG;

@@ -15,7 +15,12 @@ constexpr int kMaxWaves = 16;
 // Sum over the threads that share a row (16, 32 or whole waves), the same in all of them;
 // `slot` alternates between consecutive sums so that one barrier a sum is enough.
 __device__ __forceinline__ float row_sum(float v, float (*red)[kMaxWaves], int slot, int threads) {
-  for (int o = min(threads, 64) / 2; o; o >>= 1) v += __shfl_xor(v, o);
+  v += across<8>(v);
+  v += across<4>(v);
+  v += across<2>(v);
+  v += across<1>(v);
+  if (threads > 16) v += across<16>(v);
+  if (threads > 32) v += across<32>(v);
   if (threads <= 64) return v;
   const int wave = threadIdx.x >> 6, waves = threads >> 6;
   if ((threadIdx.x & 63) == 0) red[slot][wave] = v;
@@ -35,9 +40,9 @@ __device__ __forceinline__ void load_or(const float* p, int64_t i, int64_t k, fl
   }
 }
 
-// y = a residual + b gate z for eight elements of one row.
-template <bool XB, bool RB>
-__device__ __forceinline__ void join_residual(const Args& a, int64_t row, int64_t i, float (&v)[8]) {
+// y = a residual + b gate z for eight elements of one row; r: the residual's.
+template <bool XB>
+__device__ __forceinline__ void join_residual(const Args& a, int64_t row, int64_t i, const float (&r)[8], float (&v)[8]) {
   if (a.gate_kind == MBQ_GATE_CHANNEL) {
     float g[8];
     load8<false>(a.gate, i, a.k, g);
@@ -53,15 +58,8 @@ __device__ __forceinline__ void join_residual(const Args& a, int64_t row, int64_
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] *= g[e];
   }
-  if (a.residual) {
-    float r[8];
-    load8<RB>(static_cast<const uint8_t*>(a.residual) + row * a.ldr * (RB ? 2 : 4), i, a.k, r);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = fmaf(a.gate_scale, v[e], a.residual_scale * r[e]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= a.gate_scale;
-  }
+  for (int e = 0; e < 8; ++e) v[e] = fmaf(a.gate_scale, v[e], a.residual_scale * r[e]);
 }
 
 // Writes eight elements of h; m: whether this 16-lane group lies inside the row at all.
@@ -78,7 +76,7 @@ __device__ __forceinline__ void store_h(const Args& a, int64_t row, int64_t i, c
 
 // blockDim.x threads a row, V groups of 8 elements a thread (element 8 (tid + threads j) + e),
 // blockDim.y rows a workgroup.
-template <int V, bool XB, bool RB, int HT>
+template <int V, bool EARLY, bool XB, bool RB, int HT>
 __global__ __launch_bounds__(1024) void norm_kernel(Args a) {
   __shared__ float reds[2][2][kMaxWaves];  // of at most two rows of several waves
   const int tid = threadIdx.x, threads = blockDim.x;
@@ -89,13 +87,30 @@ __global__ __launch_bounds__(1024) void norm_kernel(Args a) {
   const int k = a.k;
   const float inv_k = 1.f / float(a.k);
   const bool layer = a.kind == MBQ_NORM_LAYER;
-  float v[V][8];
+  // EARLY: everything a row needs is asked for at once, so that the wait for memory is spent
+  // once.  With few rows that wait is the time (one row of 5120: 3.6 us from 4.7); with many
+  // the registers it takes cost more (13107 x 5120, both norms and a gate: 4.1 TB/s from 4.6).
+  Raw8<XB> rx[V];
+  Raw8<RB> rr[V];
+  Raw8<false> post_w[V], pre_w[V];
 #pragma unroll
   for (int j = 0; j < V; ++j)
-    load8<XB>(static_cast<const uint8_t*>(a.x) + row * a.ldx * (XB ? 2 : 4), 8 * (tid + threads * j), k, v[j]);
+    rx[j].load(static_cast<const uint8_t*>(a.x) + row * a.ldx * (XB ? 2 : 4), 8 * (tid + threads * j), k);
+  if (EARLY) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      const int i = 8 * (tid + threads * j);
+      if (a.post_weight) post_w[j].load(a.post_weight, i, k);
+      if (a.residual) rr[j].load(static_cast<const uint8_t*>(a.residual) + row * a.ldr * (RB ? 2 : 4), i, k);
+      if (a.pre_weight) pre_w[j].load(a.pre_weight, i, k);
+    }
+  }
+  float v[V][8];
+#pragma unroll
+  for (int j = 0; j < V; ++j) rx[j].get(v[j]);
 
   // Elements past the row are 0 before and after (their weights and biases read as 0).
-  auto norm = [&](const float* weight, const float* bias) {
+  auto norm = [&](const float* weight, const Raw8<false> (&early)[V], const float* bias) {
     if (layer) {
       float s = 0.f;
 #pragma unroll
@@ -127,7 +142,8 @@ __global__ __launch_bounds__(1024) void norm_kernel(Args a) {
       for (int e = 0; e < 8; ++e) v[j][e] *= rstd;
       if (weight) {
         float w[8];
-        load8<false>(weight, i, k, w);
+        if constexpr (EARLY) early[j].get(w);
+        else load8<false>(weight, i, k, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) v[j][e] *= w[e];
       }
@@ -140,17 +156,20 @@ __global__ __launch_bounds__(1024) void norm_kernel(Args a) {
     }
   };
 
-  if (a.post) norm(a.post_weight, a.post_bias);
+  if (a.post) norm(a.post_weight, post_w, a.post_bias);
 #pragma unroll
   for (int j = 0; j < V; ++j) {
     const int i = 8 * (tid + threads * j);
     if (i < k) {
-      join_residual<XB, RB>(a, row, i, v[j]);
+      float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      if (EARLY && a.residual) rr[j].get(r);
+      else if (a.residual) load8<RB>(static_cast<const uint8_t*>(a.residual) + row * a.ldr * (RB ? 2 : 4), i, k, r);
+      join_residual<XB>(a, row, i, r, v[j]);
       if (a.y && !spare) store8<RB>(static_cast<uint8_t*>(a.y) + row * a.ldy * (RB ? 2 : 4), i, k, v[j]);
     }
   }
   if (threads > 64 && a.post) __syncthreads();  // the first norm's sums are read before the second's are written
-  norm(a.pre_weight, a.pre_bias);
+  norm(a.pre_weight, pre_w, a.pre_bias);
   if (spare) return;
 #pragma unroll
   for (int j = 0; j < V; ++j) store_h<HT>(a, row, 8 * (tid + threads * j), v[j]);
@@ -182,7 +201,9 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(Args a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = fmaf((v[e] - mean_x) * rstd_x, w[e], b[e]);
     }
-    join_residual<XB, RB>(a, row, i, v);
+    float r[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (a.residual) load8<RB>(static_cast<const uint8_t*>(a.residual) + row * a.ldr * (RB ? 2 : 4), i, k, r);
+    join_residual<XB>(a, row, i, r, v);
   };
   auto stats = [&](auto get, float& mean, float& rstd) {
     mean = 0.f;
@@ -247,11 +268,18 @@ hipError_t launch(const Args& a, hipStream_t s) {
   const int threads = a.k <= 128 ? 16 : a.k <= 256 ? 32 : 64 * ((units + v - 1) / v);
   const int rows = threads <= 64 ? 256 / threads : threads == 128 ? 2 : 1;
   const dim3 grid((uint32_t(a.t) + rows - 1) / rows), block(threads, rows);
+  const bool early = int64_t(a.t) * threads <= 64 * 4096;  // at most four waves a SIMD in all
   switch (v) {
-    case 1: norm_kernel<1, XB, RB, HT><<<grid, block, 0, s>>>(a); break;
-    case 2: norm_kernel<2, XB, RB, HT><<<grid, block, 0, s>>>(a); break;
-    case 3: norm_kernel<3, XB, RB, HT><<<grid, block, 0, s>>>(a); break;
-    default: norm_kernel<4, XB, RB, HT><<<grid, block, 0, s>>>(a); break;
+    case 1:
+      if (early) norm_kernel<1, true, XB, RB, HT><<<grid, block, 0, s>>>(a);
+      else norm_kernel<1, false, XB, RB, HT><<<grid, block, 0, s>>>(a);
+      break;
+    case 2:
+      if (early) norm_kernel<2, true, XB, RB, HT><<<grid, block, 0, s>>>(a);
+      else norm_kernel<2, false, XB, RB, HT><<<grid, block, 0, s>>>(a);
+      break;
+    case 3: norm_kernel<3, false, XB, RB, HT><<<grid, block, 0, s>>>(a); break;
+    default: norm_kernel<4, false, XB, RB, HT><<<grid, block, 0, s>>>(a); break;
   }
   return hipGetLastError();
 }

@@ -78,6 +78,64 @@ __device__ __forceinline__ void store8(void* row, int64_t i, int64_t n, const fl
   }
 }
 
+// Eight elements of a row as they lie in memory, to be asked for early.
+template <bool BF16>
+struct Raw8 {
+  u32x4_t w[BF16 ? 1 : 2];
+  __device__ __forceinline__ void load(const void* row_, int i, int end, float missing = 0.f) {  // from i; `missing` from end on
+    const uint8_t* row = static_cast<const uint8_t*>(row_);
+    if (i + 8 <= end) {
+      const uint8_t* p = row + int64_t(i) * (BF16 ? 2 : 4);
+#pragma unroll
+      for (int h = 0; h < (BF16 ? 1 : 2); ++h) w[h] = *reinterpret_cast<const u32x4_a2*>(p + 16 * h);
+    } else {
+      float x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = i + e < end ? load_x(row, size_t(i + e), BF16) : missing;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if constexpr (BF16) {
+          w[0][e] = __float_as_uint(x[2 * e]) >> 16 | (__float_as_uint(x[2 * e + 1]) & 0xFFFF0000u);
+        } else {
+          w[0][e] = __float_as_uint(x[e]);
+          w[BF16 ? 0 : 1][e] = __float_as_uint(x[4 + e]);
+        }
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (BF16) {
+        x[2 * e] = __uint_as_float(w[0][e] << 16);
+        x[2 * e + 1] = __uint_as_float(w[0][e] & 0xFFFF0000u);
+      } else {
+        x[e] = __uint_as_float(w[0][e]);
+        x[4 + e] = __uint_as_float(w[BF16 ? 0 : 1][e]);
+      }
+    }
+  }
+};
+
+// The value of lane ^ STEP: by register moves inside 16 lanes, through LDS beyond.
+template <int STEP>
+__device__ __forceinline__ uint32_t across(uint32_t v) {
+  if constexpr (STEP == 1) return __builtin_amdgcn_update_dpp(0, int(v), 0xB1, 0xF, 0xF, true);   // quad 1 0 3 2
+  if constexpr (STEP == 2) return __builtin_amdgcn_update_dpp(0, int(v), 0x4E, 0xF, 0xF, true);   // quad 2 3 0 1
+  if constexpr (STEP == 4) {                                                                      // ^ 7, then ^ 3
+    const int m = __builtin_amdgcn_update_dpp(0, int(v), 0x141, 0xF, 0xF, true);                  // row_half_mirror
+    return __builtin_amdgcn_update_dpp(0, m, 0x1B, 0xF, 0xF, true);                               // quad 3 2 1 0
+  }
+  if constexpr (STEP == 8) return __builtin_amdgcn_update_dpp(0, int(v), 0x128, 0xF, 0xF, true);  // row_ror 8
+  return uint32_t(__shfl_xor(int(v), STEP));
+}
+template <int STEP>
+__device__ __forceinline__ float across(float v) { return __uint_as_float(across<STEP>(__float_as_uint(v))); }
+template <int STEP>
+__device__ __forceinline__ uint64_t across(uint64_t v) {
+  return uint64_t(across<STEP>(uint32_t(v >> 32))) << 32 | across<STEP>(uint32_t(v));
+}
+
 // Largest of the 16 lanes of a row, in all of them.
 __device__ __forceinline__ uint32_t max16(uint32_t m) {
   m = max(m, uint32_t(__builtin_amdgcn_update_dpp(0, int(m), 0x128, 0xF, 0xF, true)));  // row_ror 8

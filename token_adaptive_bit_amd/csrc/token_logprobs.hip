@@ -42,25 +42,6 @@ __device__ __forceinline__ uint64_t lane_key(uint64_t k, int lane) {
   return uint64_t(hi) << 32 | lo;
 }
 
-// The value of lane ^ STEP: by register moves inside 16 lanes, through LDS beyond.
-template <int STEP>
-__device__ __forceinline__ uint32_t across(uint32_t v) {
-  if constexpr (STEP == 1) return __builtin_amdgcn_update_dpp(0, int(v), 0xB1, 0xF, 0xF, true);   // quad 1 0 3 2
-  if constexpr (STEP == 2) return __builtin_amdgcn_update_dpp(0, int(v), 0x4E, 0xF, 0xF, true);   // quad 2 3 0 1
-  if constexpr (STEP == 4) {                                                                      // ^ 7, then ^ 3
-    const int m = __builtin_amdgcn_update_dpp(0, int(v), 0x141, 0xF, 0xF, true);                  // row_half_mirror
-    return __builtin_amdgcn_update_dpp(0, m, 0x1B, 0xF, 0xF, true);                               // quad 3 2 1 0
-  }
-  if constexpr (STEP == 8) return __builtin_amdgcn_update_dpp(0, int(v), 0x128, 0xF, 0xF, true);  // row_ror 8
-  return uint32_t(__shfl_xor(int(v), STEP));
-}
-template <int STEP>
-__device__ __forceinline__ float across(float v) { return __uint_as_float(across<STEP>(__float_as_uint(v))); }
-template <int STEP>
-__device__ __forceinline__ uint64_t across(uint64_t v) {
-  return uint64_t(across<STEP>(uint32_t(v >> 32))) << 32 | across<STEP>(uint32_t(v));
-}
-
 // The wave's best 64 keys, descending by lane (0: no entry).
 struct TopList {
   uint64_t mine = 0;  // this lane's entry
@@ -217,44 +198,6 @@ __device__ __forceinline__ void finish(const LpArgs& a, int row, const Sums& sum
   }
 }
 
-// Eight logits as they lie in memory.
-template <bool BF16>
-struct Raw {
-  u32x4_t w[BF16 ? 1 : 2];
-  __device__ __forceinline__ void load(const uint8_t* row, int i, int end) {  // from i; -infinity from end on
-    if (i + 8 <= end) {
-      const uint8_t* p = row + int64_t(i) * (BF16 ? 2 : 4);
-#pragma unroll
-      for (int h = 0; h < (BF16 ? 1 : 2); ++h) w[h] = *reinterpret_cast<const u32x4_a2*>(p + 16 * h);
-    } else {
-      float x[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = i + e < end ? load_x(row, size_t(i + e), BF16) : -__builtin_inff();
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if constexpr (BF16) {
-          w[0][e] = __float_as_uint(x[2 * e]) >> 16 | (__float_as_uint(x[2 * e + 1]) & 0xFFFF0000u);
-        } else {
-          w[0][e] = __float_as_uint(x[e]);
-          w[BF16 ? 0 : 1][e] = __float_as_uint(x[4 + e]);
-        }
-      }
-    }
-  }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (BF16) {
-        x[2 * e] = __uint_as_float(w[0][e] << 16);
-        x[2 * e + 1] = __uint_as_float(w[0][e] & 0xFFFF0000u);
-      } else {
-        x[e] = __uint_as_float(w[0][e]);
-        x[4 + e] = __uint_as_float(w[BF16 ? 0 : 1][e]);
-      }
-    }
-  }
-};
-
 // One part of a row a wave.  The waves of a row meet in LDS when they fit one workgroup
 // (1, 2 or 4 parts), else their results go to memory for the merging launch.
 template <bool BF16, bool TOP>
@@ -274,10 +217,10 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
     const int begin = min(part * a.per, a.v), end = min(begin + a.per, a.v);
     int tied = 0;
     constexpr int U = 4, kStep = 64 * 8 * U;
-    Raw<BF16> next[U];
+    Raw8<BF16> next[U];
     auto load = [&](int i0) __attribute__((always_inline)) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) next[u].load(base, i0 + (u * 64 + lane) * 8, end);
+      for (int u = 0; u < U; ++u) next[u].load(base, i0 + (u * 64 + lane) * 8, end, -__builtin_inff());
     };
     load(begin);
     target = target_of<BF16>(a, row);
@@ -285,7 +228,7 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
     // x > xt as x >= the next value above it
     const float above = target.at >= 0 ? from_ordered(ordered(xt) + 1) : __builtin_inff();
     for (int i0 = begin; i0 < end; i0 += kStep) {
-      Raw<BF16> raw[U];
+      Raw8<BF16> raw[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) raw[u] = next[u];
       if (i0 + kStep < end) load(i0 + kStep);
