@@ -122,6 +122,13 @@ def test_rows(api, t, k):
         check(api, t, k, quantized=True)
 
 
+@pytest.mark.parametrize("t,k", [(5000, 100), (5001, 200), (4200, 500), (3000, 700), (2000, 1500), (1203, 2100), (700, 6000), (300, 18944)])
+@pytest.mark.parametrize("quantized", [False, True])
+def test_many_rows(api, t, k, quantized):
+    """Enough rows for the form that keeps fewer registers."""
+    check(api, t, k, xd=BF, rd=BF, hd=BF, kind="layer", gate="channel", bias=True, quantized=quantized)
+
+
 def test_large_mean(api):
     """Layer norm where the mean is 1000 times the deviation: the variance is taken about it."""
     for k in (300, 4096, 20000):

@@ -127,6 +127,15 @@ def test_pack_reports_non_finite(api):
         status = torch.zeros(1, dtype=torch.int32, device=DEV)
         api.fp8_pack(w, status=status)
         assert int(status) == 1
+    for code in (0x7F, 0xFF):
+        for at in ((0, 0), (39, 199), (20, 63), (7, 190)):
+            q = torch.zeros(40, 200, dtype=torch.uint8, device=DEV)
+            q[:] = 0x7E                                      # the largest value is no NaN
+            ok, status = torch.zeros(1, dtype=torch.int32, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+            api.fp8_pack(q.view(F8), torch.ones(1, 2, device=DEV), status=ok)
+            q[at] = code
+            api.fp8_pack(q.view(F8), torch.ones(1, 2, device=DEV), status=status)
+            assert int(ok) == 0 and int(status) == 1
 
 
 SHAPES = [  # t, n, k: one token to several tiles, every remainder that a tile can have

@@ -263,12 +263,12 @@ hipError_t launch(const Args& a, hipStream_t s) {
     norm_long_kernel<XB, RB, HT><<<uint32_t(a.t), 1024, 0, s>>>(a);
     return hipGetLastError();
   }
-  int v = units == 1 ? 1 : units == 3 || units == 5 ? 3 : 2;
+  const bool early = a.t <= 4096 / units;  // at most four waves a SIMD in all
+  int v = units == 1 ? 1 : !early && (units == 3 || units == 5) ? 3 : 2;
   while ((units + v - 1) / v > kMaxWaves) ++v;
   const int threads = a.k <= 128 ? 16 : a.k <= 256 ? 32 : 64 * ((units + v - 1) / v);
   const int rows = threads <= 64 ? 256 / threads : threads == 128 ? 2 : 1;
   const dim3 grid((uint32_t(a.t) + rows - 1) / rows), block(threads, rows);
-  const bool early = int64_t(a.t) * threads <= 64 * 4096;  // at most four waves a SIMD in all
   switch (v) {
     case 1:
       if (early) norm_kernel<1, true, XB, RB, HT><<<grid, block, 0, s>>>(a);

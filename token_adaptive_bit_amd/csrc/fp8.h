@@ -9,6 +9,7 @@ typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 // Loads and stores of rows at any element alignment (gfx950 takes wide accesses at any
 // address; the attribute keeps the compiler from assuming more).
+typedef uint32_t u32x4_a1 __attribute__((__vector_size__(16), aligned(1)));
 typedef uint32_t u32x4_a2 __attribute__((__vector_size__(16), aligned(2)));
 typedef uint32_t u32x2_a2 __attribute__((__vector_size__(8), aligned(2)));
 typedef float f32x4_a4 __attribute__((__vector_size__(16), aligned(4)));

@@ -43,18 +43,26 @@ __global__ __launch_bounds__(256) void pack_fp8_kernel(mbq_fp8_desc d, int32_t p
   uint32_t bad = 0;
   float s;
   if constexpr (WT == 2) {
-    const uint8_t* p = reinterpret_cast<const uint8_t*>(w) + row * d.k;
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(w) + row * d.k + col0;
+    if (row < d.n && col0 + 64 <= d.k) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      uint32_t c = 0;
+      for (int i = 0; i < 4; ++i) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_a1*>(p + 16 * i);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int64_t col = col0 + 4 * i + e;
-        const uint32_t b = row < d.n && col < d.k ? p[col] : 0u;
-        bad |= (b & 0x7Fu) == 0x7Fu;
-        c |= b << (8 * e);
+        for (int e = 0; e < 4; ++e) codes[4 * i + e] = v[e];
       }
-      codes[i] = c;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        codes[i] = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (row < d.n && col0 + 4 * i + e < d.k) codes[i] |= uint32_t(p[4 * i + e]) << (8 * e);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {  // a byte of 0x7F or 0xFF: its low seven bits carry into the eighth when 1 is added
+      bad |= ((codes[i] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
     }
     s = w_scale[int64_t(nb) * d.k_blocks + kb];
     bad |= (__float_as_uint(s) & 0x7F800000u) == 0x7F800000u;
