@@ -80,7 +80,7 @@ int main() {
                             nullptr, 0, nullptr) == MBQ_ERR_ARG);
   EXPECT(mbq_token_logprobs(2, 500, fake(0), MBQ_BF16, 500, fake(0), 64, -1.f, 0, ffake(0), ffake(0), ifake(0), nullptr, nullptr,
                             nullptr, 0, nullptr) == MBQ_ERR_RANGE);
-  EXPECT(mbq_token_logprobs(1, 131072, fake(0), MBQ_F32, 131072, fake(0), 64, 1.f, 0, ffake(0), ffake(0), ifake(0), nullptr,
+  EXPECT(mbq_token_logprobs(1, 1 << 19, fake(0), MBQ_F32, 1 << 19, fake(0), 64, 1.f, 0, ffake(0), ffake(0), ifake(0), nullptr,
                             nullptr, nullptr, 0, nullptr) == MBQ_ERR_WORKSPACE);
   std::printf(failed ? "failed\n" : "ok\n");
   return failed;

@@ -160,9 +160,9 @@ def test_token_logprobs_refuses():
         assert call(**{name: None}) == ARG
         assert call(**{name: P(FAKE + 1)}) == ARG
     n = ctypes.c_size_t(0)
-    assert L.mbq_token_logprobs_workspace(1, 1 << 17, 20, ctypes.byref(n)) == OK and n.value > 0
+    assert L.mbq_token_logprobs_workspace(1, 1 << 19, 20, ctypes.byref(n)) == OK and n.value > 0
     for ws, wsb in ((None, 0), (f, n.value - 1), (P(FAKE + 16), n.value)):
-        assert call(t=1, v=1 << 17, ld=1 << 17, top=20, ws=ws, wsb=wsb) == WS
+        assert call(t=1, v=1 << 19, ld=1 << 19, top=20, ws=ws, wsb=wsb) == WS
     assert L.mbq_token_logprobs_workspace(1, 10, 11, ctypes.byref(n)) == SHAPE
     assert L.mbq_token_logprobs_workspace(1, 10, 1, None) == ARG
     assert call(t=0, x=None, tg=None, lp=None, en=None, rk=None, ids=None, best=None, ws=None, wsb=0) == OK

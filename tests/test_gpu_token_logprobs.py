@@ -51,8 +51,8 @@ def logits(rng, t, v, dt, spread=2.5):
     return torch.from_numpy(z).to(DEV, dt)
 
 
-@pytest.mark.parametrize("t,v", [(1, 1), (1, 2), (3, 7), (2, 8), (5, 63), (4, 513), (1, 2048), (2, 8191), (1, 8192), (3, 8193),
-                                 (1, 50021), (70, 1000), (2, 131072), (1, 262144), (1100, 300), (1030, 9000)])
+@pytest.mark.parametrize("t,v", [(1, 1), (1, 2), (3, 7), (2, 8), (5, 63), (4, 513), (1, 2048), (2, 8191), (1, 8192), (3, 8193), (5, 32768), (4, 32769), (256, 11000), (257, 11000),
+                                 (1, 50021), (70, 1000), (2, 131072), (1, 262144), (2, 300000), (1, 700001), (700, 12000), (1100, 300), (1030, 9000), (1500, 5000)])
 @pytest.mark.parametrize("dt", [BF, F32])
 def test_sizes(api, t, v, dt):
     print(f"logprobs t={t} v={v} {dt}", flush=True)
@@ -61,7 +61,7 @@ def test_sizes(api, t, v, dt):
         check(api, logits(rng, t, v, dt), rng.integers(0, v, t), top, float(rng.choice([1.0, 1.25, 0.5])))
 
 
-@pytest.mark.parametrize("v", [5, 700, 9001, 70000])
+@pytest.mark.parametrize("v", [5, 700, 9001, 70000, 270000])
 def test_ties(api, v):
     """Equal logits: ranks and alternatives by ascending token, all equal among them, and +0 with -0."""
     rng = np.random.default_rng(v)
@@ -150,12 +150,12 @@ def test_long_buffer_offsets(api):
 def test_empty_batch_stream_and_workspace(api):
     r = api.token_logprobs(torch.empty(0, 50, device=DEV), torch.empty(0, dtype=torch.int64, device=DEV), top=2)
     assert r.logprob.shape == (0,) and r.top_ids.shape == (0, 2)
-    z, tg = torch.randn(3, 60000, device=DEV), torch.tensor([1, 2, 3], device=DEV)
+    z, tg = torch.randn(3, 300000, device=DEV), torch.tensor([1, 2, 3], device=DEV)
     want = api.token_logprobs(z, tg, top=9)
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
     with torch.cuda.stream(s):
-        ws = torch.empty(max(1, api.token_logprobs_workspace(3, 60000, 9)), dtype=torch.uint8, device=DEV)
+        ws = torch.empty(max(1, api.token_logprobs_workspace(3, 300000, 9)), dtype=torch.uint8, device=DEV)
         got = [api.token_logprobs(z, tg, top=9, workspace=ws) for _ in range(3)]
     s.synchronize()
     for g in got:
@@ -163,15 +163,15 @@ def test_empty_batch_stream_and_workspace(api):
 
 
 def test_graph_replays(api):
-    z, tg = torch.randn(2, 40000, device=DEV), torch.tensor([7, 9], device=DEV)
-    ws = torch.empty(max(1, api.token_logprobs_workspace(2, 40000, 4)), dtype=torch.uint8, device=DEV)
+    z, tg = torch.randn(2, 270000, device=DEV), torch.tensor([7, 9], device=DEV)
+    ws = torch.empty(max(1, api.token_logprobs_workspace(2, 270000, 4)), dtype=torch.uint8, device=DEV)
     api.token_logprobs(z, tg, top=4, workspace=ws)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         out = api.token_logprobs(z, tg, top=4, workspace=ws)
     for i in range(4):
-        z.copy_(torch.randn(2, 40000, device=DEV))
+        z.copy_(torch.randn(2, 270000, device=DEV))
         g.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, api.token_logprobs(z, tg, top=4)))

@@ -78,6 +78,16 @@ struct TopList {
     last = lane_key(mine, top - 1);
     if (last) floor = from_ordered(uint32_t(last >> 32));
   }
+  // Fills an empty list from one descending list of `top` entries a lane (`has`: it has one):
+  // their best, then their second ...; the first round without an entry is the last.
+  __device__ __forceinline__ void take(const uint64_t* keys, bool has, int lane, int top) {
+    fill(has ? keys[0] : 0, lane, top);
+    for (int j = 1; j < top; ++j) {
+      const uint64_t k = has ? keys[j] : 0;
+      if (!__ballot(k > last)) break;
+      offer(k, lane, top);
+    }
+  }
   template <int SIZE>
   static __device__ __forceinline__ void sort(uint64_t& k, int lane) {
     merge<SIZE, SIZE / 2>(k, lane);
@@ -150,6 +160,15 @@ struct Sums {
     if constexpr (STEP < 32) join_wave<STEP * 2>(c);
   }
 };
+
+__device__ __forceinline__ int wave_sum(int v) {
+  v += int(across<8>(uint32_t(v)));
+  v += int(across<4>(uint32_t(v)));
+  v += int(across<2>(uint32_t(v)));
+  v += int(across<1>(uint32_t(v)));
+  v += int(across<16>(uint32_t(v)));
+  return v + int(across<32>(uint32_t(v)));
+}
 
 struct Part {
   Sums sums;
@@ -324,9 +343,7 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
       }
     }
     sums.join_wave(c);
-#pragma unroll
-    for (int o = 32; o; o >>= 1) tied += __shfl_xor(tied, o);
-    count += tied;
+    count += wave_sum(tied);
     if (a.parts > kWaves) {
       const int64_t at = int64_t(row) * a.parts + part;
       if (lane == 0) a.part[at] = {sums, count, {}};
@@ -350,7 +367,7 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
 
 constexpr int kMaxParts = 64;
 
-// Joins the parts of a row (more than four), one lane each.
+// Joins the parts of a row (more than one workgroup's), one lane each.
 template <bool BF16>
 __global__ __launch_bounds__(kThreads) void merge_kernel(LpArgs a) {
   __shared__ uint64_t keys[kMaxParts * MBQ_MAX_TOP];
@@ -367,21 +384,16 @@ __global__ __launch_bounds__(kThreads) void merge_kernel(LpArgs a) {
   if (threadIdx.x >= 64) return;
   const float c = a.inv_temperature * 1.4426950408889634f;
   sums.join_wave(c);
-#pragma unroll
-  for (int o = 32; o; o >>= 1) count += __shfl_xor(count, o);
+  count = wave_sum(count);
   TopList list;
-  for (int j = 0; j < a.top; ++j) {  // the parts' best, then their second ...: descending, so the first round without an entry is the last
-    const uint64_t k = lane < a.parts ? keys[lane * a.top + j] : 0;
-    if (j == 0) list.fill(k, lane, a.top);
-    else if (__ballot(k > list.last)) list.offer(k, lane, a.top);
-    else break;
-  }
+  if (a.top) list.take(keys + (lane < a.parts ? lane : 0) * a.top, lane < a.parts, lane, a.top);
   finish(a, row, sums, count, list, target, c, lane);
 }
 
 // Parts of a row: at least 4096 waves (four a SIMD), each with at least one full step of its
-// loop.  (2048 x 128000 bfloat16, top 8: 143 us with two parts a row, 162 with one; 300 x
-// 100000, top 20: 53 with 14 parts, 59 with 4.)
+// loop.  (2048 x 128000 bfloat16, top 8: 143 us with two parts a row, 162 with one.  Sixteen
+// parts in one workgroup, which would save the second launch of a short row, put them on one
+// unit: one row of 32000, top 20, 17.2 us against 15.8, and of 131072, top 8, 29.7 against 14.)
 int parts_of(int32_t t, int32_t v) {
   const int64_t want = (4096 + int64_t(t) - 1) / std::max(t, 1), most = (int64_t(v) + 2047) / 2048;
   const int p = int(std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), kMaxParts)));
