@@ -477,9 +477,10 @@ mbq_status mbq_fp8_linear_workspace(const mbq_fp8_desc* desc, int32_t t, mbq_dty
  *   packed:  a blob of mbq_fp8_pack for `desc` (desc->gated == 0).
  *   x:       [t x k], rows ldx elements apart (ldx >= k): float32 or bfloat16, or e4m3
  *            codes (MBQ_E4M3) of mbq_fp8_quantize or mbq_block_norm with
- *   x_scale: their scales [ceil(k / 128) x t] (NULL for the other types).  Codes need
- *            k % 16 == 0, ldx % 16 == 0, ldx <= 2^24 and 16-byte alignment (MBQ_ERR_SHAPE,
- *            MBQ_ERR_ARG).
+ *   x_scale: their scales [ceil(k / 128) x t] (NULL for the other types).  Codes with
+ *            k % 16 == 0 are read in place and need ldx % 16 == 0, ldx <= 2^24 and 16-byte
+ *            alignment (MBQ_ERR_SHAPE, MBQ_ERR_ARG); for other k they are copied to the
+ *            workspace first and need none of it.
  *   y:       [t x n] row-major, float32 or bfloat16.
  *   workspace: mbq_fp8_linear_workspace() bytes, 256-byte aligned, scratch (no state is
  *            kept; calls that overlap in time must not share one).

@@ -90,8 +90,11 @@ def test_linear_refuses(gated):
     assert call(xd=E4M3) == ARG                                         # codes without scales
     assert call(xd=E4M3, xs=f, x=P(FAKE + 8)) == ARG and call(xd=E4M3, xs=f, ldx=312) == SHAPE
     _, odd = desc(100, 300, int(gated))
-    assert linear_call(odd, gated, xd=E4M3, xs=f, ldx=304) == SHAPE      # k not a multiple of 16
     n = ctypes.c_size_t(0)
+    # k not a multiple of 16: the codes' copy lives in the workspace
+    assert L.mbq_fp8_linear_workspace(ctypes.byref(odd), 4, E4M3, ctypes.byref(n)) == OK and n.value == 4 * 384
+    assert linear_call(odd, gated, xd=E4M3, xs=f, ldx=299) == SHAPE
+    assert linear_call(odd, gated, xd=E4M3, xs=f, ldx=301, x=P(FAKE + 1), wsb=n.value - 1) == WS
     # 32 tokens: codes and scales live in the workspace
     assert L.mbq_fp8_linear_workspace(ctypes.byref(d), 32, BF16, ctypes.byref(n)) == OK and n.value > 0
     for ws, wsb in ((None, 0), (f, n.value - 1), (P(FAKE + 16), n.value)):

@@ -195,6 +195,45 @@ def test_linear_on_codes(api, t, n, k):
     assert torch.equal(api.fp8_linear(p, wide.view(F8)[:, 16 : 16 + k], s), want)
 
 
+@pytest.mark.parametrize("t,n,k", [(1, 64, 7), (4, 100, 300), (16, 40, 129), (40, 256, 1001), (70, 300, 777), (260, 128, 1033)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_codes_of_odd_rows(api, t, n, k, gated):
+    """Codes with k % 16 != 0, dense and as odd rows of an odd buffer of NaN codes, and the
+    codes of a norm of that width."""
+    rng = np.random.default_rng(t + n + k)
+    x, _ = make_x(rng, t, k, "bf16")
+    w = [torch.from_numpy(make_w(rng, n, k)).to(DEV) for _ in range(2)]
+    p = api.fp8_pack_gated(*w) if gated else api.fp8_pack(w[0])
+    call = api.fp8_gated if gated else api.fp8_linear
+    q, s = api.fp8_quantize(x)
+    want = call(p, x)
+    assert torch.equal(call(p, q, s), want)
+    wide = torch.full((t, k + 33), 0x7F, dtype=torch.uint8, device=DEV)
+    wide[:, 5 : 5 + k] = q.view(torch.uint8)
+    assert torch.equal(call(p, wide.view(F8)[:, 5 : 5 + k], s), want)
+    _, hq, hs = api.block_norm(x, quantized=True)
+    ref = [D.linear(D.values_x(codes_of(hq), hs.cpu().numpy()), D.values_w(*D.quantize_weight(v.cpu().numpy()))) for v in w]
+    (g, gm), (u, um) = ref
+    if gated:
+        extra = (2.0 ** -14 + 2.0 ** -16) * (1.13 * gm * np.abs(u) + np.abs(g) * um) + 2.0 ** -18 * np.abs(g * u)
+        close(call(p, hq, hs), D.act(g, "silu") * u, np.zeros_like(gm), "bf16", extra)
+    else:
+        close(call(p, hq, hs), g, gm, "bf16")
+
+
+def test_copies_of_a_weight(api):
+    """A weight copied with all it holds stands alone: the first one may go."""
+    import copy
+    rng = np.random.default_rng(3)
+    x, _ = make_x(rng, 5, 200, "bf16")
+    p = api.fp8_pack(torch.from_numpy(make_w(rng, 70, 200)).to(DEV))
+    want = api.fp8_linear(p, x)
+    other = copy.deepcopy(p)
+    p.blob.zero_()
+    del p
+    assert torch.equal(api.fp8_linear(other, x), want)
+
+
 def test_strided_and_unaligned_activations(api):
     rng = np.random.default_rng(5)
     p = api.fp8_pack(torch.from_numpy(make_w(rng, 100, 300)).to(DEV))

@@ -580,7 +580,7 @@ class Fp8Linear:
     blob: torch.Tensor
 
     def __post_init__(self):
-        self._ref, self._addr, self._sizes = ctypes.byref(self.desc), ctypes.addressof(self.desc), {}
+        self._sizes = {}
 
     @property
     def n(self): return self.desc.n
@@ -665,7 +665,7 @@ def fp8_linear_workspace(p: Fp8Linear, t: int, x_dtype=torch.bfloat16) -> int:
 
 def _fp8_run(p, x, scale, act, out_dtype, y, workspace):
     if y is None and workspace is None and _bound(x):
-        r = _bind.fp8(p._addr, p.blob, x, scale, -1 if act is None else act, out_dtype, dev := _current_device(),
+        r = _bind.fp8(ctypes.addressof(p.desc), p.blob, x, scale, -1 if act is None else act, out_dtype, dev := _current_device(),
                       _raw_stream(dev))
         if r is not None:
             return r
@@ -685,10 +685,10 @@ def _fp8_run(p, x, scale, act, out_dtype, y, workspace):
     y_ptr, y_code = _flat(y, "y", _FLOATS, dev, (t, n)), _CODE[y.dtype]
     _ws, ws_ptr, ws_bytes = _scratch(workspace, p._workspace_bytes(t, code), x)
     if act is None:
-        check(_lib.LIB.mbq_fp8_linear(p._ref, blob.data_ptr(), t, x.data_ptr(), code, ldx, scale, y_ptr, y_code, ws_ptr,
+        check(_lib.LIB.mbq_fp8_linear(ctypes.byref(p.desc), blob.data_ptr(), t, x.data_ptr(), code, ldx, scale, y_ptr, y_code, ws_ptr,
                                       ws_bytes, _stream_of(x)), "mbq_fp8_linear")
     else:
-        check(_lib.LIB.mbq_fp8_gated(p._ref, blob.data_ptr(), t, x.data_ptr(), code, ldx, scale, act, y_ptr, y_code,
+        check(_lib.LIB.mbq_fp8_gated(ctypes.byref(p.desc), blob.data_ptr(), t, x.data_ptr(), code, ldx, scale, act, y_ptr, y_code,
                                      ws_ptr, ws_bytes, _stream_of(x)), "mbq_fp8_gated")
     return y
 

@@ -500,10 +500,11 @@ mbq_status fp8_linear(const mbq_fp8_desc* desc, int32_t gated, const void* packe
   if (!valid_rows(t) || int64_t(t) * desc->n >= (int64_t(1) << 38)) return MBQ_ERR_SHAPE;
   if (t == 0) return MBQ_OK;
   if (!packed || !x || !y || codes != (x_scale != nullptr)) return MBQ_ERR_ARG;
-  if (!aligned(packed, 256) || !aligned(x, codes ? 16 : element(x_dtype)) || !aligned(x_scale, 4) ||
+  const bool direct = codes && desc->k % 16 == 0;  // read in place, 16 bytes at a time
+  if (!aligned(packed, 256) || !aligned(x, direct ? 16 : element(x_dtype)) || !aligned(x_scale, 4) ||
       !aligned(y, element(y_dtype)))
     return MBQ_ERR_ARG;
-  if (ldx < desc->k || (codes && (desc->k % 16 != 0 || ldx % 16 != 0 || ldx > (1 << 24)))) return MBQ_ERR_SHAPE;
+  if (ldx < desc->k || (direct && (ldx % 16 != 0 || ldx > (1 << 24)))) return MBQ_ERR_SHAPE;
   const size_t need = mbq::fp8_linear_workspace(*desc, t, x_dtype);
   if (need && (!workspace || ws_bytes < need || !aligned(workspace, 256))) return MBQ_ERR_WORKSPACE;
   return launched(mbq::launch_fp8_linear(*desc, packed, t, x, x_dtype, ldx, x_scale, act, y, y_dtype == MBQ_BF16,

@@ -497,11 +497,13 @@ bool quantize_inline(const mbq_fp8_desc& d, int32_t t, mbq_dtype x_dtype) {
   return x_dtype != MBQ_E4M3 && t <= 16 && int64_t(t) * d.k_blocks <= kInlineBlocks;
 }
 
-// Workspace: the activations' codes and scales, then the partial sums of a split K.
+// Workspace: the activations' codes and scales (codes given in rows that hold no whole 16
+// bytes: only their copy), then the partial sums of a split K.
 size_t fp8_linear_workspace(const mbq_fp8_desc& d, int32_t t, mbq_dtype x_dtype) {
   size_t bytes = 0;
   if (quantize_inline(d, t, x_dtype)) return 0;
   if (x_dtype != MBQ_E4M3) bytes = codes_bytes(d, t) + align256(size_t(d.k_blocks) * t * 4);
+  else if (d.k % 16 != 0) bytes = codes_bytes(d, t);
   size_t part = 0;
   if (!streams(t, d.row_blocks / (d.gated + 1)))
     for (bool exact : {false, true}) {  // y's type is not known here
@@ -526,7 +528,14 @@ hipError_t launch_fp8_linear(const mbq_fp8_desc& d, const void* packed, int32_t 
   a.kb = d.k_blocks;
   a.rbs = d.row_blocks;
   a.nblk = (d.n + 127) / 128;
-  if (x_dtype == MBQ_E4M3) {
+  if (x_dtype == MBQ_E4M3 && d.k % 16 != 0) {
+    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + codes_bytes(d, t));
+    a.ldq = a.xlim = d.k_blocks * kFp8Block;
+    const hipError_t e = launch_fp8_pad_codes(t, d.k, x, ldx, ws, stream);
+    if (e != hipSuccess) return e;
+    a.xq = static_cast<const uint8_t*>(ws);
+    a.xs = x_scale;
+  } else if (x_dtype == MBQ_E4M3) {
     a.part = static_cast<float*>(ws);
     a.xq = static_cast<const uint8_t*>(x);
     a.ldq = ldx;

@@ -27,6 +27,26 @@ __global__ __launch_bounds__(256) void quantize_kernel(int32_t t, int32_t k, int
   }
 }
 
+// Codes whose rows hold no whole 16-byte pieces, copied to rows of whole blocks (code 0 past
+// k), from which the products copy 16 bytes at a time; 16 codes a thread.
+__global__ __launch_bounds__(256) void pad_codes_kernel(int32_t t, int32_t k, int32_t pieces, const uint8_t* __restrict__ x,
+                                                        int64_t ldx, uint8_t* __restrict__ q) {
+  const int64_t all = int64_t(t) * pieces;
+  for (int64_t p = int64_t(blockIdx.x) * 256 + threadIdx.x; p < all; p += int64_t(gridDim.x) * 256) {
+    const int64_t row = p / pieces, i = (p - row * pieces) * 16;
+    const uint8_t* src = x + row * ldx + i;
+    u32x4_t v = {0, 0, 0, 0};
+    if (i + 16 <= k) {
+      v = *reinterpret_cast<const u32x4_a1*>(src);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (i + e < k) v[e / 4] |= uint32_t(src[e]) << (8 * (e % 4));
+    }
+    *reinterpret_cast<u32x4_t*>(q + p * 16) = v;
+  }
+}
+
 // One 128 x 128 block of one weight per workgroup: thread 2 r + half holds 64 inputs of row
 // r, the block's maximum goes through LDS, and every lane of the packed tiles is written
 // (rows and inputs of the padding as code 0).
@@ -120,6 +140,14 @@ hipError_t launch_fp8_quantize(int32_t t, int32_t k, const void* x, bool x_bf16,
     if (pad) quantize_kernel<false, true><<<grid, 256, 0, stream>>>(t, k, kb, x, ldx, out, ldq, scale);
     else quantize_kernel<false, false><<<grid, 256, 0, stream>>>(t, k, kb, x, ldx, out, ldq, scale);
   }
+  return hipGetLastError();
+}
+
+hipError_t launch_fp8_pad_codes(int32_t t, int32_t k, const void* x, int64_t ldx, void* q, hipStream_t stream) {
+  if (t == 0) return hipSuccess;
+  const int32_t pieces = (k + kFp8Block - 1) / kFp8Block * (kFp8Block / 16);
+  const uint32_t grid = uint32_t(std::min<int64_t>((int64_t(t) * pieces + 255) / 256, 1 << 20));
+  pad_codes_kernel<<<grid, 256, 0, stream>>>(t, k, pieces, static_cast<const uint8_t*>(x), ldx, static_cast<uint8_t*>(q));
   return hipGetLastError();
 }
 

@@ -111,6 +111,7 @@ constexpr int kFp8Block = 128;      // inputs per scale
 constexpr int kFp8TileBytes = 2048; // 16 rows x 128 inputs, one byte each
 hipError_t launch_fp8_pack(const mbq_fp8_desc& d, int32_t part, const void* w, mbq_dtype w_dtype,
                            const float* w_scale, void* packed, int32_t* dev_status, hipStream_t stream);
+hipError_t launch_fp8_pad_codes(int32_t t, int32_t k, const void* x, int64_t ldx, void* q, hipStream_t stream);
 hipError_t launch_fp8_quantize(int32_t t, int32_t k, const void* x, bool x_bf16, int64_t ldx, void* q,
                                int64_t ldq, bool pad, float* scale, hipStream_t stream);
 // Bytes of the quantized activations (codes, then scales) the linear keeps in its workspace.
