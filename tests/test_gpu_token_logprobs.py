@@ -72,6 +72,17 @@ def test_ties(api, v):
         check(api, torch.from_numpy(z.astype(np.float32)).to(DEV, BF), [0, v - 1, v // 2, v // 3], top)
 
 
+@pytest.mark.parametrize("levels", [2, 40, 600, 20000])
+@pytest.mark.parametrize("t,v", [(3, 90), (2, 2048), (1100, 3000), (2, 9000), (1500, 7000), (1, 140000)])
+def test_long_lists(api, t, v, levels):
+    """Lists of 13 to 64 over few to many different logits: from one tie for every place to none."""
+    rng = np.random.default_rng(v + levels)
+    z = torch.from_numpy(rng.integers(0, levels, (t, v)).astype(np.float32) * np.float32(16 / levels)).to(DEV)
+    z[0, : v // 2] = NEG
+    for top in (13, 33, 64):
+        check(api, z, rng.integers(v // 2, v, t), top)
+
+
 @pytest.mark.parametrize("dt", [BF, F32])
 @pytest.mark.parametrize("v", [6, 300, 20000])
 def test_masks(api, v, dt):

@@ -48,27 +48,29 @@ struct TopList {
   uint64_t last = 0;  // entry top - 1
   float floor = -__builtin_inff();  // no value below it can enter
   float gate = -__builtin_inff();   // nor, from a vector of higher indexes, one below this
+  // More keys at once than this are absorbed, fewer offered (5, 12 and 24 measured alike).
+  static constexpr int kMany = 12;
 
   // A full list takes no equal value of a higher index: from the next vector on.
   __device__ __forceinline__ void close_vector() {
     gate = last ? from_ordered(uint32_t(last >> 32) + 1) : floor;
   }
-  __device__ __forceinline__ void insert(uint64_t k, int lane, int top) {
-    const int pos = __popcll(__ballot(mine > k));
-    const uint32_t lo = __builtin_amdgcn_update_dpp(0, int(uint32_t(mine)), 0x138, 0xF, 0xF, true);  // wave_shr 1
-    const uint32_t hi = __builtin_amdgcn_update_dpp(0, int(uint32_t(mine >> 32)), 0x138, 0xF, 0xF, true);
-    if (lane == pos) mine = k;
-    else if (lane > pos) mine = uint64_t(hi) << 32 | lo;
+  // Every lane takes the larger of its entry and of the smaller of k and the entry before it.
+  __device__ __forceinline__ void insert(uint64_t k, int top) {
+    const uint32_t lo = __builtin_amdgcn_update_dpp(-1, int(uint32_t(mine)), 0x138, 0xF, 0xF, false);  // wave_shr 1
+    const uint32_t hi = __builtin_amdgcn_update_dpp(-1, int(uint32_t(mine >> 32)), 0x138, 0xF, 0xF, false);
+    const uint64_t before = uint64_t(hi) << 32 | lo;
+    mine = max(mine, min(before, k));
     last = lane_key(mine, top - 1);
     if (last) floor = from_ordered(uint32_t(last >> 32));
   }
   // Offers one key a lane (0: none).
-  __device__ __forceinline__ void offer(uint64_t k, int lane, int top) {
+  __device__ __forceinline__ void offer(uint64_t k, int top) {
     uint64_t m = __ballot(k > last);
     while (m) {
-      insert(lane_key(k, __builtin_ctzll(m)), lane, top);
+      insert(lane_key(k, __builtin_ctzll(m)), top);
       m &= m - 1;
-      m &= __ballot(k > last);
+      if (m) m &= __ballot(k > last);
     }
   }
   // Fills an empty list with one key a lane: a bitonic sort of the wave.
@@ -78,14 +80,28 @@ struct TopList {
     last = lane_key(mine, top - 1);
     if (last) floor = from_ordered(uint32_t(last >> 32));
   }
+  // Takes in many keys at once: `back` ascends by lane.  (Top 64 with every key offered:
+  // one row of 131072 41.9 us against 20.0, 4096 x 5000 75 against 41.)
+  __device__ __forceinline__ void absorb(uint64_t back, int lane, int top) {
+    mine = max(mine, back);
+    merge<64, 32>(mine, lane);
+    last = lane_key(mine, top - 1);
+    if (last) floor = from_ordered(uint32_t(last >> 32));
+  }
+  __device__ __forceinline__ void absorb_any(uint64_t k, int lane, int top) {
+    sort<2>(k, lane);
+    absorb(__shfl(k, 63 - lane), lane, top);
+  }
   // Fills an empty list from one descending list of `top` entries a lane (`has`: it has one):
   // their best, then their second ...; the first round without an entry is the last.
   __device__ __forceinline__ void take(const uint64_t* keys, bool has, int lane, int top) {
     fill(has ? keys[0] : 0, lane, top);
     for (int j = 1; j < top; ++j) {
       const uint64_t k = has ? keys[j] : 0;
-      if (!__ballot(k > last)) break;
-      offer(k, lane, top);
+      const int in = __popcll(__ballot(k > last));
+      if (in == 0) break;
+      if (in > kMany) absorb_any(k, lane, top);
+      else offer(k, top);
     }
   }
   template <int SIZE>
@@ -100,20 +116,23 @@ struct TopList {
     if ((o > k) == larger) k = o;
     if constexpr (STEP > 1) merge<SIZE, STEP / 2>(k, lane);
   }
-  // Raises the floor of a list without real values yet to one that at least `top` lanes' x
-  // reach, found bit by bit over the upper half of the ordered value: the list then fills
-  // with little more than `top` entries, not with top (1 + ln(n / top)).  (NaN sorts above
-  // all; its row has no list.)
-  __device__ __forceinline__ void start(float x, int top) {
-    const uint32_t o = ordered(x);
+  // Raises the floor of a list without real values yet to one that at least `top` of the
+  // lanes' x and y (maxima of several logits each) reach, found bit by bit over the upper
+  // half of the ordered value: the list then fills with little more than `top` entries, not
+  // with top (1 + ln(n / top)).  (One maximum a lane: 64 x 50021, top 64, 46.5 us against
+  // 22.4.  NaN sorts above all; its row has no list.)
+  __device__ __forceinline__ void start(float x, float y, int top) {
+    const uint32_t o = ordered(x), p = ordered(y);
     uint32_t t = 0;
 #pragma unroll
     for (int b = 31; b >= 16; --b)
-      if (__popcll(__ballot(o >= (t | 1u << b))) >= top) t |= 1u << b;
+      if (__popcll(__ballot(o >= (t | 1u << b))) + __popcll(__ballot(p >= (t | 1u << b))) >= top) t |= 1u << b;
     floor = fmaxf(floor, from_ordered(t));  // t == 0 maps to a NaN, which fmaxf drops
     gate = fmaxf(gate, floor);
   }
 };
+
+constexpr int kFirst = 256;  // keys of a part's first step that are sorted at once
 
 constexpr float kLn2 = 0.69314718f;
 
@@ -222,7 +241,7 @@ __device__ __forceinline__ void finish(const LpArgs& a, int row, const Sums& sum
 template <bool BF16, bool TOP>
 __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
   __shared__ Part parts[kWaves];
-  __shared__ uint64_t lists[TOP ? kWaves : 1][64];
+  __shared__ uint64_t lists[TOP ? kWaves : 1][TOP ? kFirst : 1];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t id = int64_t(blockIdx.x) * kWaves + wave;
   const int row = __builtin_amdgcn_readfirstlane(int(min(id / a.parts, int64_t(a.t - 1)))), part = int(id - int64_t(row) * a.parts);
@@ -261,10 +280,11 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
       bool listed = false;  // this step's entries are in the list already
       if constexpr (TOP) {
         if (list.floor == -__builtin_inff()) {
-          list.start(fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3])), a.top);
-          if (a.top > 8 && __ballot(list.mine != 0) == 0) {
-            // an empty list: what reaches the floor, side by side in LDS, sorted at once (one
-            // row of 131072, top 20: 16.8 us against 18.1; 2048 x 128000, top 8: 147 against 143)
+          list.start(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]), a.top);
+          if (a.top > 12 && __ballot(list.mine != 0) == 0) {
+            // an empty list: what reaches the floor, side by side in LDS, sorted at once (us
+            // sorted / offered: 64 x 50021 top 8 15.6 / 14.7, top 12 16.1 / 15.8, top 16 16.6 /
+            // 17.1, top 20 17.0 / 18.1)
             int n = 0;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -277,13 +297,14 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
                   const bool in = x[e] >= list.floor && i + e < end;
                   const uint64_t m = __ballot(in);
                   const int at = n + __builtin_amdgcn_mbcnt_hi(uint32_t(m >> 32), __builtin_amdgcn_mbcnt_lo(uint32_t(m), 0));
-                  if (in && at < 64) lists[wave][at] = key_of(x[e], uint32_t(i + e));
+                  if (in && at < kFirst) lists[wave][at] = key_of(x[e], uint32_t(i + e));
                   n += __popcll(m);
                 }
               }
             }
-            if (n <= 64) {
+            if (n <= kFirst) {
               list.fill(lane < n ? lists[wave][lane] : 0, lane, a.top);
+              for (int j = 64; j < n; j += 64) list.absorb_any(j + lane < n ? lists[wave][j + lane] : 0, lane, a.top);
               list.close_vector();
               listed = true;
             }
@@ -336,7 +357,7 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               if (__ballot(x[e] >= list.floor && at + e < end))
-                list.offer(at + e < end && x[e] >= list.floor ? key_of(x[e], uint32_t(at + e)) : 0, lane, a.top);
+                list.offer(at + e < end && x[e] >= list.floor ? key_of(x[e], uint32_t(at + e)) : 0, a.top);
             list.close_vector();
           }
         }
@@ -360,7 +381,13 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
   for (int w = 1; w < a.parts; ++w) {
     sums.join(parts[wave + w].sums, c);
     count += parts[wave + w].count;
-    if constexpr (TOP) list.offer(lane < a.top ? lists[wave + w][lane] : 0, lane, a.top);
+    if constexpr (TOP) {
+      const uint64_t k = lane < a.top ? lists[wave + w][lane] : 0;
+      if (__popcll(__ballot(k > list.last)) > TopList::kMany)
+        list.absorb(63 - lane < a.top ? lists[wave + w][63 - lane] : 0, lane, a.top);
+      else
+        list.offer(k, a.top);
+    }
   }
   finish(a, row, sums, count, list, target, c, lane);
 }
