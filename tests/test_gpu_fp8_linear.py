@@ -142,7 +142,7 @@ SHAPES = [  # t, n, k: one token to several tiles, every remainder that a tile c
     (1, 1, 1), (1, 17, 128), (1, 512, 2176), (2, 130, 256), (15, 100, 300), (16, 256, 1024), (17, 48, 130),
     (31, 33, 512), (33, 200, 1100), (63, 512, 256), (64, 272, 384), (65, 30, 200), (100, 300, 129), (129, 520, 640),
     (256, 256, 256), (257, 255, 128), (300, 1000, 777), (513, 700, 400), (1500, 3000, 300), (4096, 3584, 256), (70, 100, 9000), (600, 520, 4000),
-    (2000, 2050, 130), (1, 256, 18944), (16, 64, 18944)]
+    (2000, 2050, 130), (1, 256, 18944), (16, 64, 18944), (2090, 4090, 300), (700, 6150, 200), (700, 1500, 8000), (570, 3590, 7900)]
 
 
 @pytest.mark.parametrize("t,n,k", SHAPES)
@@ -162,7 +162,8 @@ def test_linear(api, t, n, k, dtype, out):
 
 @pytest.mark.parametrize("t,n,k", [(1, 1, 1), (1, 100, 300), (7, 144, 640), (16, 128, 128), (20, 70, 513), (64, 33, 256),
                                    (65, 128, 300), (200, 300, 256), (300, 129, 1000), (3, 64, 18944),
-                                   (1030, 2100, 256), (130, 40, 6000), (520, 1000, 700)])
+                                   (1030, 2100, 256), (130, 40, 6000), (520, 1000, 700), (700, 4090, 400), (1100, 4090, 300),
+                                   (2040, 4000, 300)])
 @pytest.mark.parametrize("act", ["silu", "gelu_tanh"])
 @pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("f32", "f32")])
 def test_gated(api, t, n, k, act, dtype, out):

@@ -392,36 +392,43 @@ __global__ __launch_bounds__(64 * W) void stream_kernel(LinArgs a) {
   store4<YBF>(a.y, token, a.n, int32_t(blockIdx.x) * 16 + 4 * c, v);
 }
 
-// The tile and the chunks of K for a shape.  A workgroup's time is its blocks times the
-// tile's time a block, and workgroups run in rounds of one on each of the 256 compute units
-// (two on a unit take twice as long).  Times a block measured on one box, alone and with
-// every unit busy: 256 x 256 1.46-1.86 us, 128 x 128 0.64, 64 x 128 0.52, 128 x 64 0.48,
-// 64 x 64 0.40 (the smaller, the more of it is the wait of a block).
-// Splitting K costs a second launch and the partial sums' traffic.  For instance (us, tiles
-// in this order without the second): 1024 x 4096 x 4096 60 / 27 / 38 / 44; 512 x 3584 x 3584
-// 53 / 23 / 19 / 22; 1024 x 1024 x 8192 105 / 44 / 36 / 27.
+// The tile and the chunks of K for a shape.  Workgroups run in rounds of one on each of the
+// 256 compute units (two on a unit take twice as long): a round takes block_us for each of
+// the workgroup's blocks, and tile_us to start and to write.  Of the small tiles several fit
+// a unit and hide one another's waits: wait_us is what a block waits, once for all rounds.
+// Splitting K costs a second launch and the partial sums' traffic.  The times are a fit to
+// every tile with 1 to 8 chunks on 59 shapes (1390 timings): the choice is 0.3% above the best
+// on the mean and 5% at most (without wait_us 10%, with one time a block and no more 34%).
+// For instance, us of 256 x 256 / 256 x 192 / 256 x 128 / 128 x 128: 18944 x 3584 with 256
+// tokens 52 / 47 / 36 / 45, with 2048 163 / 180 / 173 / 218; 11008 x 4096 with 2048 117 / 102 /
+// 112 / 139.
 struct Tile {
   int rn, rt;
-  float us;
+  float block_us, tile_us, wait_us;
 };
-constexpr Tile kTiles[] = {{8, 4, 1.8f}, {4, 2, 0.64f}, {2, 2, 0.52f}, {4, 1, 0.48f}, {2, 1, 0.40f}};
+constexpr Tile kTiles[] = {{8, 4, 1.55f, 3.0f, 0.f},   {8, 3, 1.31f, 2.8f, 0.f},   {8, 2, 0.96f, 2.9f, 0.f},
+                           {4, 2, 0.63f, 1.9f, 0.f},   {2, 2, 0.34f, 1.3f, 0.11f}, {4, 1, 0.35f, 1.4f, 0.11f},
+                           {2, 1, 0.23f, 0.9f, 0.13f}};
+constexpr int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16};
 struct Plan {
   int tile, chunks;
 };
 
 Plan plan_gemm(int32_t t, int32_t rbs, int32_t kb, bool exact) {
-  Plan best{4, 1};
+  Plan best{6, 1};
   float best_us = 1e30f;
-  for (int i = exact ? 1 : 0; i < 5; ++i) {  // float32 outputs: the smaller tiles only (registers)
-    const int64_t tiles = int64_t((rbs + 2 * kTiles[i].rn - 1) / (2 * kTiles[i].rn)) * ((t + 64 * kTiles[i].rt - 1) / (64 * kTiles[i].rt));
-    for (int s = 1; s <= 16 && s <= kb; s *= 2) {
-      if (s > 1 && tiles * s > 512) break;
-      const int per = (kb + s - 1) / s;
-      const float join = s == 1 ? 0.f : 4.f + float(s) * t * rbs * 64.f * 2.f / 4e6f;
-      const float us = float((tiles * s + 255) / 256) * per * kTiles[i].us + join;
+  for (int i = exact ? 3 : 0; i < 7; ++i) {  // float32 outputs: the smaller tiles only (registers)
+    const Tile& c = kTiles[i];
+    const int64_t tiles = int64_t((rbs + 2 * c.rn - 1) / (2 * c.rn)) * ((t + 64 * c.rt - 1) / (64 * c.rt));
+    for (int s : kSplits) {
+      if (s > kb || (s > 1 && tiles * s > 512)) break;
+      const int per = (kb + s - 1) / s, chunks = (kb + per - 1) / per;
+      const float rounds = float((tiles * chunks + 255) / 256);
+      const float join = chunks == 1 ? 0.f : 2.3f + float(chunks) * t * rbs * 64.f * 2.f / 6e6f;
+      const float us = per * (rounds * c.block_us + c.wait_us) + rounds * c.tile_us + join;
       if (us < best_us) {
         best_us = us;
-        best = {i, (kb + per - 1) / per};
+        best = {i, chunks};
       }
     }
   }
@@ -475,9 +482,15 @@ hipError_t launch(LinArgs& a, mbq_dtype x_dtype, hipStream_t stream) {
     case 0:
       if constexpr (YBF) launch_gemm<8, 4, 2, ACT, YBF>(a, stream);
       break;
-    case 1: launch_gemm<4, 2, 3, ACT, YBF>(a, stream); break;
-    case 2: launch_gemm<2, 2, 3, ACT, YBF>(a, stream); break;
-    case 3: launch_gemm<4, 1, 3, ACT, YBF>(a, stream); break;
+    case 1:
+      if constexpr (YBF) launch_gemm<8, 3, 2, ACT, YBF>(a, stream);
+      break;
+    case 2:
+      if constexpr (YBF) launch_gemm<8, 2, 3, ACT, YBF>(a, stream);
+      break;
+    case 3: launch_gemm<4, 2, 3, ACT, YBF>(a, stream); break;
+    case 4: launch_gemm<2, 2, 3, ACT, YBF>(a, stream); break;
+    case 5: launch_gemm<4, 1, 3, ACT, YBF>(a, stream); break;
     default: launch_gemm<2, 1, 3, ACT, YBF>(a, stream); break;
   }
   if (a.chunks > 1)
