@@ -141,8 +141,9 @@ def test_pack_reports_non_finite(api):
 SHAPES = [  # t, n, k: one token to several tiles, every remainder that a tile can have
     (1, 1, 1), (1, 17, 128), (1, 512, 2176), (2, 130, 256), (15, 100, 300), (16, 256, 1024), (17, 48, 130),
     (31, 33, 512), (33, 200, 1100), (63, 512, 256), (64, 272, 384), (65, 30, 200), (100, 300, 129), (129, 520, 640),
-    (256, 256, 256), (257, 255, 128), (300, 1000, 777), (513, 700, 400), (1500, 3000, 300), (4096, 3584, 256), (70, 100, 9000), (600, 520, 4000),
-    (2000, 2050, 130), (1, 256, 18944), (16, 64, 18944), (2090, 4090, 300), (700, 6150, 200), (700, 1500, 8000), (570, 3590, 7900)]
+    (256, 256, 256), (257, 255, 128), (300, 1000, 777), (513, 700, 400), (1500, 3000, 300), (4096, 3584, 256),
+    (70, 100, 9000), (600, 520, 4000), (12, 64, 2048), (13, 64, 2048), (3, 4200, 4096), (3, 4200, 4097), (2000, 2050, 130), (1, 256, 18944), (16, 64, 18944),
+    (2090, 4090, 300), (700, 6150, 200), (700, 1500, 8000), (570, 3590, 7900)]
 
 
 @pytest.mark.parametrize("t,n,k", SHAPES)

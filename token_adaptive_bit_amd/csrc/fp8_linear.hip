@@ -278,7 +278,7 @@ __global__ __launch_bounds__(256) void join_kernel(LinArgs a) {
 // XT: the type of x.  Codes (MBQ_E4M3) are read from memory, with every block of the weight;
 // a few float tokens are quantized here, once a workgroup into LDS, while the first weight
 // tiles are on their way, which saves the quantizing launch.
-constexpr int kInlineBlocks = 148;  // quantized in the kernel: at most 5 blocks for each 16 lanes
+constexpr int kInlineBlocks = 192;  // most that are quantized in the kernel (their place in LDS)
 
 template <int W, int TT, int XT, int ACT, bool YBF>
 __global__ __launch_bounds__(64 * W) void stream_kernel(LinArgs a) {
@@ -504,10 +504,12 @@ size_t codes_bytes(const mbq_fp8_desc& d, int32_t t) { return size_t(t) * d.k_bl
 }  // namespace
 
 // Float activations quantized inside the streaming kernel: its workgroups each do all of it,
-// so a few blocks only.  One token of 5120 x 5120 (40 blocks): 8.1 us in one launch against
-// 2.5 + 6.8 us and the gap between two.
+// so a few blocks only, more where there is one workgroup a unit or less.  us within / in a
+// launch before, by blocks: 5120 x 5120 (320 workgroups) 40 7.9 / 9.0, 80 8.4 / 9.1, 120 9.6 /
+// 9.2; 18944 x 3584 (1184) 56 13.2 / 14.2, 112 14.7 / 14.4, 140 16.0 / 14.5; 3584 x 18944 (224)
+// 148 13.8 / 15.3; 4096 x 4096 (256) 128 6.6 / 7.7, 192 7.6 / 7.7, 256 8.6 / 7.9.
 bool quantize_inline(const mbq_fp8_desc& d, int32_t t, mbq_dtype x_dtype) {
-  return x_dtype != MBQ_E4M3 && t <= 16 && int64_t(t) * d.k_blocks <= kInlineBlocks;
+  return x_dtype != MBQ_E4M3 && t <= 16 && int64_t(t) * d.k_blocks <= (d.row_blocks / (d.gated + 1) <= 256 ? kInlineBlocks : 96);
 }
 
 // Workspace: the activations' codes and scales (codes given in rows that hold no whole 16
