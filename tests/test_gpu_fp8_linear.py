@@ -143,7 +143,8 @@ SHAPES = [  # t, n, k: one token to several tiles, every remainder that a tile c
     (31, 33, 512), (33, 200, 1100), (63, 512, 256), (64, 272, 384), (65, 30, 200), (100, 300, 129), (129, 520, 640),
     (256, 256, 256), (257, 255, 128), (300, 1000, 777), (513, 700, 400), (1500, 3000, 300), (4096, 3584, 256),
     (70, 100, 9000), (600, 520, 4000), (12, 64, 2048), (13, 64, 2048), (3, 4200, 4096), (3, 4200, 4097), (2000, 2050, 130), (1, 256, 18944), (16, 64, 18944),
-    (2090, 4090, 300), (700, 6150, 200), (700, 1500, 8000), (570, 3590, 7900)]
+    (2090, 4090, 300), (700, 6150, 200), (700, 1500, 8000), (570, 3590, 7900),
+    (32, 4100, 3000), (32, 4100, 3200), (64, 512, 4096), (64, 500, 4100), (48, 530, 6150)]
 
 
 @pytest.mark.parametrize("t,n,k", SHAPES)

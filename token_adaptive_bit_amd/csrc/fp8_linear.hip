@@ -441,11 +441,14 @@ void launch_gemm(const LinArgs& a, hipStream_t stream) {
   gemm_kernel<RN, RT, NS, ACT, YBF><<<uint32_t(tiles * a.chunks), 512, 0, stream>>>(a);
 }
 
-// Up to 16 tokens the streaming kernel serves every weight; up to 64 those of few row blocks
-// (us with it / in tiles: 32 tokens 1024 x 4096 9.2 / 12.6, 5120 x 5120 17.0 / 14.4; 64
-// tokens 18944 x 3584 41.1 / 21.6).
-bool streams(int32_t t, int32_t row_groups) { return t <= 16 || (t <= 64 && (t + 15) / 16 * row_groups <= 256); }
-
+// Up to 16 tokens the streaming kernel serves every weight; up to 64 those whose workgroups
+// pass few blocks, all rounds of 256 of them together (us with it / in tiles: 17 to 32 tokens
+// 4096 x 4096, 32 blocks, 7.0 / 10.5, 2048 x 8192, 64, 10.7 to 12.4 / 12.5 to 11.0, 512 x 16384,
+// 128, 22.1 / 12.6; 48 to 64 tokens 2048 x 2048, 16, 6.7 / 9.1, 1024 x 4096, 32, 9.5 to 10.4 /
+// 10.3 to 9.4, 2048 x 8192 18.3 / 11.8).
+bool streams(int32_t t, int32_t row_groups, int32_t kb) {
+  return t <= 16 || (t <= 64 && int64_t((row_groups + 255) / 256) * kb <= (t <= 32 ? 48 : 32));
+}
 
 template <int W, int TT, int ACT, bool YBF>
 void launch_stream(const LinArgs& a, mbq_dtype x_dtype, hipStream_t stream) {
@@ -466,7 +469,7 @@ void launch_stream(const LinArgs& a, mbq_dtype x_dtype, hipStream_t stream) {
 template <int ACT, bool YBF>
 hipError_t launch(LinArgs& a, mbq_dtype x_dtype, hipStream_t stream) {
   constexpr int R = ACT == kPlain ? 1 : 2;
-  if (streams(a.t, a.rbs / R)) {
+  if (streams(a.t, a.rbs / R, a.kb)) {
     // sixteen waves for long rows of few row groups, which leave the units half empty with
     // eight (one token, 8 / 16 waves: 3584 x 18944 17.9 / 14.2 us, 5120 x 5120 7.8 / 8.3)
     if (a.t <= 16 && a.rbs / R <= 256 && a.kb >= 64) launch_stream<16, 1, ACT, YBF>(a, x_dtype, stream);
@@ -520,7 +523,7 @@ size_t fp8_linear_workspace(const mbq_fp8_desc& d, int32_t t, mbq_dtype x_dtype)
   if (x_dtype != MBQ_E4M3) bytes = codes_bytes(d, t) + align256(size_t(d.k_blocks) * t * 4);
   else if (d.k % 16 != 0) bytes = codes_bytes(d, t);
   size_t part = 0;
-  if (!streams(t, d.row_blocks / (d.gated + 1)))
+  if (!streams(t, d.row_blocks / (d.gated + 1), d.k_blocks))
     for (bool exact : {false, true}) {  // y's type is not known here
       const int chunks = plan_gemm(t, d.row_blocks, d.k_blocks, exact).chunks;
       if (chunks > 1) part = std::max(part, size_t(chunks) * t * d.row_blocks * 64);
