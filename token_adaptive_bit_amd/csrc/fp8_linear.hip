@@ -469,7 +469,7 @@ void launch_stream(const LinArgs& a, mbq_dtype x_dtype, hipStream_t stream) {
 template <int ACT, bool YBF>
 hipError_t launch(LinArgs& a, mbq_dtype x_dtype, hipStream_t stream) {
   constexpr int R = ACT == kPlain ? 1 : 2;
-  if (streams(a.t, a.rbs / R, a.kb)) {
+  if (a.x || streams(a.t, a.rbs / R, a.kb)) {  // float x (at most 16 tokens): only the streaming kernel reads it
     // sixteen waves for long rows of few row groups, which leave the units half empty with
     // eight (one token, 8 / 16 waves: 3584 x 18944 17.9 / 14.2 us, 5120 x 5120 7.8 / 8.3)
     if (a.t <= 16 && a.rbs / R <= 256 && a.kb >= 64) launch_stream<16, 1, ACT, YBF>(a, x_dtype, stream);
