@@ -136,6 +136,10 @@ template <int STEP>
 __device__ __forceinline__ uint64_t across(uint64_t v) {
   return uint64_t(across<STEP>(uint32_t(v >> 32))) << 32 | across<STEP>(uint32_t(v));
 }
+template <int STEP>
+__device__ __forceinline__ double across(double v) {
+  return __longlong_as_double(int64_t(across<STEP>(uint64_t(__double_as_longlong(v)))));
+}
 
 // Largest of the 16 lanes of a row, in all of them.
 __device__ __forceinline__ uint32_t max16(uint32_t m) {

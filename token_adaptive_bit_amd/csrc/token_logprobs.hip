@@ -2,7 +2,10 @@
 // over the logits.  With c = inv_temperature log2 e, a running reference r and d = c (x - r),
 //   s = sum 2^d,  q = sum 2^d d
 // give the log probability ln 2 d - ln s of x and the entropy ln s - ln 2 q / s; both sums
-// are kept per lane in float32 and rescaled when the values outgrow r.  The rank counts
+// are kept per lane in float32 about one reference a wave, which follows the wave's largest
+// logit to within a factor of 2^1.5 in the terms.  (Where terms lead it further, ln s and d
+// are large numbers whose difference is the answer: with a lead of up to 2^16 the entropy of
+// rows near one certain token was off by 4e-6, now by a tenth of that.)  The rank counts
 // lanes' comparisons on the scalar unit.  The top list is a sorted list of 64-bit keys
 // (value, then lower index first), one entry a lane; a vector of logits is looked at only if
 // it reaches the list's last entry.
@@ -136,11 +139,11 @@ constexpr int kFirst = 256;  // keys of a part's first step that are sorted at o
 
 constexpr float kLn2 = 0.69314718f;
 
-// The sums of a set of logits.  The reference of the exponents is one of two: a whole
+// What a set of sums is about.  The reference of the exponents is one of two: a whole
 // number M in units of ln 2 (m = 0), so that c x - M is a single FMA and rounds once; or,
 // for values that c x would overflow or blur, a logit m (M = 0).
-struct Sums {
-  float m, M, s, q;
+struct Reference {
+  float m, M;
   static constexpr float kNone = -3e38f;  // M while nothing above -infinity has been seen
 
   __device__ __forceinline__ float exponent(float x, float c) const { return fmaf(x - m, c, -M); }
@@ -149,36 +152,62 @@ struct Sums {
     const float d = exponent(x, c);
     return fabsf(d) < 1e6f ? d * kLn2 : fmaf(x - m, inv_t, -M * kLn2);
   }
-  // Moves the reference up; terms further than 2^-10000 below it are 0 (finite, and at most
-  // 0 from the empty set's reference too, so that an empty sum stays 0).
-  __device__ __forceinline__ void move(float m2, float M2, float c) {
-    const float d = fminf(fmaxf(fmaf(m - m2, c, M - M2), -1e4f), 0.f), f = __builtin_amdgcn_exp2f(d);
-    q = f * fmaf(d, s, q);
-    s *= f;
-    m = m2;
-    M = M2;
+  // The exponent of this reference about r, which lies above it; less than 2^-10000 is 0
+  // (finite, and at most 0 for the empty set's reference too, so that an empty sum stays 0).
+  __device__ __forceinline__ float below(Reference r, float c) const {
+    return fminf(fmaxf(fmaf(m - r.m, c, M - r.M), -1e4f), 0.f);
   }
+};
+
+// A lane's sums of a wave's part.
+struct Sums {
+  Reference r;  // the same in all lanes
+  float s, q;
+
   __device__ __forceinline__ void refer(float x, float c) {
     const bool plain = fabsf(x * c) < 1e6f;
-    move(plain ? 0.f : x, plain ? rintf(x * c) : 0.f, c);
+    const Reference to = {plain ? 0.f : x, plain ? rintf(x * c) : 0.f};
+    const float d = r.below(to, c), f = __builtin_amdgcn_exp2f(d);
+    q = f * fmaf(d, s, q);
+    s *= f;
+    r = to;
   }
-  __device__ __forceinline__ void join(Sums o, float c) {
-    if (o.s == 0.f) return;
-    if (s == 0.f || m + M / c < o.m + o.M / c) {
-      const Sums t = *this;
+};
+
+// The sums of a part or of a row.  Lanes and parts meet in double, once a row: in float32
+// the dozen small sums added to one near 1 would cost a confident row its last digits.
+struct Total {
+  Reference r;
+  double s, q;
+
+  __device__ __forceinline__ void join(Total o, float c) {
+    if (o.s == 0.) return;
+    if (s == 0. || r.m + r.M / c < o.r.m + o.r.M / c) {
+      const Total t = *this;
       *this = o;
       o = t;
     }
-    o.move(m, M, c);
-    s += o.s;
-    q += o.q;
+    const float d = o.r.below(r, c);
+    const double f = __builtin_amdgcn_exp2f(d);
+    s += f * o.s;
+    q += f * (o.q + d * o.s);
   }
   template <int STEP = 1>
   __device__ __forceinline__ void join_wave(float c) {
-    join({across<STEP>(m), across<STEP>(M), across<STEP>(s), across<STEP>(q)}, c);
+    join({{across<STEP>(r.m), across<STEP>(r.M)}, across<STEP>(s), across<STEP>(q)}, c);
     if constexpr (STEP < 32) join_wave<STEP * 2>(c);
   }
 };
+
+template <int STEP = 32>
+__device__ __forceinline__ double wave_sum(double v) {
+  v += across<STEP>(v);
+  if constexpr (STEP > 1) v = wave_sum<STEP / 2>(v);
+  return v;
+}
+__device__ __forceinline__ Total wave_total(const Sums& a) {
+  return {a.r, wave_sum(double(a.s)), wave_sum(double(a.q))};
+}
 
 __device__ __forceinline__ int wave_sum(int v) {
   v += int(across<8>(uint32_t(v)));
@@ -189,9 +218,18 @@ __device__ __forceinline__ int wave_sum(int v) {
   return v + int(across<32>(uint32_t(v)));
 }
 
+__device__ __forceinline__ float wave_max(float v) {  // NaN lanes take no part
+  v = fmaxf(v, across<8>(v));
+  v = fmaxf(v, across<4>(v));
+  v = fmaxf(v, across<2>(v));
+  v = fmaxf(v, across<1>(v));
+  v = fmaxf(v, across<16>(v));
+  return fmaxf(v, across<32>(v));
+}
+
 struct Part {
-  Sums sums;
-  int count, unused[3];
+  Total total;
+  int count, unused;
 };
 
 // A row's target (-1: none) and its logit.  Two reads that wait for one another, so they are
@@ -218,21 +256,21 @@ __device__ __forceinline__ Target target_of(const LpArgs& a, int row) {
 }
 
 // Writes a row's results from its sums and its top list (one wave).
-__device__ __forceinline__ void finish(const LpArgs& a, int row, const Sums& sums, int count, const TopList& list,
+__device__ __forceinline__ void finish(const LpArgs& a, int row, const Total& total, int count, const TopList& list,
                                        Target target, float c, int lane) {
-  const float s = sums.s;
+  const float s = float(total.s);
   const bool valid = target.at >= 0;
   const bool none = s == 0.f, bad = s != s;  // nothing but -infinity; a NaN or +infinity
-  const float log_s = logf(s), inf = __builtin_inff();
+  const float log_s = logf(s) + float(total.s - s) / s, inf = __builtin_inff();
   if (lane == 0) {
-    a.logprob[row] = !valid ? 0.f : none ? -inf : at_most_0(sums.natural(target.x, c, a.inv_temperature) - log_s);
-    a.entropy[row] = none ? 0.f : -at_most_0(kLn2 * (sums.q / s) - log_s);
+    a.logprob[row] = !valid ? 0.f : none ? -inf : at_most_0(total.r.natural(target.x, c, a.inv_temperature) - log_s);
+    a.entropy[row] = none ? 0.f : -at_most_0(kLn2 * (float(total.q) / s) - log_s);
     a.rank[row] = valid && !bad ? count + 1 : 0;
   }
   if (lane < a.top) {
     const float x = from_ordered(uint32_t(list.mine >> 32));
     a.top_ids[int64_t(row) * a.top + lane] = bad ? -1 : int32_t(~uint32_t(list.mine));
-    a.top_logprobs[int64_t(row) * a.top + lane] = none ? -inf : bad ? s : at_most_0(sums.natural(x, c, a.inv_temperature) - log_s);
+    a.top_logprobs[int64_t(row) * a.top + lane] = none ? -inf : bad ? s : at_most_0(total.r.natural(x, c, a.inv_temperature) - log_s);
   }
 }
 
@@ -247,7 +285,8 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
   const int row = __builtin_amdgcn_readfirstlane(int(min(id / a.parts, int64_t(a.t - 1)))), part = int(id - int64_t(row) * a.parts);
   const uint8_t* base = static_cast<const uint8_t*>(a.logits) + int64_t(row) * a.ld * (BF16 ? 2 : 4);
   const float c = a.inv_temperature * 1.4426950408889634f;
-  Sums sums = {0.f, Sums::kNone, 0.f, 0.f};
+  Sums sums = {{0.f, Reference::kNone}, 0.f, 0.f};
+  Total total = {};
   int count = 0;
   TopList list;
   Target target = {-1, 0.f};
@@ -277,6 +316,11 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
         raw[u].get(x);
         best[u] = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
       }
+      // The same reference in every lane: after the first step the wave's maximum grows a few
+      // times a row, where lanes of their own would each outgrow theirs.
+      const float top_of = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
+      if (__ballot(top_of > -__builtin_inff() && (sums.r.M == Reference::kNone || sums.r.exponent(top_of, c) > 1.f)))
+        sums.refer(wave_max(top_of), c);
       bool listed = false;  // this step's entries are in the list already
       if constexpr (TOP) {
         if (list.floor == -__builtin_inff()) {
@@ -311,37 +355,32 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
           }
         }
       }
+      // A step's 32 terms are summed apart, by the vector, and then added: the lane's long
+      // chain has few roundings.
+      float ps = 0.f, pq = 0.f;
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int i = i0 + (u * 64 + lane) * 8;
         float x[8];
         raw[u].get(x);
-        // The reference follows the largest value with a lead of up to 2^16 in the terms, so
-        // that the sums are rescaled rarely.
-        const bool far = best[u] > -__builtin_inff() && (sums.M == Sums::kNone || sums.exponent(best[u], c) > 16.f);
-        if (__ballot(far)) {
-          if (far) sums.refer(best[u], c);
-        }
-        // A vector's terms are summed apart and then added: the lane's long chain has an
-        // eighth of the roundings.
-        float ps = 0.f, pq = 0.f;
-        if (__ballot(sums.m != 0.f)) {
+        float vs = 0.f, vq = 0.f;
+        if (__ballot(sums.r.m != 0.f)) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float d = sums.exponent(x[e], c), p = __builtin_amdgcn_exp2f(d);
-            ps += p;
-            pq = fmaf(p, fmaxf(d, -1e4f), pq);  // finite, so that p = 0 adds 0
+            const float d = sums.r.exponent(x[e], c), p = __builtin_amdgcn_exp2f(d);
+            vs += p;
+            vq = fmaf(p, fmaxf(d, -1e4f), vq);  // finite, so that p = 0 adds 0
           }
         } else {
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const float d = fmaf(x[e], c, -sums.M), p = __builtin_amdgcn_exp2f(d);
-            ps += p;
-            pq = fmaf(p, fmaxf(d, -1e4f), pq);
+            const float d = fmaf(x[e], c, -sums.r.M), p = __builtin_amdgcn_exp2f(d);
+            vs += p;
+            vq = fmaf(p, fmaxf(d, -1e4f), vq);
           }
         }
-        sums.s += ps;
-        sums.q += pq;
+        ps += vs;
+        pq += vq;
         // a part ends on a vector; what is read past it counts for nothing
         const float bound = i >= end ? __builtin_inff() : i + 8 <= target.at ? xt : above;
 #pragma unroll
@@ -362,24 +401,26 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
           }
         }
       }
+      sums.s += ps;
+      sums.q += pq;
     }
-    sums.join_wave(c);
+    total = wave_total(sums);
     count += wave_sum(tied);
     if (a.parts > kWaves) {
       const int64_t at = int64_t(row) * a.parts + part;
-      if (lane == 0) a.part[at] = {sums, count, {}};
+      if (lane == 0) a.part[at] = {total, count, 0};
       if (TOP && lane < a.top) a.keys[at * a.top + lane] = list.mine;
     } else if (a.parts == 1) {
-      finish(a, row, sums, count, list, target, c, lane);
+      finish(a, row, total, count, list, target, c, lane);
     }
   }
   if (a.parts == 1 || a.parts > kWaves) return;
-  if (lane == 0) parts[wave] = {sums, count, {}};
+  if (lane == 0) parts[wave] = {total, count, 0};
   if constexpr (TOP) lists[wave][lane] = list.mine;
   __syncthreads();
   if (part) return;
   for (int w = 1; w < a.parts; ++w) {
-    sums.join(parts[wave + w].sums, c);
+    total.join(parts[wave + w].total, c);
     count += parts[wave + w].count;
     if constexpr (TOP) {
       const uint64_t k = lane < a.top ? lists[wave + w][lane] : 0;
@@ -389,7 +430,7 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
         list.offer(k, a.top);
     }
   }
-  finish(a, row, sums, count, list, target, c, lane);
+  finish(a, row, total, count, list, target, c, lane);
 }
 
 constexpr int kMaxParts = 64;
@@ -400,21 +441,21 @@ __global__ __launch_bounds__(kThreads) void merge_kernel(LpArgs a) {
   __shared__ uint64_t keys[kMaxParts * MBQ_MAX_TOP];
   const int row = blockIdx.x, lane = threadIdx.x & 63, all = a.parts * a.top;
   const Target target = target_of<BF16>(a, row);
-  Sums sums = {0.f, Sums::kNone, 0.f, 0.f};
+  Total total = {{0.f, Reference::kNone}, 0., 0.};
   int count = 0;
   if (lane < a.parts) {
-    sums = a.part[int64_t(row) * a.parts + lane].sums;
+    total = a.part[int64_t(row) * a.parts + lane].total;
     count = a.part[int64_t(row) * a.parts + lane].count;
   }
   for (int i = threadIdx.x; i < all; i += kThreads) keys[i] = a.keys[int64_t(row) * all + i];
   __syncthreads();
   if (threadIdx.x >= 64) return;
   const float c = a.inv_temperature * 1.4426950408889634f;
-  sums.join_wave(c);
+  total.join_wave(c);
   count = wave_sum(count);
   TopList list;
   if (a.top) list.take(keys + (lane < a.parts ? lane : 0) * a.top, lane < a.parts, lane, a.top);
-  finish(a, row, sums, count, list, target, c, lane);
+  finish(a, row, total, count, list, target, c, lane);
 }
 
 // Parts of a row: at least 4096 waves (four a SIMD), each with at least one full step of its
