@@ -255,6 +255,14 @@ __device__ __forceinline__ Target target_of(const LpArgs& a, int row) {
   return r;
 }
 
+// Between the LDS writes of a wave's lanes and the reads of its others: a wave's LDS accesses
+// complete in order, so this only keeps the compiler from moving one past the other.
+__device__ __forceinline__ void wave_exchange() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
 // Writes a row's results from its sums and its top list (one wave).
 __device__ __forceinline__ void finish(const LpArgs& a, int row, const Total& total, int count, const TopList& list,
                                        Target target, float c, int lane) {
@@ -346,12 +354,14 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
                 }
               }
             }
+            wave_exchange();
             if (n <= kFirst) {
               list.fill(lane < n ? lists[wave][lane] : 0, lane, a.top);
               for (int j = 64; j < n; j += 64) list.absorb_any(j + lane < n ? lists[wave][j + lane] : 0, lane, a.top);
               list.close_vector();
               listed = true;
             }
+            wave_exchange();  // the next writes come after these reads
           }
         }
       }
