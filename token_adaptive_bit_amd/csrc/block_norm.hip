@@ -62,7 +62,7 @@ __device__ __forceinline__ void join_residual(const Args& a, int64_t row, int64_
   for (int e = 0; e < 8; ++e) v[e] = fmaf(a.gate_scale, v[e], a.residual_scale * r[e]);
 }
 
-// Writes eight elements of h; m: whether this 16-lane group lies inside the row at all.
+// Writes eight elements of h (those inside the row; with codes the 16 lanes of a block together).
 template <int HT>
 __device__ __forceinline__ void store_h(const Args& a, int64_t row, int64_t i, const float (&h)[8]) {
   if constexpr (HT == MBQ_E4M3) {
@@ -205,28 +205,35 @@ __global__ __launch_bounds__(1024) void norm_long_kernel(Args a) {
     if (a.residual) load8<RB>(static_cast<const uint8_t*>(a.residual) + row * a.ldr * (RB ? 2 : 4), i, k, r);
     join_residual<XB>(a, row, i, r, v);
   };
+  // A lane's sum over the row of `term` of its elements, in three levels (a vector, kRun
+  // vectors, the row).  In one chain of the lane's elements a sum of equal terms drifts by up
+  // to 2^-14 of itself in rows of 2^22 and 2^-12 in rows of 2^24; 512 x 65536 bfloat16, both
+  // norms, 91.4 us so and 91.0 in one chain.
+  auto lane_sum = [&](auto get, auto term) {
+    constexpr int kRun = 32;
+    float s = 0.f, v[8];
+    for (int64_t i0 = 8 * tid; i0 < k; i0 += kRun * step) {
+      const int64_t end = min(i0 + kRun * step, k);
+      float run = 0.f;
+      for (int64_t i = i0; i < end; i += step) {
+        get(i, v);
+        float p = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) p = i + e < k ? term(v[e], p) : p;
+        run += p;
+      }
+      s += run;
+    }
+    return s;
+  };
   auto stats = [&](auto get, float& mean, float& rstd) {
     mean = 0.f;
-    float v[8];
     if (layer) {
-      float s = 0.f;
-      for (int64_t i = 8 * tid; i < k; i += step) {
-        get(i, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s += i + e < k ? v[e] : 0.f;
-      }
-      mean = row_sum(s, red, slot, 1024) * inv_k;
+      mean = row_sum(lane_sum(get, [](float v, float p) { return p + v; }), red, slot, 1024) * inv_k;
       slot ^= 1;
     }
-    float s = 0.f;
-    for (int64_t i = 8 * tid; i < k; i += step) {
-      get(i, v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float d = i + e < k ? v[e] - mean : 0.f;
-        s = fmaf(d, d, s);
-      }
-    }
+    const float m = mean;
+    const float s = lane_sum(get, [m](float v, float p) { return fmaf(v - m, v - m, p); });
     rstd = 1.f / sqrtf(row_sum(s, red, slot, 1024) * inv_k + a.eps);
     slot ^= 1;
     __syncthreads();
