@@ -674,8 +674,8 @@ def _fp8_run(p, x, scale, act, out_dtype, y, workspace):
     dev, code, n, blob = x.get_device(), _CODE[x.dtype], p.desc.n, p.blob
     if k != p.desc.k:
         raise ValueError(f"x has {k} inputs, the weight {p.desc.k}")
-    if blob.dtype != torch.uint8 or blob.get_device() != dev or blob.numel() < p.desc.total_bytes:
-        raise ValueError(f"packed blob must be uint8 on cuda:{dev} holding at least desc.total_bytes")
+    if blob.dtype != torch.uint8 or blob.get_device() != dev or not blob.is_contiguous() or blob.numel() < p.desc.total_bytes:
+        raise ValueError(f"packed blob must be contiguous uint8 on cuda:{dev} holding at least desc.total_bytes")
     if code == MBQ_E4M3:
         scale = _flat(scale, "scale", _F32S, dev, (p.desc.k_blocks, t))
     elif scale is not None:
