@@ -14,3 +14,10 @@ def test_a_blob_lies_in_one_piece(rec, gated):
     with pytest.raises(ValueError, match="contiguous"):
         (api.fp8_gated if gated else api.fp8_linear)(apart, z(3, 256), y=z(3, 64))
     assert rec.calls == []
+
+
+@pytest.mark.parametrize("gate", [0.5, [1.0, 2.0, 3.0]])
+def test_a_gate_is_a_tensor(rec, gate):
+    with pytest.raises(TypeError, match="gate must be a tensor"):
+        api.block_norm(z(3, 300), gate=gate, y=z(3, 300), h=z(3, 300))
+    assert rec.calls == []

@@ -754,6 +754,8 @@ def block_norm(x: torch.Tensor, residual: torch.Tensor | None = None, pre: torch
     postb_ptr = 0 if post_bias is None else _flat(post_bias, "post_bias", _F32S, dev, (k,))
     gate_kind = gate_ptr = 0
     if gate is not None:
+        if not isinstance(gate, torch.Tensor):
+            raise TypeError("gate must be a tensor")
         if gate.dim() == 2:
             gate_kind, gate_ptr = _lib.MBQ_GATE_FULL, _flat(gate, "gate", (x.dtype,), dev, shape)
         elif gate.shape == (k,):
