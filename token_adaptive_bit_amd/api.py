@@ -8,16 +8,23 @@ without synchronizing.  No arithmetic happens here.
 from __future__ import annotations
 
 import ctypes
+import warnings
 from dataclasses import dataclass
 from typing import NamedTuple
 
 import torch
 
 from . import _lib
-from . import _bind  # after _lib: the library and torch's runtime are loaded
 from ._lib import (MBQ_BF16, MBQ_E4M3, MBQ_F32, MBQ_MUL_AUTO, MBQ_MUL_BF16, MBQ_MUL_FP8_FP4, MBQ_PATH_AUTO,
                    MBQ_PATH_GENERIC, MbqDesc, MbqError, MbqFp8Desc, MbqOpts, check, describe,
                    fp8_describe)
+
+try:
+    from . import _bind  # after _lib: the library and torch's runtime are loaded
+except ImportError as e:  # built without torch's headers, or for another torch
+    _bind = None
+    warnings.warn(f"native binding of the dense operators not loaded ({e}); their calls take the slower way through "
+                  "ctypes", RuntimeWarning, stacklevel=2)
 
 __all__ = ["PackedLinear", "pack", "pack_bitplane", "pack_concat", "route", "route_from_logits", "regroup", "linear",
            "linear_workspace", "describe", "MbqError", "MlpRouter", "route_mlp",
@@ -501,7 +508,7 @@ def linear_lowrank(p: PackedLinear, x: torch.Tensor, perm: torch.Tensor, offsets
 # --- log probabilities of tokens.  A decode step makes many of these calls and each runs for
 # --- a few microseconds, so ordinary calls (plain contiguous tensors, no buffers given) are
 # --- checked and made by _bind; what it leaves alone comes back here, where the checks name
-# --- what is wrong.
+# --- what is wrong.  Without _bind every call comes here: the same kernels, a few microseconds later.
 
 _F8 = torch.float8_e4m3fn
 _CODE = {torch.float32: MBQ_F32, torch.bfloat16: MBQ_BF16, _F8: MBQ_E4M3}
@@ -519,7 +526,7 @@ def _stream_of(x: torch.Tensor):
 
 
 def _bound(x) -> bool:
-    return type(x) is torch.Tensor and x.is_cuda
+    return _bind is not None and type(x) is torch.Tensor and x.is_cuda
 
 
 def _rows(t, name: str, dtypes, dev=None, shape=None) -> int:

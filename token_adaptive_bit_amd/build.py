@@ -1,5 +1,7 @@
 """Build libmbq.so (gfx950) in the package directory with hipcc, and the native binding of
-the dense operators (_bind.so, host code) with the C++ compiler.
+the dense operators (_bind.so, host code) with the C++ compiler.  The library comes first and
+needs neither Python's nor torch's headers; without those the binding is left out, and the
+dense operators are called through ctypes.
 
 Every translation unit is compiled for gfx950 only, with packed FP32 instructions
 disabled (-packed-fp32-ops) and IEEE-correct float32 division.  The pack kernel is also
@@ -118,6 +120,19 @@ def _run(cmd: list, what: str, verbose: bool) -> None:
         raise RuntimeError(f"{what} failed:\n{res.stdout}\n{res.stderr}")
 
 
+def _binding_lacks() -> str:
+    """What the binding needs and this machine does not have ('' if all is there)."""
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    try:
+        torch = _torch_dir()
+    except RuntimeError:
+        return "torch"
+    if not os.path.exists(os.path.join(torch, "include", "torch", "csrc", "autograd", "python_variable.h")):
+        return "torch's headers"
+    return ""
+
+
 def _compile_bind(verbose: bool) -> str:
     """csrc/bind.cpp, the native calls of the dense operators (host code only)."""
     obj, torch = os.path.join(BUILD_DIR, "bind.o"), _torch_dir()
@@ -139,15 +154,19 @@ def _link_bind(obj: str, verbose: bool) -> None:
 def build(verbose: bool = False, jobs: int | None = None) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     jobs = jobs or min(len(SOURCES), max(1, min(8, os.cpu_count() or 1)))
+    lacks = _binding_lacks()
     with cf.ThreadPoolExecutor(jobs) as ex:
-        bind = ex.submit(_compile_bind, verbose)
+        bind = None if lacks else ex.submit(_compile_bind, verbose)
         objs = list(ex.map(lambda kv: _compile(kv[0], kv[1], verbose), SOURCES.items()))
-        bind_obj = bind.result()
-    tmp = OUT + ".tmp"
-    cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
-    _run(cmd, "link", verbose)
-    os.replace(tmp, OUT)
-    _link_bind(bind_obj, verbose)
+        tmp = OUT + ".tmp"
+        _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs], "link", verbose)
+        os.replace(tmp, OUT)
+        if bind is None:
+            print(f"{os.path.basename(BIND)} not built: {lacks} not found", file=sys.stderr)
+            if os.path.exists(BIND):  # of another build
+                os.remove(BIND)
+        else:
+            _link_bind(bind.result(), verbose)
     return OUT
 
 
