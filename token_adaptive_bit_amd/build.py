@@ -56,6 +56,7 @@ COMMON = [
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     "-fhip-fp32-correctly-rounded-divide-sqrt",
     "-Wno-unused-result",
+    "-Werror=inline-asm",  # registers that assembly may not take (m0 among its clobbers)
     "-I", os.path.join(ROOT, "include"),
 ]
 
@@ -87,6 +88,11 @@ def _spills(remarks: str) -> list:
     return out
 
 
+def _warnings(text: str) -> list:
+    """The warnings of a compiler's output; the host pass's about the GPU feature switched off in COMMON is none."""
+    return [line for line in text.splitlines() if "warning:" in line and "-packed-fp32-ops" not in line]
+
+
 def _compile(src: str, extra: list, verbose: bool) -> str:
     obj = os.path.join(BUILD_DIR, src.replace(".hip", ".o"))
     check = src in SPILL_FREE
@@ -97,6 +103,8 @@ def _compile(src: str, extra: list, verbose: bool) -> str:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"hipcc failed on {src}:\n{res.stdout}\n{res.stderr}")
+    for line in _warnings(res.stderr):
+        print(line, file=sys.stderr, flush=True)
     if check:
         bad = _spills(res.stderr)
         if bad:

@@ -51,6 +51,7 @@ const char* mbq_status_str(mbq_status s) {
     case MBQ_ERR_WORKSPACE: return "workspace missing or too small";
     case MBQ_ERR_DEVICE: return "HIP launch failed";
     case MBQ_ERR_UNSUPPORTED: return "unsupported group, slice count, bit width or ABI version";
+    default: break;  // the range markers and values of no name
   }
   return "unknown status";
 }

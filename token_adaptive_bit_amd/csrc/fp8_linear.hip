@@ -54,17 +54,16 @@ __device__ __forceinline__ void store4(void* y, int64_t row, int32_t n, int32_t 
 
 // 16 (or 4) bytes a lane from memory to LDS, the lanes side by side at l.  Written in
 // assembly because the compiler waits for every copy in flight before any LDS read that
-// follows one of its own (it cannot tell the buffers apart).  The instruction has no
-// register outputs; to_lds_wait() before the barrier completes it.
+// follows one of its own (it cannot tell the buffers apart).  The instruction takes the LDS
+// address from m0, where the compiler puts it (s_nop: one wait state after a write of m0),
+// and has no register outputs; to_lds_wait() before the barrier completes it.
 template <int BYTES>
 __device__ __forceinline__ void to_lds(const void* base, uint32_t offset, const void* l) {  // base, l: the wave's
   const uint32_t at = uint32_t(uintptr_t((const __attribute__((address_space(3))) void*)l));
   if constexpr (BYTES == 16)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 ::"s"(at), "v"(offset), "s"(base) : "memory", "m0");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(at), "v"(offset), "s"(base) : "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dword %1, %2"
-                 ::"s"(at), "v"(offset), "s"(base) : "memory", "m0");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, %2" ::"{m0}"(at), "v"(offset), "s"(base) : "memory");
 }
 // Waits until at most N of the wave's copies are on their way (nothing else of it may be).
 template <int N>
