@@ -70,7 +70,7 @@ typedef enum {
 
 /* Element types.  Any other int32 value is MBQ_ERR_ARG (the range markers make it a valid
    mbq_dtype, so the check itself is defined). */
-typedef enum { MBQ_F32 = 0, MBQ_BF16 = 1, MBQ_E4M3 = 2 /* mbq_fp8_* only */, MBQ_DTYPE_MIN_ = INT32_MIN, MBQ_DTYPE_MAX_ = INT32_MAX } mbq_dtype;
+typedef enum { MBQ_F32 = 0, MBQ_BF16 = 1, MBQ_E4M3 = 2 /* mbq_fp8_* and mbq_block_norm only */, MBQ_DTYPE_MIN_ = INT32_MIN, MBQ_DTYPE_MAX_ = INT32_MAX } mbq_dtype;
 
 /*
  * Kernel and tiling choices of the routed linear, for tests and tuning.  Every call that

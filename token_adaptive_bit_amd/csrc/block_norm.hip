@@ -90,6 +90,8 @@ __global__ __launch_bounds__(1024) void norm_kernel(Args a) {
   // EARLY: everything a row needs is asked for at once, so that the wait for memory is spent
   // once.  With few rows that wait is the time (one row of 5120: 3.6 us from 4.7); with many
   // the registers it takes cost more (13107 x 5120, both norms and a gate: 4.1 TB/s from 4.6).
+  // That holds where the row fills the threads' slots: a wave with a lane past the row's end
+  // takes the way of single elements for it, which begins with a wait for its earlier loads.
   Raw8<XB> rx[V];
   Raw8<RB> rr[V];
   Raw8<false> post_w[V], pre_w[V];

@@ -272,12 +272,14 @@ __global__ __launch_bounds__(256) void join_kernel(LinArgs a) {
 }
 
 // Up to 16 TT tokens: every workgroup streams one row block (gated: the pair), its W
-// waves take every W-th 128-input block, and their sums meet in LDS in a fixed order.  What
-// keeps memory busy is the number of waves on a unit: a set of loads one step ahead in
-// registers was slower (18944 x 3584, 16 tokens: 23.0 us against 17.6).
+// waves take every W-th 128-input block, and their sums meet in LDS in a fixed order.  Of
+// the U blocks of a step a wave has one in flight at a time: the compiler puts each block's
+// loads behind the test that ends the row.  What keeps memory busy is therefore the number of
+// waves on a unit.  (18944 x 3584, 16 tokens, codes in: 14.3 us, 4.8 TB/s.)
 // XT: the type of x.  Codes (MBQ_E4M3) are read from memory, with every block of the weight;
-// a few float tokens are quantized here, once a workgroup into LDS, while the first weight
-// tiles are on their way, which saves the quantizing launch.
+// a few float tokens are quantized here, once a workgroup into LDS, which saves the quantizing
+// launch.  Their loads come after the first U weight tiles' and are waited for in order, so
+// the quantization begins when those tiles are in.
 constexpr int kInlineBlocks = 192;  // most that are quantized in the kernel (their place in LDS)
 
 template <int W, int TT, int XT, int ACT, bool YBF>

@@ -114,7 +114,8 @@ hipError_t launch_fp8_pack(const mbq_fp8_desc& d, int32_t part, const void* w, m
 hipError_t launch_fp8_pad_codes(int32_t t, int32_t k, const void* x, int64_t ldx, void* q, hipStream_t stream);
 hipError_t launch_fp8_quantize(int32_t t, int32_t k, const void* x, bool x_bf16, int64_t ldx, void* q,
                                int64_t ldq, bool pad, float* scale, hipStream_t stream);
-// Bytes of the quantized activations (codes, then scales) the linear keeps in its workspace.
+// Bytes of the linear's workspace: the activations' codes and scales, or a copy of the codes
+// given, then the partial sums of a split K.
 size_t fp8_linear_workspace(const mbq_fp8_desc& d, int32_t t, mbq_dtype x_dtype);
 // act: -1 for the plain linear, an mbq_act for a gated blob.
 hipError_t launch_fp8_linear(const mbq_fp8_desc& d, const void* packed, int32_t t, const void* x,

@@ -84,7 +84,7 @@ struct TopList {
     if (last) floor = from_ordered(uint32_t(last >> 32));
   }
   // Takes in many keys at once: `back` ascends by lane.  (Top 64 with every key offered:
-  // one row of 131072 41.9 us against 20.0, 4096 x 5000 75 against 41.)
+  // one row of 131072 27.7 us against 18.8, 4096 x 5000 54 against 43.)
   __device__ __forceinline__ void absorb(uint64_t back, int lane, int top) {
     mine = max(mine, back);
     merge<64, 32>(mine, lane);
@@ -122,8 +122,8 @@ struct TopList {
   // Raises the floor of a list without real values yet to one that at least `top` of the
   // lanes' x and y (maxima of several logits each) reach, found bit by bit over the upper
   // half of the ordered value: the list then fills with little more than `top` entries, not
-  // with top (1 + ln(n / top)).  (One maximum a lane: 64 x 50021, top 64, 46.5 us against
-  // 22.4.  NaN sorts above all; its row has no list.)
+  // with top (1 + ln(n / top)).  (One maximum a lane: 64 x 50021, top 64, 46.6 us against
+  // 21.6.  NaN sorts above all; its row has no list.)
   __device__ __forceinline__ void start(float x, float y, int top) {
     const uint32_t o = ordered(x), p = ordered(y);
     uint32_t t = 0;
@@ -325,7 +325,8 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
         best[u] = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
       }
       // The same reference in every lane: after the first step the wave's maximum grows a few
-      // times a row, where lanes of their own would each outgrow theirs.
+      // times a row, where lanes of their own would each outgrow theirs.  (Following it within
+      // 2^1.5 and not 2^16.5 costs 2048 x 128000, top 8, 123.9 us against 121.1.)
       const float top_of = fmaxf(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]));
       if (__ballot(top_of > -__builtin_inff() && (sums.r.M == Reference::kNone || sums.r.exponent(top_of, c) > 1.f)))
         sums.refer(wave_max(top_of), c);
@@ -335,8 +336,8 @@ __global__ __launch_bounds__(kThreads) void part_kernel(LpArgs a) {
           list.start(fmaxf(best[0], best[1]), fmaxf(best[2], best[3]), a.top);
           if (a.top > 12 && __ballot(list.mine != 0) == 0) {
             // an empty list: what reaches the floor, side by side in LDS, sorted at once (us
-            // sorted / offered: 64 x 50021 top 8 15.6 / 14.7, top 12 16.1 / 15.8, top 16 16.6 /
-            // 17.1, top 20 17.0 / 18.1)
+            // sorted / offered: 64 x 50021 top 8 14.7 / 13.7, top 12 15.4 / 14.8, top 16 15.6 /
+            // 15.8, top 20 15.7 / 16.8)
             int n = 0;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -469,9 +470,10 @@ __global__ __launch_bounds__(kThreads) void merge_kernel(LpArgs a) {
 }
 
 // Parts of a row: at least 4096 waves (four a SIMD), each with at least one full step of its
-// loop.  (2048 x 128000 bfloat16, top 8: 143 us with two parts a row, 162 with one.  Sixteen
+// loop.  (2048 x 128000 bfloat16, top 8: 124 us with two parts a row, 140 with one.  Sixteen
 // parts in one workgroup, which would save the second launch of a short row, put them on one
-// unit: one row of 32000, top 20, 17.2 us against 15.8, and of 131072, top 8, 29.7 against 14.)
+// unit: an earlier form of this kernel took 17.2 us so against 15.8 for one row of 32000, top
+// 20, and 29.7 against 14 for one of 131072, top 8.)
 int parts_of(int32_t t, int32_t v) {
   const int64_t want = (4096 + int64_t(t) - 1) / std::max(t, 1), most = (int64_t(v) + 2047) / 2048;
   const int p = int(std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), kMaxParts)));
