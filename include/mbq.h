@@ -70,7 +70,7 @@ typedef enum {
 
 /* Element types.  Any other int32 value is MBQ_ERR_ARG (the range markers make it a valid
    mbq_dtype, so the check itself is defined). */
-typedef enum { MBQ_F32 = 0, MBQ_BF16 = 1, MBQ_E4M3 = 2 /* mbq_fp8_* and mbq_block_norm only */, MBQ_DTYPE_MIN_ = INT32_MIN, MBQ_DTYPE_MAX_ = INT32_MAX } mbq_dtype;
+typedef enum { MBQ_F32 = 0, MBQ_BF16 = 1, MBQ_E4M3 = 2 /* mbq_fp8_* and mbq_block_norm only */, MBQ_INT8 = 3 /* mbq_int8_* only */, MBQ_DTYPE_MIN_ = INT32_MIN, MBQ_DTYPE_MAX_ = INT32_MAX } mbq_dtype;
 
 /*
  * Kernel and tiling choices of the routed linear, for tests and tuning.  Every call that
@@ -590,6 +590,153 @@ mbq_status mbq_token_logprobs(int32_t t, int32_t v, const void* logits, mbq_dtyp
                               const void* targets, int32_t target_bits, float inv_temperature, int32_t top,
                               float* logprob, float* entropy, int32_t* rank, int32_t* top_ids,
                               float* top_logprobs, void* workspace, size_t ws_bytes, hipStream_t stream);
+
+/*
+ * ---------------------------------------------------------------------------------------
+ * 8-bit integers with one scale per token and output, for one weight or for experts: ragged
+ * groups of rows with a weight each.  Route, gated half, down projection and combine are the
+ * feed-forward half of a block of experts.
+ *
+ * A quantized row of inputs has one float32 scale; with a = max(max |v|, 2^-96) over the row,
+ *     code = rint(v * (127 / a)),   scale = a / 127
+ * (float32, every operation rounded once, ties to even).  A row that holds a NaN or infinity
+ * has codes 0 and scale NaN.
+ */
+
+/*
+ * Geometry of packed 8-bit integer weights W [experts x n x k] (gated == 0), or of two of the
+ * same shape that read the same inputs, Wg and Wu (gated == 1).  Treat as read-only.
+ *
+ * Blob layout:
+ *   codes  at expert * expert_stride: row_blocks * k_blocks tiles of 2048 bytes, as in
+ *          mbq_fp8_desc (two's complement bytes in place of e4m3).
+ *   scales at +scales_offset: float32 [experts][row_blocks][16], in the order of the tiles'
+ *          rows (0 for rows of the padding).
+ */
+typedef struct {
+  int32_t abi;             /* MBQ_ABI_VERSION */
+  int32_t n, k;            /* outputs of each weight, inputs */
+  int32_t gated;           /* 0: one weight an expert, 1: two interleaved */
+  int32_t experts;         /* 1 for a plain linear */
+  int32_t row_blocks;      /* of an expert: ceil(n / 16) * (gated + 1) */
+  int32_t k_blocks;        /* ceil(k / 128) */
+  int32_t reserved;        /* 0 */
+  uint64_t expert_stride;  /* row_blocks * k_blocks * 2048 */
+  uint64_t scales_offset;  /* experts * expert_stride */
+  uint64_t total_bytes;    /* scales_offset + the scales, rounded up to 256 */
+} mbq_int8_desc;
+
+#define MBQ_MAX_EXPERTS 1024
+#define MBQ_MAX_EXPERT_TOP 32
+
+/* Host only: validates the shape (1 <= n <= 2^24, 1 <= k < 2^17, so that no sum of products
+ * leaves 32 bits, 1 <= experts <= MBQ_MAX_EXPERTS, codes below 64 GiB) and fills *out. */
+mbq_status mbq_int8_describe(int32_t n, int32_t k, int32_t gated, int32_t experts, mbq_int8_desc* out);
+
+/*
+ * Pack the weights of all experts into a blob.
+ *   part:     0 (the weights, or Wg of a gated blob), 1 (Wu).  A gated blob is complete after both.
+ *   w:        [experts x n x k] contiguous: float32 or bfloat16 (quantized here, one scale per
+ *             output, by the formula above), or codes (MBQ_INT8) with
+ *   w_scale:  float32 [experts x n], what a code of that output is multiplied by; must be
+ *             NULL for the other types.
+ *   packed:   desc->total_bytes, 256-byte aligned; every byte of the part is written.
+ *   dev_status: nullable int32; bit 0 is ORed in if w or w_scale holds a non-finite value.
+ */
+mbq_status mbq_int8_pack(const mbq_int8_desc* desc, int32_t part, const void* w, mbq_dtype w_dtype, const float* w_scale,
+                         void* packed, int32_t* dev_status, hipStream_t stream);
+
+/*
+ * Quantize activations x [t x k] (float32 or bfloat16, rows ldx elements apart) per token.
+ *   q:     [t x k] codes, rows ldq bytes apart; only bytes 0 .. k - 1 of a row are written.
+ *   scale: [t] float32.          0 <= t <= 2^21, 1 <= k < 2^17.
+ */
+mbq_status mbq_int8_quantize(int32_t t, int32_t k, const void* x, mbq_dtype x_dtype, int64_t ldx, void* q, int64_t ldq,
+                             float* scale, hipStream_t stream);
+
+/* Arguments of mbq_int8_linear. */
+typedef struct {
+  int32_t t;               /* rows of x, at most 2^21 */
+  int32_t p;               /* rows of y, at most 2^24; t where rows is NULL */
+  int32_t x_dtype;         /* MBQ_F32, MBQ_BF16, or MBQ_INT8 (codes, with x_scale) */
+  int32_t y_dtype;         /* MBQ_F32 or MBQ_BF16 */
+  int32_t act;             /* mbq_act of a gated blob; 0 for a plain one */
+  int32_t reserved;        /* 0 */
+  const void* x;           /* [t x k], rows ldx elements apart */
+  const float* x_scale;    /* [t], of codes; NULL for the other types */
+  const int32_t* offsets;  /* [experts + 1] first row of y of every expert, or NULL: one weight for all rows */
+  const int32_t* rows;     /* [p] row of x behind a row of y, or NULL: the same row */
+  void* y;                 /* [p x n] row-major */
+  void* workspace;         /* mbq_int8_workspace() bytes, 256-byte aligned scratch */
+  uint64_t ws_bytes;
+  int64_t ldx;
+} mbq_int8_args;
+
+/* Host only: bytes of device workspace mbq_int8_linear needs (0 possible); grouped: offsets is
+ * given.  Depends only on desc, t, p, grouped and x_dtype. */
+mbq_status mbq_int8_workspace(const mbq_int8_desc* desc, int32_t t, int32_t p, int32_t grouped, mbq_dtype x_dtype, size_t* bytes);
+
+/*
+ * The 8-bit integer linear, or the gated half on a gated blob, of one weight or of experts:
+ *   y[i][j] = xs[r] ws[e][j] sum_k xq[r][k] wq[e][j][k],          r = rows[i] (i without rows)
+ *   y = act(x . Wg^T) * (x . Wu^T)                                 (gated; neither product reaches memory)
+ * with x quantized within the call, or given as codes and scales of mbq_int8_quantize.
+ * Without offsets the blob has one expert and y a row for each row of x.  With offsets rows
+ * offsets[e] .. offsets[e + 1] - 1 of y belong to expert e (mbq_expert_route); an expert may
+ * have none, and the rows at offsets[experts] and after (a padded batch) are left as they are.
+ * offsets and rows are read on the device: offsets are cut to 0 .. p, and a row index
+ * outside 0 .. t - 1 makes a row of zeros (gated: act(0) * 0); offsets that descend leave
+ * rows unwritten or written twice.  Codes with k % 16 == 0 are read in place and need
+ * ldx % 16 == 0 and 16-byte alignment; for other k they are copied to the workspace.
+ * Sums are exact; a sum is rounded to float32 once and multiplied by the product of the
+ * scales, a gate is float32, and y is rounded once.  A row that holds a NaN or infinity
+ * yields NaN for itself only.  Calls that overlap in time must not share a workspace.
+ */
+mbq_status mbq_int8_linear(const mbq_int8_desc* desc, const void* packed, const mbq_int8_args* args, hipStream_t stream);
+
+/* Host only: bytes of device workspace mbq_expert_route needs.  Depends only on t and experts. */
+mbq_status mbq_expert_route_workspace(int32_t t, int32_t experts, size_t* bytes);
+
+typedef enum {
+  MBQ_SCORE_SOFTMAX = 0, /* exp(l) / sum exp(l), over the chosen (normalize) or all experts */
+  MBQ_SCORE_SIGMOID = 1, /* 1 / (1 + exp(-l)), divided by the chosen ones' sum (normalize) or as it is */
+  MBQ_SCORE_MIN_ = INT32_MIN,
+  MBQ_SCORE_MAX_ = INT32_MAX
+} mbq_score;
+
+/*
+ * Each token's top experts, and the token copies grouped by expert.
+ *   logits:  [t x experts] float32 or bfloat16, rows ld elements apart; -infinity rules an
+ *            expert out for the token.  1 <= experts <= MBQ_MAX_EXPERTS, 0 <= t <= 2^21.
+ *   top:     1 .. min(experts, MBQ_MAX_EXPERT_TOP)
+ *   ids:     [t x top] int32, by descending logit, equal logits by ascending expert; -1 where
+ *            no expert is left.
+ *   weights: [t x top] float32, weight_scale times the score (0 beside an id of -1).
+ *   perm:    [t * top] int32, the token of every grouped row: by expert, then by token; rows
+ *            without a copy (offsets[experts] and after) hold -1.
+ *   offsets: [experts + 1] int32, the first grouped row of every expert.
+ *   place:   [t x top] int32, the grouped row of the token's copy, or -1.
+ * A token whose logits are all -infinity (padding) has no copies.  One whose logits hold a
+ * NaN or +infinity has none either and weights NaN, which mbq_expert_combine makes its
+ * outputs.  Identical from run to run.  With t == 0 offsets is written and nothing else.
+ */
+mbq_status mbq_expert_route(int32_t t, int32_t experts, const void* logits, mbq_dtype dtype, int64_t ld, int32_t top,
+                            mbq_score score, int32_t normalize, float weight_scale, int32_t* ids, float* weights,
+                            int32_t* perm, int32_t* offsets, int32_t* place, void* workspace, size_t ws_bytes,
+                            hipStream_t stream);
+
+/*
+ * The experts' outputs back to the tokens: y[t] = residual[t] + sum_j weights[t][j] rows[place[t][j]],
+ * float32 sums in the order of j, rounded once.
+ *   rows:     [p x n] float32 or bfloat16, ldr elements apart.
+ *   weights, place: [t x top], 1 <= top <= MBQ_MAX_EXPERT_TOP.  A place outside 0 .. p - 1 has no row and adds
+ *             its weight times 0 (nothing, or NaN).
+ *   residual: [t x n] of r_dtype, ldres elements apart, or NULL.
+ *   y:        [t x n] of r_dtype, ldy elements apart; may be residual itself (same ld), but overlap nothing else.
+ */
+mbq_status mbq_expert_combine(int32_t t, int32_t n, int32_t top, int32_t p, const void* rows, mbq_dtype dtype, int64_t ldr,
+                              const float* weights, const int32_t* place, const void* residual, mbq_dtype r_dtype,
+                              int64_t ldres, void* y, int64_t ldy, hipStream_t stream);
 
 /* Static string for a status code. */
 const char* mbq_status_str(mbq_status status);

@@ -14,7 +14,7 @@ import struct
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libmbq.so")
 
-MBQ_F32, MBQ_BF16, MBQ_E4M3 = 0, 1, 2
+MBQ_F32, MBQ_BF16, MBQ_E4M3, MBQ_INT8 = 0, 1, 2, 3
 STATIC_SCRATCH_BYTES = 16 << 20      # MBQ_STATIC_SCRATCH_BYTES
 ABI_VERSION = 3
 
@@ -28,7 +28,9 @@ EXPORTS = ("mbq_describe", "mbq_pack", "mbq_pack_rows", "mbq_pack_bitplane", "mb
            "mbq_linear_lowrank_workspace",
            "mbq_linear_lowrank", "mbq_fp8_describe", "mbq_fp8_pack", "mbq_fp8_quantize",
            "mbq_fp8_linear_workspace", "mbq_fp8_linear", "mbq_fp8_gated", "mbq_block_norm",
-           "mbq_token_logprobs_workspace", "mbq_token_logprobs", "mbq_status_str", "mbq_abi_version")
+           "mbq_token_logprobs_workspace", "mbq_token_logprobs", "mbq_int8_describe", "mbq_int8_pack", "mbq_int8_quantize",
+           "mbq_int8_workspace", "mbq_int8_linear", "mbq_expert_route_workspace", "mbq_expert_route", "mbq_expert_combine",
+           "mbq_status_str", "mbq_abi_version")
 
 
 class MbqDesc(ctypes.Structure):
@@ -58,6 +60,8 @@ MBQ_ACT_SILU, MBQ_ACT_GELU_TANH = 0, 1
 MBQ_NORM_RMS, MBQ_NORM_LAYER = 0, 1
 MBQ_GATE_NONE, MBQ_GATE_CHANNEL, MBQ_GATE_TOKEN, MBQ_GATE_FULL = 0, 1, 2, 3
 MBQ_MAX_TOP = 64
+MBQ_SCORE_SOFTMAX, MBQ_SCORE_SIGMOID = 0, 1
+MBQ_MAX_EXPERTS, MBQ_MAX_EXPERT_TOP = 1024, 32
 
 
 class MbqFp8Desc(ctypes.Structure):
@@ -65,6 +69,19 @@ class MbqFp8Desc(ctypes.Structure):
     _fields_ = [("abi", ctypes.c_int32), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
                 ("gated", ctypes.c_int32), ("row_blocks", ctypes.c_int32), ("k_blocks", ctypes.c_int32),
                 ("scales_offset", ctypes.c_uint64), ("total_bytes", ctypes.c_uint64)]
+
+
+class MbqInt8Desc(ctypes.Structure):
+    """Geometry of packed 8-bit integer weights (mbq_int8_desc in include/mbq.h)."""
+    _fields_ = ([(f, ctypes.c_int32) for f in ("abi", "n", "k", "gated", "experts", "row_blocks", "k_blocks", "reserved")]
+                + [(f, ctypes.c_uint64) for f in ("expert_stride", "scales_offset", "total_bytes")])
+
+
+class MbqInt8Args(ctypes.Structure):
+    """Arguments of mbq_int8_linear (include/mbq.h)."""
+    _fields_ = ([(f, ctypes.c_int32) for f in ("t", "p", "x_dtype", "y_dtype", "act", "reserved")]
+                + [(f, ctypes.c_void_p) for f in ("x", "x_scale", "offsets", "rows", "y", "workspace")]
+                + [("ws_bytes", ctypes.c_uint64), ("ldx", ctypes.c_int64)])
 
 
 class MbqBlockNormArgs(ctypes.Structure):
@@ -133,6 +150,15 @@ def _load() -> ctypes.CDLL:
     lib.mbq_token_logprobs_workspace.argtypes = [I32, I32, I32, P(ctypes.c_size_t)]
     lib.mbq_token_logprobs.argtypes = [I32, I32, VP, I32, I64, VP, I32, F, I32, VP, VP, VP, VP, VP, VP,
                                        ctypes.c_size_t, VP]
+    I8 = P(MbqInt8Desc)
+    lib.mbq_int8_describe.argtypes = [I32, I32, I32, I32, I8]
+    lib.mbq_int8_pack.argtypes = [I8, I32, VP, I32, VP, VP, VP, VP]
+    lib.mbq_int8_quantize.argtypes = [I32, I32, VP, I32, I64, VP, I64, VP, VP]
+    lib.mbq_int8_workspace.argtypes = [I8, I32, I32, I32, I32, P(ctypes.c_size_t)]
+    lib.mbq_int8_linear.argtypes = [I8, VP, P(MbqInt8Args), VP]
+    lib.mbq_expert_route_workspace.argtypes = [I32, I32, P(ctypes.c_size_t)]
+    lib.mbq_expert_route.argtypes = [I32, I32, VP, I32, I64, I32, I32, I32, F, VP, VP, VP, VP, VP, VP, ctypes.c_size_t, VP]
+    lib.mbq_expert_combine.argtypes = [I32, I32, I32, I32, VP, I32, I64, VP, VP, VP, I32, I64, VP, I64, VP]
     lib.mbq_status_str.argtypes = [I32]
     lib.mbq_status_str.restype = ctypes.c_char_p
     lib.mbq_abi_version.argtypes = []
@@ -206,4 +232,23 @@ def fp8_linear_workspace_bytes(desc: MbqFp8Desc, t: int, x_dtype: int) -> int:
 def token_logprobs_workspace_bytes(t: int, v: int, top: int) -> int:
     n = ctypes.c_size_t(0)
     check(LIB.mbq_token_logprobs_workspace(t, v, top, ctypes.byref(n)), "mbq_token_logprobs_workspace")
+    return int(n.value)
+
+
+def int8_describe(n: int, k: int, gated: bool = False, experts: int = 1) -> MbqInt8Desc:
+    d = MbqInt8Desc()
+    check(LIB.mbq_int8_describe(n, k, int(gated), experts, ctypes.byref(d)), "mbq_int8_describe")
+    return d
+
+
+def int8_workspace_bytes(desc: MbqInt8Desc, t: int, p: int, grouped: bool, x_dtype: int) -> int:
+    n = ctypes.c_size_t(0)
+    check(LIB.mbq_int8_workspace(ctypes.byref(desc), t, p, int(grouped), x_dtype, ctypes.byref(n)), "mbq_int8_workspace")
+    return int(n.value)
+
+
+@functools.lru_cache(maxsize=256)
+def expert_route_workspace_bytes(t: int, experts: int) -> int:
+    n = ctypes.c_size_t(0)
+    check(LIB.mbq_expert_route_workspace(t, experts, ctypes.byref(n)), "mbq_expert_route_workspace")
     return int(n.value)

@@ -15,9 +15,9 @@ from typing import NamedTuple
 import torch
 
 from . import _lib
-from ._lib import (MBQ_BF16, MBQ_E4M3, MBQ_F32, MBQ_MUL_AUTO, MBQ_MUL_BF16, MBQ_MUL_FP8_FP4, MBQ_PATH_AUTO,
-                   MBQ_PATH_GENERIC, MbqDesc, MbqError, MbqFp8Desc, MbqOpts, check, describe,
-                   fp8_describe)
+from ._lib import (MBQ_BF16, MBQ_E4M3, MBQ_F32, MBQ_INT8, MBQ_MUL_AUTO, MBQ_MUL_BF16, MBQ_MUL_FP8_FP4, MBQ_PATH_AUTO,
+                   MBQ_PATH_GENERIC, MbqDesc, MbqError, MbqFp8Desc, MbqInt8Desc, MbqOpts, check, describe,
+                   fp8_describe, int8_describe)
 
 try:
     from . import _bind  # after _lib: the library and torch's runtime are loaded
@@ -32,7 +32,10 @@ __all__ = ["PackedLinear", "pack", "pack_bitplane", "pack_concat", "route", "rou
            "linear_lowrank_workspace", "route_linear", "route_linear_workspace", "linear_static", "opts",
            "route_prepare", "route_prepare_workspace", "route_linear_prepared",
            "Fp8Linear", "fp8_describe", "fp8_pack", "fp8_pack_gated", "fp8_quantize", "fp8_linear", "fp8_gated",
-           "fp8_linear_workspace", "block_norm", "TokenLogprobs", "token_logprobs", "token_logprobs_workspace"]
+           "fp8_linear_workspace", "block_norm", "TokenLogprobs", "token_logprobs", "token_logprobs_workspace",
+           "Int8Linear", "int8_describe", "int8_pack", "int8_pack_gated", "int8_quantize", "int8_linear", "int8_gated",
+           "int8_workspace", "expert_pack", "expert_pack_gated", "ExpertRoute", "expert_route", "expert_route_workspace",
+           "expert_linear", "expert_gated", "expert_combine"]
 
 _FLOATS = (torch.float32, torch.bfloat16)
 
@@ -838,3 +841,278 @@ def token_logprobs(logits: torch.Tensor, targets: torch.Tensor, top: int = 0, in
                                       logprob.data_ptr(), entropy.data_ptr(), rank.data_ptr(), ids_ptr, best_ptr, ws_ptr,
                                       ws_bytes, _stream_of(logits)), "mbq_token_logprobs")
     return TokenLogprobs(logprob, entropy, rank, ids, best)
+
+
+# --- 8-bit integers with one scale per token and output, for one weight or for experts: ragged
+# --- groups of rows with a weight each.  expert_route, expert_gated, expert_linear and
+# --- expert_combine are the feed-forward half of a block of experts.
+
+_INT_CODE = {torch.float32: MBQ_F32, torch.bfloat16: MBQ_BF16, torch.int8: MBQ_INT8}
+_I8S, _I32S = (torch.int8,), (torch.int32,)
+
+
+@dataclass
+class Int8Linear:
+    """Packed 8-bit integer weights (of one linear or of experts; of a gated half both): geometry plus the blob."""
+    desc: MbqInt8Desc
+    blob: torch.Tensor
+
+    def __post_init__(self):
+        self._sizes = {}
+
+    @property
+    def n(self): return self.desc.n
+
+    @property
+    def k(self): return self.desc.k
+
+    @property
+    def gated(self): return bool(self.desc.gated)
+
+    @property
+    def experts(self): return self.desc.experts
+
+    def _workspace_bytes(self, t: int, p: int, grouped: bool, code: int) -> int:
+        """Sizes already asked for, by rows and type (they depend on nothing else)."""
+        key = (t, p, grouped, code)
+        need = self._sizes.get(key)
+        if need is None:
+            need = _lib.int8_workspace_bytes(self.desc, t, p, grouped, code)
+            if len(self._sizes) < 4096:  # a batch of any size may come
+                self._sizes[key] = need
+        return need
+
+
+def _int8_pack(ws, scales, status, out, dims: int) -> Int8Linear:
+    for w, s in zip(ws, scales):
+        _dev(w, "w")
+        if w.dim() != dims or w.dtype not in _INT_CODE:
+            raise TypeError(f"w must be a {dims}-D float32, bfloat16 or int8 tensor")
+        if w.shape != ws[0].shape:
+            raise ValueError(f"both weights must have one shape, got {tuple(ws[0].shape)} and {tuple(w.shape)}")
+        if w.device != ws[0].device:
+            raise ValueError("both weights must be on one device")
+        if (w.dtype == torch.int8) != (s is not None):
+            raise TypeError("an int8 weight needs its scale, and only that")
+        _opt(s, "scale", tuple(w.shape[:-1]), _F32S, w.device)
+    shape, dev = ws[0].shape, ws[0].device
+    _opt(status, "status", (1,), _I32S, dev)
+    d = int8_describe(shape[-2], shape[-1], len(ws) == 2, shape[0] if dims == 3 else 1)
+    if out is None:
+        out = torch.empty(int(d.total_bytes), dtype=torch.uint8, device=dev)
+    _workspace(out, "out", int(d.total_bytes), dev)
+    stream = _stream_of(ws[0])
+    for part, (w, s) in enumerate(zip(ws, scales)):
+        check(_lib.LIB.mbq_int8_pack(ctypes.byref(d), part, _p(w), _INT_CODE[w.dtype], _p(s), _p(out), _p(status), stream),
+              "mbq_int8_pack")
+    return Int8Linear(d, out)
+
+
+def int8_pack(w: torch.Tensor, scale: torch.Tensor | None = None, status: torch.Tensor | None = None,
+              out: torch.Tensor | None = None) -> Int8Linear:
+    """8-bit integer pack of W [n, k]: float32 or bfloat16 (quantized, one scale per output), or
+    int8 codes with their scale [n] float32."""
+    return _int8_pack((w,), (scale,), status, out, 2)
+
+
+def int8_pack_gated(w_gate: torch.Tensor, w_up: torch.Tensor, scale_gate: torch.Tensor | None = None,
+                    scale_up: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                    out: torch.Tensor | None = None) -> Int8Linear:
+    """The two weights [n, k] of a gated half in one blob, for int8_gated."""
+    return _int8_pack((w_gate, w_up), (scale_gate, scale_up), status, out, 2)
+
+
+def expert_pack(w: torch.Tensor, scale: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                out: torch.Tensor | None = None) -> Int8Linear:
+    """The weights [experts, n, k] of expert_linear: float32, bfloat16, or int8 codes with their scale [experts, n]."""
+    return _int8_pack((w,), (scale,), status, out, 3)
+
+
+def expert_pack_gated(w_gate: torch.Tensor, w_up: torch.Tensor, scale_gate: torch.Tensor | None = None,
+                      scale_up: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                      out: torch.Tensor | None = None) -> Int8Linear:
+    """The two weights [experts, n, k] of the experts' gated halves in one blob, for expert_gated."""
+    return _int8_pack((w_gate, w_up), (scale_gate, scale_up), status, out, 3)
+
+
+def int8_quantize(x: torch.Tensor, q: torch.Tensor | None = None, scale: torch.Tensor | None = None):
+    """8-bit integer codes of x [t, k] per token.  Returns (q [t, k] int8, scale [t] float32): x is
+    about q * scale[:, None]."""
+    ldx = _rows(x, "x", _FLOATS)
+    t, k = x.shape
+    dev = x.get_device()
+    if q is None:
+        q = torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format)
+    ldq = _rows(q, "q", _I8S, dev, (t, k))
+    if scale is None:
+        scale = torch.empty(t, dtype=torch.float32, device=x.device)
+    check(_lib.LIB.mbq_int8_quantize(t, k, x.data_ptr(), _CODE[x.dtype], ldx, q.data_ptr(), ldq,
+                                     _flat(scale, "scale", _F32S, dev, (t,)), _stream_of(x)), "mbq_int8_quantize")
+    return q, scale
+
+
+def int8_workspace(p: Int8Linear, t: int, x_dtype=torch.bfloat16, rows: int | None = None) -> int:
+    """Bytes of workspace for t rows of x: of int8_linear / int8_gated, or with rows (those of y) of
+    expert_linear / expert_gated."""
+    return p._workspace_bytes(t, t if rows is None else rows, rows is not None, _INT_CODE[x_dtype])
+
+
+def _int8_run(p, x, scale, act, offsets, rows, out_dtype, y, workspace):
+    if y is None and workspace is None and _bound(x):
+        r = _bind.int8(ctypes.addressof(p.desc), p.blob, x, scale, act, offsets, rows, out_dtype, dev := _current_device(),
+                       _raw_stream(dev))
+        if r is not None:
+            return r
+    ldx = _rows(x, "x", _INT_CODE)
+    t, k = x.shape
+    dev, code, d, blob = x.get_device(), _INT_CODE[x.dtype], p.desc, p.blob
+    if k != d.k:
+        raise ValueError(f"x has {k} inputs, the weight {d.k}")
+    if blob.dtype != torch.uint8 or blob.get_device() != dev or not blob.is_contiguous() or blob.numel() < d.total_bytes:
+        raise ValueError(f"packed blob must be contiguous uint8 on cuda:{dev} holding at least desc.total_bytes")
+    s_ptr = offsets_ptr = rows_ptr = None
+    if code == MBQ_INT8:
+        s_ptr = _flat(scale, "scale", _F32S, dev, (t,))
+    elif scale is not None:
+        raise TypeError("scale belongs to int8 activations")
+    m = t
+    if offsets is not None:
+        offsets_ptr = _flat(offsets, "offsets", _I32S, dev, (d.experts + 1,))
+        if rows is not None:
+            _dev(rows, "rows")
+            if rows.dim() != 1:
+                raise ValueError("rows must be 1-D")
+            m = rows.numel()
+            rows_ptr = _flat(rows, "rows", _I32S, dev, (m,))
+    if y is None:
+        y = torch.empty(m, d.n, dtype=out_dtype or (torch.bfloat16 if code == MBQ_INT8 else x.dtype), device=x.device)
+    y_ptr = _flat(y, "y", _FLOATS, dev, (m, d.n))
+    _ws, ws_ptr, ws_bytes = _scratch(workspace, p._workspace_bytes(t, m, offsets is not None, code), x)
+    args = _lib.MbqInt8Args(t, m, code, _CODE[y.dtype], act, 0, x.data_ptr(), s_ptr, offsets_ptr, rows_ptr, y_ptr, ws_ptr,
+                            ws_bytes, ldx)
+    check(_lib.LIB.mbq_int8_linear(ctypes.byref(d), blob.data_ptr(), ctypes.byref(args), _stream_of(x)), "mbq_int8_linear")
+    return y
+
+
+def _int8_kind(p, gated: bool, experts: bool, act: str = "silu") -> int:
+    if p.desc.gated != gated:
+        raise ValueError(f"a {'plain' if gated else 'gated'} blob needs {'expert' if experts else 'int8'}_{'linear' if gated else 'gated'}")
+    if not experts and p.desc.experts != 1:
+        raise ValueError("a blob of several experts needs expert_linear or expert_gated")
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {sorted(_ACTS)}")
+    return _ACTS[act] if gated else 0
+
+
+def int8_linear(p: Int8Linear, x: torch.Tensor, scale: torch.Tensor | None = None, out_dtype: torch.dtype | None = None,
+                y: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """8-bit integer linear y = x . W^T: x [t, k] float32 or bfloat16 (quantized per token within
+    the call), or the codes and scale of int8_quantize."""
+    return _int8_run(p, x, scale, _int8_kind(p, False, False), None, None, out_dtype, y, workspace)
+
+
+def int8_gated(p: Int8Linear, x: torch.Tensor, scale: torch.Tensor | None = None, act: str = "silu",
+               out_dtype: torch.dtype | None = None, y: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Gated half of a feed-forward block: act(x . Wg^T) * (x . Wu^T) on a gated blob."""
+    return _int8_run(p, x, scale, _int8_kind(p, True, False, act), None, None, out_dtype, y, workspace)
+
+
+def expert_linear(p: Int8Linear, x: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor | None = None,
+                  scale: torch.Tensor | None = None, out_dtype: torch.dtype | None = None, y: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The products of ragged groups of rows with their experts' weights: rows offsets[e] ..
+    offsets[e + 1] - 1 of y are x . W[e]^T.  x holds the rows themselves, or with rows (int32, as
+    perm of expert_route) row i of y takes row rows[i] of x.  y rows at offsets[experts] and
+    after are left as they are."""
+    if offsets is None:
+        raise TypeError("offsets must be a tensor")
+    return _int8_run(p, x, scale, _int8_kind(p, False, True), offsets, rows, out_dtype, y, workspace)
+
+
+def expert_gated(p: Int8Linear, x: torch.Tensor, offsets: torch.Tensor, rows: torch.Tensor | None = None,
+                 scale: torch.Tensor | None = None, act: str = "silu", out_dtype: torch.dtype | None = None,
+                 y: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """The experts' gated halves, act(x . Wg[e]^T) * (x . Wu[e]^T), on a gated blob; rows as in expert_linear."""
+    if offsets is None:
+        raise TypeError("offsets must be a tensor")
+    return _int8_run(p, x, scale, _int8_kind(p, True, True, act), offsets, rows, out_dtype, y, workspace)
+
+
+class ExpertRoute(NamedTuple):
+    """Per token its experts (-1: none) and their weights [t, top], the token of every grouped row
+    [t * top] (-1: no copy), the first grouped row of every expert [experts + 1], and the grouped
+    row of every copy [t, top] (-1: none)."""
+    ids: torch.Tensor
+    weights: torch.Tensor
+    perm: torch.Tensor
+    offsets: torch.Tensor
+    place: torch.Tensor
+
+
+_SCORES = {"softmax": _lib.MBQ_SCORE_SOFTMAX, "sigmoid": _lib.MBQ_SCORE_SIGMOID}
+
+
+def expert_route_workspace(t: int, experts: int) -> int:
+    return _lib.expert_route_workspace_bytes(t, experts)
+
+
+def expert_route(logits: torch.Tensor, top: int, score: str = "softmax", normalize: bool = True, weight_scale: float = 1.0,
+                 workspace: torch.Tensor | None = None) -> ExpertRoute:
+    """Each token's top experts from its logits [t, experts] (equal logits: the lower expert; -infinity
+    rules one out), their weights (softmax or sigmoid scores, normalized over the chosen ones or
+    not, times weight_scale), and the copies grouped by expert, then by token."""
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}")
+    if workspace is None and _bound(logits):
+        r = _bind.expert_route(logits, top, _SCORES[score], normalize, weight_scale, dev := _current_device(), _raw_stream(dev))
+        if r is not None:
+            return ExpertRoute._make(r)
+    ld = _rows(logits, "logits", _FLOATS)
+    t, e = logits.shape
+    if not 1 <= top <= min(e, _lib.MBQ_MAX_EXPERT_TOP):
+        raise ValueError(f"top must lie in 1 .. {min(e, _lib.MBQ_MAX_EXPERT_TOP)}")
+    need = _lib.expert_route_workspace_bytes(t, e)
+    weights = torch.empty(t, top, dtype=torch.float32, device=logits.device)
+    ids, place = torch.empty_like(weights, dtype=torch.int32), torch.empty_like(weights, dtype=torch.int32)
+    perm = torch.empty(t * top, dtype=torch.int32, device=logits.device)
+    offsets = torch.empty(e + 1, dtype=torch.int32, device=logits.device)
+    _ws, ws_ptr, ws_bytes = _scratch(workspace, need, logits)
+    check(_lib.LIB.mbq_expert_route(t, e, logits.data_ptr(), _CODE[logits.dtype], ld, top, _SCORES[score], bool(normalize),
+                                    weight_scale, ids.data_ptr(), weights.data_ptr(), perm.data_ptr(), offsets.data_ptr(),
+                                    place.data_ptr(), ws_ptr, ws_bytes, _stream_of(logits)), "mbq_expert_route")
+    return ExpertRoute(ids, weights, perm, offsets, place)
+
+
+def expert_combine(rows: torch.Tensor, weights: torch.Tensor, place: torch.Tensor, residual: torch.Tensor | None = None,
+                   out_dtype: torch.dtype | None = None, y: torch.Tensor | None = None) -> torch.Tensor:
+    """y[t] = residual[t] + sum_j weights[t, j] * rows[place[t, j]]: rows [p, n], weights and place
+    [t, top] of expert_route (a place of -1 has no row), residual [t, n] or None.  y has residual's
+    type (without one rows' type, or out_dtype) and may be residual itself."""
+    if y is None and _bound(rows):
+        r = _bind.expert_combine(rows, weights, place, residual, out_dtype, dev := _current_device(), _raw_stream(dev))
+        if r is not None:
+            return r
+    ldr = _rows(rows, "rows", _FLOATS)
+    p, n = rows.shape
+    dev = rows.get_device()
+    _dev(weights, "weights")
+    if weights.dim() != 2:
+        raise ValueError("weights must be 2-D [t, top]")
+    t, top = weights.shape
+    w_ptr, place_ptr = _flat(weights, "weights", _F32S, dev, (t, top)), _flat(place, "place", _I32S, dev, (t, top))
+    r_ptr, ldres, r_dtype = None, n, out_dtype or rows.dtype
+    if residual is not None:
+        ldres, r_ptr = _rows(residual, "residual", _FLOATS, dev, (t, n)), residual.data_ptr()
+        if out_dtype not in (None, residual.dtype):
+            raise TypeError(f"out_dtype {out_dtype}, residual has {residual.dtype}")
+        r_dtype = residual.dtype
+    if r_dtype not in _FLOATS:
+        raise TypeError(f"out_dtype {r_dtype}, expected float32 or bfloat16")
+    if y is None:
+        y, ldy = torch.empty(t, n, dtype=r_dtype, device=rows.device), n
+    else:
+        ldy = _rows(y, "y", (r_dtype,), dev, (t, n))
+    check(_lib.LIB.mbq_expert_combine(t, n, top, p, rows.data_ptr(), _CODE[rows.dtype], ldr, w_ptr, place_ptr, r_ptr,
+                                      _CODE[r_dtype], ldres, y.data_ptr(), ldy, _stream_of(rows)), "mbq_expert_combine")
+    return y

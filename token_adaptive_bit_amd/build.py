@@ -42,6 +42,9 @@ SOURCES = {
     "fp8_linear.hip": [],
     "block_norm.hip": [],
     "token_logprobs.hip": [],
+    "int8_quant.hip": [],
+    "int8_linear.hip": [],
+    "experts.hip": [],
 }
 
 # Translation units whose kernels must not spill registers: their load pipelines rely on
@@ -49,7 +52,8 @@ SOURCES = {
 # stores) would stall, and the variants a launcher can pick are chosen to fit.  The build
 # reads the compiler's resource-usage remarks and fails on any spill to scratch memory.
 SPILL_FREE = ("decode_stream.hip", "prefill_mfma.hip", "route_mlp.hip", "lowrank.hip",
-              "fp8_quant.hip", "fp8_linear.hip", "block_norm.hip", "token_logprobs.hip")
+              "fp8_quant.hip", "fp8_linear.hip", "block_norm.hip", "token_logprobs.hip",
+              "int8_quant.hip", "int8_linear.hip", "experts.hip")
 
 COMMON = [
     "--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17",

@@ -618,4 +618,136 @@ mbq_status mbq_token_logprobs(int32_t t, int32_t v, const void* logits, mbq_dtyp
                                              workspace, stream));
 }
 
+mbq_status mbq_int8_describe(int32_t n, int32_t k, int32_t gated, int32_t experts, mbq_int8_desc* out) {
+  if (!out || (gated != 0 && gated != 1)) return MBQ_ERR_ARG;
+  if (n < 1 || k < 1 || n > (1 << 24) || k >= (1 << 17) || experts < 1 || experts > MBQ_MAX_EXPERTS) return MBQ_ERR_SHAPE;
+  mbq_int8_desc d{};
+  d.abi = MBQ_ABI_VERSION;
+  d.n = n;
+  d.k = k;
+  d.gated = gated;
+  d.experts = experts;
+  d.row_blocks = (n + mbq::kRowBlock - 1) / mbq::kRowBlock * (gated + 1);
+  d.k_blocks = (k + mbq::kFp8Block - 1) / mbq::kFp8Block;
+  d.expert_stride = uint64_t(d.row_blocks) * d.k_blocks * mbq::kFp8TileBytes;
+  d.scales_offset = d.expert_stride * experts;
+  if (d.scales_offset >= (uint64_t(1) << 36)) return MBQ_ERR_SHAPE;  // 64 GiB: grids stay in range
+  d.total_bytes = d.scales_offset + align256(uint64_t(experts) * d.row_blocks * mbq::kRowBlock * 4);
+  *out = d;
+  return MBQ_OK;
+}
+
+namespace {
+mbq_status check_int8_desc(const mbq_int8_desc* d) {
+  if (!d) return MBQ_ERR_ARG;
+  if (d->abi != MBQ_ABI_VERSION) return MBQ_ERR_UNSUPPORTED;
+  mbq_int8_desc ref;
+  const mbq_status st = mbq_int8_describe(d->n, d->k, d->gated, d->experts, &ref);
+  if (st != MBQ_OK) return st;
+  if (ref.row_blocks != d->row_blocks || ref.k_blocks != d->k_blocks || ref.expert_stride != d->expert_stride ||
+      ref.scales_offset != d->scales_offset || ref.total_bytes != d->total_bytes)
+    return MBQ_ERR_SHAPE;
+  return MBQ_OK;
+}
+bool valid_copies(int32_t p) { return p >= 0 && p <= (1 << 24); }
+bool valid_int8_x(int32_t t) { return t == MBQ_F32 || t == MBQ_BF16 || t == MBQ_INT8; }
+bool valid_float(int32_t t) { return t == MBQ_F32 || t == MBQ_BF16; }
+}  // namespace
+
+mbq_status mbq_int8_pack(const mbq_int8_desc* desc, int32_t part, const void* w, mbq_dtype w_dtype, const float* w_scale,
+                         void* packed, int32_t* dev_status, hipStream_t stream) {
+  const mbq_status st = check_int8_desc(desc);
+  if (st != MBQ_OK) return st;
+  if (part < 0 || part > desc->gated || !valid_int8_x(w_dtype)) return MBQ_ERR_ARG;
+  if (!w || !packed || (w_dtype == MBQ_INT8) != (w_scale != nullptr)) return MBQ_ERR_ARG;
+  if (!aligned(packed, 256) || !aligned(w, element(w_dtype)) || !aligned(w_scale, 4) || !aligned(dev_status, 4))
+    return MBQ_ERR_ARG;
+  return launched(mbq::launch_int8_pack(*desc, part, w, w_dtype, w_scale, packed, dev_status, stream));
+}
+
+mbq_status mbq_int8_quantize(int32_t t, int32_t k, const void* x, mbq_dtype x_dtype, int64_t ldx, void* q, int64_t ldq,
+                             float* scale, hipStream_t stream) {
+  if (!valid_dtype(x_dtype)) return MBQ_ERR_ARG;
+  if (!valid_rows(t) || k < 1 || k >= (1 << 17)) return MBQ_ERR_SHAPE;
+  if (t == 0) return MBQ_OK;
+  if (!x || !q || !scale || !aligned(x, element(x_dtype)) || !aligned(scale, 4)) return MBQ_ERR_ARG;
+  if (ldx < k || ldq < k) return MBQ_ERR_SHAPE;
+  return launched(mbq::launch_int8_quantize(t, k, x, x_dtype == MBQ_BF16, ldx, q, ldq, false, scale, stream));
+}
+
+mbq_status mbq_int8_workspace(const mbq_int8_desc* desc, int32_t t, int32_t p, int32_t grouped, mbq_dtype x_dtype, size_t* bytes) {
+  const mbq_status st = check_int8_desc(desc);
+  if (st != MBQ_OK) return st;
+  if (!bytes || !valid_int8_x(x_dtype) || (grouped != 0 && grouped != 1)) return MBQ_ERR_ARG;
+  if (!valid_rows(t) || !valid_copies(p) || (!grouped && (p != t || desc->experts != 1))) return MBQ_ERR_SHAPE;
+  *bytes = mbq::int8_workspace(*desc, t, p, grouped != 0, x_dtype);
+  return MBQ_OK;
+}
+
+mbq_status mbq_int8_linear(const mbq_int8_desc* desc, const void* packed, const mbq_int8_args* a, hipStream_t stream) {
+  const mbq_status st = check_int8_desc(desc);
+  if (st != MBQ_OK) return st;
+  if (!a || !valid_int8_x(a->x_dtype) || !valid_float(a->y_dtype) || a->reserved != 0) return MBQ_ERR_ARG;
+  if (desc->gated ? a->act != MBQ_ACT_SILU && a->act != MBQ_ACT_GELU_TANH : a->act != 0) return MBQ_ERR_ARG;
+  if (!valid_rows(a->t) || !valid_copies(a->p) || int64_t(a->p) * desc->n >= (int64_t(1) << 38)) return MBQ_ERR_SHAPE;
+  if (a->rows ? !a->offsets : a->p != a->t) return a->rows ? MBQ_ERR_ARG : MBQ_ERR_SHAPE;
+  if (!a->offsets && desc->experts != 1) return MBQ_ERR_UNSUPPORTED;
+  if (a->p == 0) return MBQ_OK;
+  if (a->t == 0) return MBQ_ERR_SHAPE;  // rows of y and none of x
+  const bool codes = a->x_dtype == MBQ_INT8, direct = codes && desc->k % 16 == 0;
+  if (!packed || !a->x || !a->y || codes != (a->x_scale != nullptr)) return MBQ_ERR_ARG;
+  const uintptr_t xe = a->x_dtype == MBQ_INT8 ? 1 : element(a->x_dtype);
+  if (!aligned(packed, 256) || !aligned(a->x, direct ? 16 : xe) || !aligned(a->x_scale, 4) || !aligned(a->offsets, 4) ||
+      !aligned(a->rows, 4) || !aligned(a->y, element(a->y_dtype)))
+    return MBQ_ERR_ARG;
+  if (a->ldx < desc->k || (direct && a->ldx % 16 != 0)) return MBQ_ERR_SHAPE;
+  const size_t need = mbq::int8_workspace(*desc, a->t, a->p, a->offsets != nullptr, mbq_dtype(a->x_dtype));
+  if (need && (!a->workspace || a->ws_bytes < need || !aligned(a->workspace, 256))) return MBQ_ERR_WORKSPACE;
+  return launched(mbq::launch_int8_linear(*desc, packed, *a, stream));
+}
+
+mbq_status mbq_expert_route_workspace(int32_t t, int32_t experts, size_t* bytes) {
+  if (!bytes) return MBQ_ERR_ARG;
+  if (!valid_rows(t) || experts < 1 || experts > MBQ_MAX_EXPERTS) return MBQ_ERR_SHAPE;
+  *bytes = mbq::expert_route_workspace(t, experts);
+  return MBQ_OK;
+}
+
+mbq_status mbq_expert_route(int32_t t, int32_t experts, const void* logits, mbq_dtype dtype, int64_t ld, int32_t top,
+                            mbq_score score, int32_t normalize, float weight_scale, int32_t* ids, float* weights,
+                            int32_t* perm, int32_t* offsets, int32_t* place, void* workspace, size_t ws_bytes,
+                            hipStream_t stream) {
+  if (!valid_dtype(dtype) || (score != MBQ_SCORE_SOFTMAX && score != MBQ_SCORE_SIGMOID) || (normalize != 0 && normalize != 1))
+    return MBQ_ERR_ARG;
+  if (!valid_rows(t) || experts < 1 || experts > MBQ_MAX_EXPERTS || top < 1 || top > experts || top > MBQ_MAX_EXPERT_TOP)
+    return MBQ_ERR_SHAPE;
+  if (!std::isfinite(weight_scale)) return MBQ_ERR_RANGE;
+  if (!offsets || !aligned(offsets, 4)) return MBQ_ERR_ARG;
+  if (t > 0) {
+    if (ld < experts) return MBQ_ERR_SHAPE;
+    if (!logits || !ids || !weights || !perm || !place || !aligned(logits, element(dtype)) || !aligned(ids, 4) ||
+        !aligned(weights, 4) || !aligned(perm, 4) || !aligned(place, 4))
+      return MBQ_ERR_ARG;
+  }
+  const size_t need = mbq::expert_route_workspace(t, experts);
+  if (need && (!workspace || ws_bytes < need || !aligned(workspace, 256))) return MBQ_ERR_WORKSPACE;
+  return launched(mbq::launch_expert_route(t, experts, logits, dtype == MBQ_BF16, ld, top, score == MBQ_SCORE_SIGMOID,
+                                           normalize != 0, weight_scale, ids, weights, perm, offsets, place, workspace, stream));
+}
+
+mbq_status mbq_expert_combine(int32_t t, int32_t n, int32_t top, int32_t p, const void* rows, mbq_dtype dtype, int64_t ldr,
+                              const float* weights, const int32_t* place, const void* residual, mbq_dtype r_dtype,
+                              int64_t ldres, void* y, int64_t ldy, hipStream_t stream) {
+  if (!valid_dtype(dtype) || !valid_dtype(r_dtype)) return MBQ_ERR_ARG;
+  if (!valid_rows(t) || !valid_copies(p) || n < 1 || n > (1 << 24) || top < 1 || top > MBQ_MAX_EXPERT_TOP) return MBQ_ERR_SHAPE;
+  if (t == 0) return MBQ_OK;
+  if ((p > 0 && !rows) || !weights || !place || !y) return MBQ_ERR_ARG;
+  if (!aligned(rows, element(dtype)) || !aligned(weights, 4) || !aligned(place, 4) || !aligned(residual, element(r_dtype)) ||
+      !aligned(y, element(r_dtype)))
+    return MBQ_ERR_ARG;
+  if (ldr < n || ldy < n || (residual && ldres < n) || (y == residual && ldy != ldres)) return MBQ_ERR_SHAPE;
+  return launched(mbq::launch_expert_combine(t, n, top, p, rows, dtype == MBQ_BF16, ldr, weights, place, residual,
+                                             r_dtype == MBQ_BF16, ldres, y, ldy, stream));
+}
+
 }  // extern "C"

@@ -211,6 +211,124 @@ PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
                        THPVariable_Wrap(ids), THPVariable_Wrap(best));
 }
 
+// (desc address, blob, x, scale, act, offsets, rows, out_dtype, device, stream) -> y
+PyObject* int8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 10) return PyErr_Format(PyExc_TypeError, "int8 takes 10 arguments");
+  const auto* d = static_cast<const mbq_int8_desc*>(PyLong_AsVoidPtr(a[0]));
+  const long act = PyLong_AsLong(a[4]);
+  const int64_t device = PyLong_AsLongLong(a[8]);
+  void* stream = PyLong_AsVoidPtr(a[9]);
+  if (PyErr_Occurred()) return nullptr;
+  const at::Tensor *blob = tensor(a[1]), *x = tensor(a[2]);
+  if (!plain(x, device, 2) || !plain(blob, device, 1)) Py_RETURN_NONE;
+  const int64_t t = x->size(0);
+  const at::ScalarType xt = x->scalar_type();
+  if (x->size(1) != d->k || t > (1 << 21) || blob->scalar_type() != at::kByte || uint64_t(blob->numel()) < d->total_bytes)
+    Py_RETURN_NONE;
+  mbq_int8_args g = {};
+  if (xt == at::kChar) {
+    const at::Tensor* s = tensor(a[3]);
+    if (!plain(s, device, 1) || s->scalar_type() != at::kFloat || s->size(0) != t) Py_RETURN_NONE;
+    g.x_scale = static_cast<const float*>(s->data_ptr());
+  } else if (!is_float(xt) || a[3] != Py_None) {
+    Py_RETURN_NONE;
+  }
+  int64_t p = t;
+  if (a[5] != Py_None) {
+    const at::Tensor* o = tensor(a[5]);
+    if (!plain(o, device, 1) || o->scalar_type() != at::kInt || o->size(0) != int64_t(d->experts) + 1) Py_RETURN_NONE;
+    g.offsets = static_cast<const int32_t*>(o->data_ptr());
+    if (a[6] != Py_None) {
+      const at::Tensor* r = tensor(a[6]);
+      if (!plain(r, device, 1) || r->scalar_type() != at::kInt || r->size(0) > (1 << 24)) Py_RETURN_NONE;
+      p = r->size(0);
+      g.rows = static_cast<const int32_t*>(r->data_ptr());
+    }
+  }
+  at::ScalarType yt;
+  size_t need = 0;
+  g.t = int32_t(t);
+  g.p = int32_t(p);
+  g.x_dtype = xt == at::kChar ? MBQ_INT8 : code(xt);
+  if (!out_type(a[7], xt == at::kChar ? at::kBFloat16 : xt, yt) ||
+      mbq_int8_workspace(d, g.t, g.p, g.offsets != nullptr, mbq_dtype(g.x_dtype), &need) != MBQ_OK)
+    Py_RETURN_NONE;
+  at::AutoDispatchBelowADInplaceOrView guard;
+  const at::Tensor y = empty({p, d->n}, yt, *x);
+  at::Tensor ws;
+  if (need) ws = empty({int64_t(need)}, at::kByte, *x);
+  g.y_dtype = code(yt);
+  g.act = int32_t(act);
+  g.x = x->data_ptr();
+  g.y = y.data_ptr();
+  g.workspace = need ? ws.data_ptr() : nullptr;
+  g.ws_bytes = need;
+  g.ldx = d->k;
+  if (mbq_int8_linear(d, blob->data_ptr(), &g, static_cast<hipStream_t>(stream)) != MBQ_OK) Py_RETURN_NONE;
+  return THPVariable_Wrap(y);
+}
+
+// (logits, top, score, normalize, weight_scale, device, stream) -> (ids, weights, perm, offsets, place)
+PyObject* expert_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 7) return PyErr_Format(PyExc_TypeError, "expert_route takes 7 arguments");
+  const long top = PyLong_AsLong(a[1]), score = PyLong_AsLong(a[2]);
+  const int normalize = PyObject_IsTrue(a[3]);
+  const float weight_scale = float(PyFloat_AsDouble(a[4]));
+  const int64_t device = PyLong_AsLongLong(a[5]);
+  void* stream = PyLong_AsVoidPtr(a[6]);
+  if (PyErr_Occurred()) return nullptr;
+  const at::Tensor* x = tensor(a[0]);
+  if (!plain(x, device, 2) || !is_float(x->scalar_type())) Py_RETURN_NONE;
+  const int64_t t = x->size(0), e = x->size(1);
+  if (t > (1 << 21) || e < 1 || e > MBQ_MAX_EXPERTS || top < 1 || top > e || top > MBQ_MAX_EXPERT_TOP) Py_RETURN_NONE;
+  size_t need = 0;
+  if (mbq_expert_route_workspace(int32_t(t), int32_t(e), &need) != MBQ_OK) Py_RETURN_NONE;
+  at::AutoDispatchBelowADInplaceOrView guard;
+  const at::Tensor ids = empty({t, top}, at::kInt, *x), weights = empty({t, top}, at::kFloat, *x),
+                   perm = empty({t * top}, at::kInt, *x), offsets = empty({e + 1}, at::kInt, *x),
+                   place = empty({t, top}, at::kInt, *x);
+  at::Tensor ws;
+  if (need) ws = empty({int64_t(need)}, at::kByte, *x);
+  const auto ints = [](const at::Tensor& v) { return static_cast<int32_t*>(v.data_ptr()); };
+  if (mbq_expert_route(int32_t(t), int32_t(e), x->data_ptr(), code(x->scalar_type()), e, int32_t(top), mbq_score(score), normalize,
+                       weight_scale, ints(ids), static_cast<float*>(weights.data_ptr()), ints(perm), ints(offsets), ints(place),
+                       need ? ws.data_ptr() : nullptr, need, static_cast<hipStream_t>(stream)) != MBQ_OK)
+    Py_RETURN_NONE;
+  return Py_BuildValue("(NNNNN)", THPVariable_Wrap(ids), THPVariable_Wrap(weights), THPVariable_Wrap(perm),
+                       THPVariable_Wrap(offsets), THPVariable_Wrap(place));
+}
+
+// (rows, weights, place, residual, out_dtype, device, stream) -> y
+PyObject* expert_combine(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 7) return PyErr_Format(PyExc_TypeError, "expert_combine takes 7 arguments");
+  const int64_t device = PyLong_AsLongLong(a[5]);
+  void* stream = PyLong_AsVoidPtr(a[6]);
+  if (PyErr_Occurred()) return nullptr;
+  const at::Tensor *rows = tensor(a[0]), *w = tensor(a[1]), *place = tensor(a[2]);
+  if (!plain(rows, device, 2) || !is_float(rows->scalar_type()) || !plain(w, device, 2) || w->scalar_type() != at::kFloat ||
+      !plain(place, device, 2) || place->scalar_type() != at::kInt || place->sizes() != w->sizes())
+    Py_RETURN_NONE;
+  const int64_t p = rows->size(0), width = rows->size(1), t = w->size(0), top = w->size(1);
+  if (p > (1 << 24) || width > (1 << 24) || t > (1 << 21) || top > MBQ_MAX_EXPERT_TOP) Py_RETURN_NONE;
+  at::ScalarType yt = rows->scalar_type();
+  const void* residual = nullptr;
+  if (a[3] != Py_None) {
+    const at::Tensor* r = tensor(a[3]);
+    if (!plain(r, device, 2) || !is_float(r->scalar_type()) || r->size(0) != t || r->size(1) != width || a[4] != Py_None) Py_RETURN_NONE;
+    yt = r->scalar_type();
+    residual = r->data_ptr();
+  } else if (!out_type(a[4], yt, yt)) {
+    Py_RETURN_NONE;
+  }
+  at::AutoDispatchBelowADInplaceOrView guard;
+  const at::Tensor y = empty({t, width}, yt, *rows);
+  if (mbq_expert_combine(int32_t(t), int32_t(width), int32_t(top), int32_t(p), rows->data_ptr(), code(rows->scalar_type()), width,
+                         static_cast<const float*>(w->data_ptr()), static_cast<const int32_t*>(place->data_ptr()), residual, code(yt),
+                         width, y.data_ptr(), width, static_cast<hipStream_t>(stream)) != MBQ_OK)
+    Py_RETURN_NONE;
+  return THPVariable_Wrap(y);
+}
+
 // No C++ exception (an allocation that fails, above all) crosses into the interpreter.
 template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
 PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
@@ -228,7 +346,8 @@ constexpr PyMethodDef method(const char* name) {
 }
 
 PyMethodDef methods[] = {method<fp8>("fp8"), method<fp8_quantize>("fp8_quantize"), method<block_norm>("block_norm"),
-                         method<token_logprobs>("token_logprobs"), {nullptr, nullptr, 0, nullptr}};
+                         method<token_logprobs>("token_logprobs"), method<int8>("int8"),
+                         method<expert_route>("expert_route"), method<expert_combine>("expert_combine"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_bind", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

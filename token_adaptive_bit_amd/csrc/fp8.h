@@ -1,4 +1,4 @@
-// Device helpers of the 8-bit (e4m3) operators.
+// Device helpers of the 8-bit operators (e4m3, and what the integer ones share with them).
 #pragma once
 
 #include "mbq_internal.h"
@@ -261,6 +261,55 @@ __device__ __forceinline__ i32x8_t join(u32x4_t lo, u32x4_t hi) {
     v[4 + i] = int(hi[i]);
   }
   return v;
+}
+
+constexpr int kPlain = -1;  // in place of an mbq_act: no gate
+typedef __attribute__((address_space(4))) float ConstFloat;  // read by scalar loads
+
+template <int ACT>
+__device__ __forceinline__ float gated(float g, float u) {
+  float a = g;
+  if constexpr (ACT == MBQ_ACT_GELU_TANH) a = 1.5957691216057308f * g * fmaf(0.044715f * g, g, 1.f);
+  return g * __builtin_amdgcn_rcpf(1.f + __expf(-a)) * u;
+}
+
+template <bool YBF>
+__device__ __forceinline__ void store4(void* y, int64_t row, int32_t n, int32_t col, const float (&v)[4]) {
+  if constexpr (YBF) {
+    uint16_t* p = reinterpret_cast<uint16_t*>(y) + row * n + col;
+    const u32x2_a2 w = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
+    if (col + 4 <= n) {
+      *reinterpret_cast<u32x2_a2*>(p) = w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (col + e < n) p[e] = uint16_t(w[e / 2] >> (16 * (e & 1)));
+    }
+  } else {
+    float* p = reinterpret_cast<float*>(y) + row * n + col;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (col + e < n) p[e] = v[e];
+  }
+}
+
+// 16 (or 4) bytes a lane from memory to LDS, the lanes side by side at l.  Written in
+// assembly because the compiler waits for every copy in flight before any LDS read that
+// follows one of its own (it cannot tell the buffers apart).  The instruction takes the LDS
+// address from m0, where the compiler puts it (s_nop: one wait state after a write of m0),
+// and has no register outputs; to_lds_wait() before the barrier completes it.
+template <int BYTES>
+__device__ __forceinline__ void to_lds(const void* base, uint32_t offset, const void* l) {  // base, l: the wave's
+  const uint32_t at = uint32_t(uintptr_t((const __attribute__((address_space(3))) void*)l));
+  if constexpr (BYTES == 16)
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(at), "v"(offset), "s"(base) : "memory");
+  else
+    asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, %2" ::"{m0}"(at), "v"(offset), "s"(base) : "memory");
+}
+// Waits until at most N of the wave's copies are on their way (nothing else of it may be).
+template <int N>
+__device__ __forceinline__ void to_lds_wait() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
 }  // namespace mbq

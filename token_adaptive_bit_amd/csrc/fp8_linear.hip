@@ -23,55 +23,6 @@ struct LinArgs {
   int32_t chunks, chunk_kb;  // chunks of the blocks, chunk_kb each (the last one less)
 };
 
-constexpr int kPlain = -1;
-typedef __attribute__((address_space(4))) float ConstFloat;  // read by scalar loads
-
-template <int ACT>
-__device__ __forceinline__ float gated(float g, float u) {
-  float a = g;
-  if constexpr (ACT == MBQ_ACT_GELU_TANH) a = 1.5957691216057308f * g * fmaf(0.044715f * g, g, 1.f);
-  return g * __builtin_amdgcn_rcpf(1.f + __expf(-a)) * u;
-}
-
-template <bool YBF>
-__device__ __forceinline__ void store4(void* y, int64_t row, int32_t n, int32_t col, const float (&v)[4]) {
-  if constexpr (YBF) {
-    uint16_t* p = reinterpret_cast<uint16_t*>(y) + row * n + col;
-    const u32x2_a2 w = {bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
-    if (col + 4 <= n) {
-      *reinterpret_cast<u32x2_a2*>(p) = w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (col + e < n) p[e] = uint16_t(w[e / 2] >> (16 * (e & 1)));
-    }
-  } else {
-    float* p = reinterpret_cast<float*>(y) + row * n + col;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (col + e < n) p[e] = v[e];
-  }
-}
-
-// 16 (or 4) bytes a lane from memory to LDS, the lanes side by side at l.  Written in
-// assembly because the compiler waits for every copy in flight before any LDS read that
-// follows one of its own (it cannot tell the buffers apart).  The instruction takes the LDS
-// address from m0, where the compiler puts it (s_nop: one wait state after a write of m0),
-// and has no register outputs; to_lds_wait() before the barrier completes it.
-template <int BYTES>
-__device__ __forceinline__ void to_lds(const void* base, uint32_t offset, const void* l) {  // base, l: the wave's
-  const uint32_t at = uint32_t(uintptr_t((const __attribute__((address_space(3))) void*)l));
-  if constexpr (BYTES == 16)
-    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"{m0}"(at), "v"(offset), "s"(base) : "memory");
-  else
-    asm volatile("s_nop 0\n\tglobal_load_lds_dword %1, %2" ::"{m0}"(at), "v"(offset), "s"(base) : "memory");
-}
-// Waits until at most N of the wave's copies are on their way (nothing else of it may be).
-template <int N>
-__device__ __forceinline__ void to_lds_wait() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
-}
-
 // Tiles of 32 RN packed rows x 64 RT tokens on 2 x 4 waves (16 RN rows x 16 RT tokens each);
 // both operands and the tokens' scales of a block go through NS LDS buffers, NS - 1 blocks
 // ahead.  With few tiles K is split into chunks, one workgroup each.

@@ -128,4 +128,19 @@ hipError_t launch_token_logprobs(int32_t t, int32_t v, const void* logits, bool 
                                  float* logprob, float* entropy, int32_t* rank, int32_t* top_ids,
                                  float* top_logprobs, void* ws, hipStream_t stream);
 
+// 8-bit integers and experts (int8_quant.hip, int8_linear.hip, experts.hip).
+hipError_t launch_int8_pack(const mbq_int8_desc& d, int32_t part, const void* w, mbq_dtype w_dtype,
+                            const float* w_scale, void* packed, int32_t* dev_status, hipStream_t stream);
+hipError_t launch_int8_quantize(int32_t t, int32_t k, const void* x, bool x_bf16, int64_t ldx, void* q,
+                                int64_t ldq, bool pad, float* scale, hipStream_t stream);
+size_t int8_workspace(const mbq_int8_desc& d, int32_t t, int32_t p, bool grouped, mbq_dtype x_dtype);
+hipError_t launch_int8_linear(const mbq_int8_desc& d, const void* packed, const mbq_int8_args& args, hipStream_t stream);
+size_t expert_route_workspace(int32_t t, int32_t experts);
+hipError_t launch_expert_route(int32_t t, int32_t e, const void* logits, bool bf16, int64_t ld, int32_t top,
+                               bool sigmoid, bool normalize, float scale, int32_t* ids, float* weights, int32_t* perm,
+                               int32_t* offsets, int32_t* place, void* ws, hipStream_t stream);
+hipError_t launch_expert_combine(int32_t t, int32_t n, int32_t top, int32_t p, const void* rows, bool bf16, int64_t ldr,
+                                 const float* weights, const int32_t* place, const void* residual, bool r_bf16,
+                                 int64_t ldres, void* y, int64_t ldy, hipStream_t stream);
+
 }  // namespace mbq
