@@ -30,28 +30,35 @@ struct Tile {
   int expert, first, count;
 };
 
-// The tile-th tile of at most T rows, counted through the experts in their order.  Offsets
-// are data: whatever they hold, the rows found lie in 0 .. p - 1.
+// The expert that the tile-th tile of at most T rows, counted through the experts in their
+// order, belongs to: its rows, and the number of its first tile.  Offsets are data: whatever
+// they hold, the rows found lie in 0 .. p - 1.
+struct Group {
+  int expert, first, count, tile0;
+};
 template <int T>
-__device__ __forceinline__ Tile find_tile(const Args& a, int tile) {
+__device__ __forceinline__ Group find_group(const Args& a, int tile) {
   const int lane = threadIdx.x & 63;
+  int before = 0;
   for (int e0 = 0; e0 < a.experts; e0 += 64) {
     int lo = 0, hi = 0;
     if (e0 + lane < a.experts) {
       lo = min(max(a.offsets[e0 + lane], 0), a.p);
       hi = min(max(a.offsets[e0 + lane + 1], lo), a.p);
     }
-    const int tiles = (hi - lo + T - 1) / T, upto = scan64(tiles);
+    const int tiles = (hi - lo + T - 1) / T, upto = before + scan64(tiles);
     const uint64_t past = __ballot(tile < upto);
     if (past) {
-      const int l = __builtin_ctzll(past);
-      const int first = __builtin_amdgcn_readlane(lo, l) + (tile - __builtin_amdgcn_readlane(upto - tiles, l)) * T;
-      return {e0 + l, first, min(T, __builtin_amdgcn_readlane(hi, l) - first)};
+      const int l = __builtin_ctzll(past), first = __builtin_amdgcn_readlane(lo, l);
+      return {e0 + l, first, __builtin_amdgcn_readlane(hi, l) - first, __builtin_amdgcn_readlane(upto - tiles, l)};
     }
-    tile -= __builtin_amdgcn_readlane(upto, 63);
+    before = __builtin_amdgcn_readlane(upto, 63);
   }
-  return {0, 0, 0};
+  return {0, 0, 0, 0};
 }
+// The part-th tile of a group.
+template <int T>
+__device__ __forceinline__ Tile tile_of(const Group& g, int part) { return {g.expert, g.first + part * T, min(T, g.count - part * T)}; }
 
 // The row of x behind row i of y; there says whether it has one (an index outside x makes a row of zeros).
 __device__ __forceinline__ int source(const Args& a, int i, bool& there) {
@@ -66,41 +73,115 @@ __device__ __forceinline__ void to_lds_from(const uint8_t* p, const void* l) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(at), "v"(p) : "memory");
 }
 
+// Four outputs of a token from their sums (gated: from both products').
 template <int P>
-__device__ __forceinline__ void finish(const Args& a, int64_t row, int rb, int c, const i32x4_t (&sum)[P], float xs, const float* ws) {
-  float v[P][4];
+__device__ __forceinline__ void outputs(const Args& a, const i32x4_t (&sum)[P], float xs, const f32x4_t (&ws)[P], float (&v)[4]) {
+  float u[4];
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const f32x4_t w = *reinterpret_cast<const f32x4_t*>(ws + (rb + i) * kRowBlock + 4 * c);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[i][e] = float(sum[i][e]) * (xs * w[e]);
+  for (int e = 0; e < 4; ++e) {
+    v[e] = float(sum[0][e]) * (xs * ws[0][e]);
+    u[e] = float(sum[P - 1][e]) * (xs * ws[P - 1][e]);
   }
   if constexpr (P == 2) {
     if (a.gelu) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[0][e] = gated<MBQ_ACT_GELU_TANH>(v[0][e], v[1][e]);
+      for (int e = 0; e < 4; ++e) v[e] = gated<MBQ_ACT_GELU_TANH>(v[e], u[e]);
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[0][e] = gated<MBQ_ACT_SILU>(v[0][e], v[1][e]);
+      for (int e = 0; e < 4; ++e) v[e] = gated<MBQ_ACT_SILU>(v[e], u[e]);
     }
   }
-  if (a.y_bf16) store4<true>(a.y, row, a.n, rb / P * kRowBlock + 4 * c, v[0]);
-  else store4<false>(a.y, row, a.n, rb / P * kRowBlock + 4 * c, v[0]);
 }
 
-// Tiles of 16 RN WN packed rows x 16 RT WT tokens on WN x WT waves (16 RN rows x 16 RT tokens
-// each); both operands go through NS LDS buffers of 128 inputs.  A block is two halves of 64
-// inputs.  While a half's products run, the next half's operands are read from LDS; the
-// barrier stands between the halves, where the block's buffer has been read to its end and
-// the next block's copies, a whole block old, are in, and frees the buffer for a new copy.
-template <int WN, int WT, int RN, int RT, int NS, int P, bool GROUPED>
-__global__ __launch_bounds__(64 * WN * WT, 1) void gemm_kernel(Args a) {
+template <int P>
+__device__ __forceinline__ void finish(const Args& a, int64_t row, int rb, int c, const i32x4_t (&sum)[P], float xs,
+                                       const f32x4_t (&ws)[P]) {
+  float v[4];
+  outputs<P>(a, sum, xs, ws, v);
+  if (a.y_bf16) store4<true>(a.y, row, a.n, rb / P * kRowBlock + 4 * c, v);
+  else store4<false>(a.y, row, a.n, rb / P * kRowBlock + 4 * c, v);
+}
+
+// A wave's 16 RN / P outputs of 16 RT tokens to y, 16 tokens at a time: from the instruction's
+// layout, where a lane holds four outputs of one token, through the wave's own LDS to whole
+// rows.  (Stored as they lie, in pieces of 8 bytes, a tile of 256 x 256 took 10 us more.)
+template <int RN, int RT, int P, bool YBF>
+__device__ __forceinline__ void write_rows(const Args& a, const i32x4_t (&acc)[RN][RT], const float (&xs)[RT], const float* ws,
+                                           int rb, int64_t first, int count, uint8_t* lds) {
+  constexpr int kBytes = YBF ? 2 : 4, kRow = RN / P * kRowBlock * kBytes, kPieces = kRow / 16, kStride = kRow + 16;
+  const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
+  f32x4_t w[RN];
+#pragma unroll
+  for (int i = 0; i < RN; ++i) w[i] = *reinterpret_cast<const f32x4_t*>(ws + min(rb + i, a.rbs - 1) * kRowBlock + 4 * c);
+#pragma unroll
+  for (int j = 0; j < RT; ++j) {
+    if (j * 16 >= count) break;
+#pragma unroll
+    for (int i = 0; i < RN; i += P) {
+      i32x4_t sum[P];
+      f32x4_t scale[P];
+#pragma unroll
+      for (int e = 0; e < P; ++e) {
+        sum[e] = acc[i + e][j];
+        scale[e] = w[i + e];
+      }
+      float v[4];
+      outputs<P>(a, sum, xs[j], scale, v);
+      uint8_t* at = lds + r * kStride + (i / P * kRowBlock + 4 * c) * kBytes;
+      if constexpr (YBF) {
+        *reinterpret_cast<uint64_t*>(at) = uint64_t(bf16_pair(v[2], v[3])) << 32 | bf16_pair(v[0], v[1]);
+      } else {
+        *reinterpret_cast<f32x4_t*>(at) = f32x4_t{v[0], v[1], v[2], v[3]};
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+#pragma unroll
+    for (int q = lane; q < 16 * kPieces; q += 64) {
+      const int token = j * 16 + q / kPieces, col = rb / P * kRowBlock + q % kPieces * (16 / kBytes);
+      const u32x4_t piece = *reinterpret_cast<const u32x4_t*>(lds + q / kPieces * kStride + q % kPieces * 16);
+      if (token >= count || col >= a.n) continue;
+      uint8_t* out = static_cast<uint8_t*>(a.y) + ((first + token) * a.n + col) * kBytes;
+      if (col + 16 / kBytes <= a.n) {
+        if constexpr (YBF) *reinterpret_cast<u32x4_a2*>(out) = piece;
+        else *reinterpret_cast<f32x4_a4*>(out) = __builtin_bit_cast(f32x4_t, piece);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16 / kBytes; ++e)
+          if (col + e < a.n) {
+            if constexpr (YBF) reinterpret_cast<uint16_t*>(out)[e] = uint16_t(piece[e / 2] >> (16 * (e & 1)));
+            else reinterpret_cast<uint32_t*>(out)[e] = piece[e];
+          }
+      }
+    }
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+}
+
+// Many tokens: tiles of 16 RN WN packed rows x 16 RT WT tokens on WN x WT waves (16 RN rows x
+// 16 RT tokens each); both operands go through LDS, in NW buffers for the weight and NX for the
+// tokens' codes of 128 inputs each.  A block is two halves of 64 inputs.  While a half's
+// products run, the next half's operands are read from LDS; the barrier stands between the
+// halves, where the block's buffers have been read to their end and the next block's copies
+// are in, and frees the buffers for new ones.  The weight, which comes from farther away, has a
+// buffer more (4096 tokens, 3584 x 18944: 206 us from 213; 8 experts of 4096 x 14336, 16384
+// rows: 912 from 954).  256 x 256 fills LDS to its last byte: its reads and copies
+// take 2048 clocks a block, as many as the products.
+// (Four waves of 128 x 128, which read a third less, have nothing to hide a wait behind: 304 us.)
+template <int WN, int WT, int RN, int RT, int NW, int NX, int P, bool GROUPED>
+__global__ __launch_bounds__(64 * WN * WT, 1) void shared_kernel(Args a) {
   constexpr int kWaves = WN * WT, kRb = WN * RN, kTb = WT * RT, kTok = 16 * kTb;
   constexpr int kCopiesW = 2 * kRb / kWaves, kCopiesX = 2 * kTb / kWaves;  // a wave's 1 KiB copies to LDS a block
   constexpr int kCopies = kCopiesW + kCopiesX;
   static_assert(RN % P == 0, "a gate tile and its up tile in one wave");
   static_assert(2 * kRb % kWaves == 0 && 2 * kTb % kWaves == 0, "every wave makes as many copies as the waits count");
-  __shared__ __align__(1024) uint8_t lds[NS][(kRb + kTb) * kFp8TileBytes];
+  static_assert(NW >= NX && NX >= 2, "the order of the copies");
+  constexpr int kAhead = NW > NX ? kCopiesW : 0;  // copies issued behind the x of one block that belong to later blocks
+  __shared__ __align__(1024) uint8_t lds[(NW * kRb + NX * kTb) * kFp8TileBytes];
+  uint8_t *lw = lds, *lx = lds + NW * kRb * kFp8TileBytes;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, c = lane >> 4;
   const int wn = wave % WN, wt = wave / WN;
@@ -110,19 +191,16 @@ __global__ __launch_bounds__(64 * WN * WT, 1) void gemm_kernel(Args a) {
   const int wg = blockIdx.x / 8 + xcd * per + min(xcd, rest);
   const int chunk = GROUPED ? 0 : wg % a.chunks, id = GROUPED ? wg : wg / a.chunks;
   const int kb0 = chunk * a.chunk_kb, kb1 = min(kb0 + a.chunk_kb, a.kb);
-  Tile tile;
-  int rb0;
+  Group g{0, 0, a.t, 0};
   if constexpr (GROUPED) {
-    rb0 = id % tiles_n * kRb;
-    tile = find_tile<kTok>(a, id / tiles_n);
-    if (tile.count == 0) return;
-  } else {  // four token tiles by as many row tiles as it takes
-    const int tiles_t = (a.t + kTok - 1) / kTok;
-    const int group = id / (4 * tiles_n), gt = min(4, tiles_t - 4 * group), in = id - group * 4 * tiles_n;
-    rb0 = in / gt * kRb;
-    const int first = (4 * group + in % gt) * kTok;
-    tile = {0, first, min(kTok, a.t - first)};
+    g = find_group<kTok>(a, id / tiles_n);
+    if (g.count == 0) return;
   }
+  // four token tiles of an expert by as many row tiles as it takes
+  const int local = id - g.tile0 * tiles_n, four = local / (4 * tiles_n), in = local - four * 4 * tiles_n;
+  const int tiles_t = (g.count + kTok - 1) / kTok, gt = min(4, tiles_t - 4 * four);
+  const int rb0 = in / gt * kRb;
+  const Tile tile = tile_of<kTok>(g, 4 * four + in % gt);
   const uint8_t* codes = a.codes + int64_t(tile.expert) * a.stride;
   const float* ws = a.ws + int64_t(tile.expert) * a.rbs * kRowBlock;
 
@@ -149,12 +227,12 @@ __global__ __launch_bounds__(64 * WN * WT, 1) void gemm_kernel(Args a) {
     const int at = kb * kFp8Block + col;
     const int off = at < a.xlim ? at : 0;
 #pragma unroll
-    for (int i = 0; i < kCopiesX; ++i) to_lds_from(xp[i] + off, &lds[buf][(2 * kRb + i * kWaves + wave) * 1024]);
+    for (int i = 0; i < kCopiesX; ++i) to_lds_from(xp[i] + off, lx + buf * (kTb * kFp8TileBytes) + (i * kWaves + wave) * 1024);
   };
   auto copy_w = [&](int kb, int buf) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < kCopiesW; ++i)
-      to_lds<16>(wp[i] + int64_t(kb) * kFp8TileBytes, uint32_t(lane) * 16, &lds[buf][(i * kWaves + wave) * 1024]);
+      to_lds<16>(wp[i] + int64_t(kb) * kFp8TileBytes, uint32_t(lane) * 16, lw + buf * (kRb * kFp8TileBytes) + (i * kWaves + wave) * 1024);
   };
 
   i32x4_t acc[RN][RT];
@@ -164,10 +242,10 @@ __global__ __launch_bounds__(64 * WN * WT, 1) void gemm_kernel(Args a) {
     for (int j = 0; j < RT; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
   u32x4_t w[2][RN], x[2][RT];
   auto read_w = [&](int buf, int half, int i) __attribute__((always_inline)) {
-    w[half][i] = *(reinterpret_cast<const u32x4_t*>(&lds[buf][(wn * RN + i) * kFp8TileBytes + half * 1024]) + lane);
+    w[half][i] = *(reinterpret_cast<const u32x4_t*>(lw + (buf * kRb + wn * RN + i) * kFp8TileBytes + half * 1024) + lane);
   };
   auto read_x = [&](int buf, int half, int j) __attribute__((always_inline)) {
-    x[half][j] = *reinterpret_cast<const u32x4_t*>(&lds[buf][(kRb + wt * RT + j) * kFp8TileBytes + (xread ^ (64 * half))]);
+    x[half][j] = *reinterpret_cast<const u32x4_t*>(lx + (buf * kTb + wt * RT + j) * kFp8TileBytes + (xread ^ (64 * half)));
   };
   auto products = [&](int half) __attribute__((always_inline)) {
 #pragma unroll
@@ -175,65 +253,208 @@ __global__ __launch_bounds__(64 * WN * WT, 1) void gemm_kernel(Args a) {
 #pragma unroll
       for (int j = 0; j < RT; ++j) acc[i][j] = mfma_i8(w[half][i], x[half][j], acc[i][j]);
   };
-  auto read = [&](int buf, int half) __attribute__((always_inline)) {
+  auto read = [&](int wbuf, int xbuf, int half) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < RT; ++j) read_x(buf, half, j);
+    for (int j = 0; j < RT; ++j) read_x(xbuf, half, j);
 #pragma unroll
-    for (int i = 0; i < RN; ++i) read_w(buf, half, i);
+    for (int i = 0; i < RN; ++i) read_w(wbuf, half, i);
   };
 
   // One path without tests: past the end the last block is copied again, to a buffer that no
   // one reads, so that the copies on their way are always as many as the waits count.
-  auto copy = [&](int kb, int buf) __attribute__((always_inline)) {
-    copy_x(min(kb, kb1 - 1), buf);
-    copy_w(min(kb, kb1 - 1), buf);
-  };
+  auto next_x = [&](int kb, int buf) __attribute__((always_inline)) { copy_x(min(kb, kb1 - 1), buf); };
+  auto next_w = [&](int kb, int buf) __attribute__((always_inline)) { copy_w(min(kb, kb1 - 1), buf); };
 #pragma unroll
-  for (int i = 0; i < NS; ++i) copy(kb0 + i, i);
-  to_lds_wait<(NS - 1) * kCopies>();
-  __syncthreads();
-  read(0, 0);
-  int buf = 0;
-  for (int kb = kb0; kb < kb1 - 1; ++kb) {
-    read(buf, 1);
-    products(0);
-    const int next = buf == NS - 1 ? 0 : buf + 1;
-    to_lds_wait<(NS - 2) * kCopies>();  // block kb + 1 is in
-    __syncthreads();
-    read(next, 0);
-    copy(kb + NS, buf);
-    products(1);
-    buf = next;
+  for (int i = 0; i < NW - NX; ++i) next_w(kb0 + i, i);
+#pragma unroll
+  for (int i = 0; i < NX; ++i) {
+    next_x(kb0 + i, i);
+    next_w(kb0 + i + NW - NX, i + NW - NX);
   }
-  read(buf, 1);
+  to_lds_wait<(NX - 1) * kCopies + kAhead>();
+  __syncthreads();
+  read(0, 0, 0);
+  int wbuf = 0, xbuf = 0;
+  for (int kb = kb0; kb < kb1 - 1; ++kb) {
+    read(wbuf, xbuf, 1);
+    products(0);
+    const int wnext = wbuf == NW - 1 ? 0 : wbuf + 1, xnext = xbuf == NX - 1 ? 0 : xbuf + 1;
+    to_lds_wait<(NX - 2) * kCopies + kAhead>();  // block kb + 1 is in
+    __syncthreads();
+    read(wnext, xnext, 0);
+    next_x(kb + NX, xbuf);
+    next_w(kb + NW, wbuf);
+    products(1);
+    wbuf = wnext;
+    xbuf = xnext;
+  }
+  read(wbuf, xbuf, 1);
   products(0);
   products(1);
   to_lds_wait<0>();  // none of them outlives the workgroup
 
   const int rbw = rb0 + wn * RN;
+  if (!GROUPED && a.chunks > 1) {
 #pragma unroll
-  for (int j = 0; j < RT; ++j) {
-    const int in = (wt * RT + j) * 16 + r;
-    if (in >= tile.count) continue;
-    const int64_t row = tile.first + in;
-    if (!GROUPED && a.chunks > 1) {
-      int32_t* sums = a.part + (int64_t(chunk) * a.p + row) * a.rbs * kRowBlock + 4 * c;
+    for (int j = 0; j < RT; ++j) {
+      const int in = (wt * RT + j) * 16 + r;
+      if (in >= tile.count) continue;
+      int32_t* sums = a.part + (int64_t(chunk) * a.p + tile.first + in) * a.rbs * kRowBlock + 4 * c;
 #pragma unroll
       for (int i = 0; i < RN; ++i)
         if (rbw + i < a.rbs) *reinterpret_cast<i32x4_t*>(sums + (rbw + i) * kRowBlock) = acc[i][j];
-      continue;
     }
+    return;
+  }
+  float xs[RT];
+#pragma unroll
+  for (int j = 0; j < RT; ++j) {
     bool there;
-    const int from = source(a, int(row), there);
-    const float xs = there ? a.xs[from] : 0.f;
+    const int from = source(a, tile.first + min((wt * RT + j) * 16 + r, tile.count - 1), there);
+    xs[j] = there ? a.xs[from] : 0.f;
+  }
+  constexpr int kOutBytes = 16 * (RN / P * kRowBlock * 4 + 16);
+  static_assert(kWaves * kOutBytes <= sizeof(lds), "the waves' outputs go through the operands' buffers");
+  __syncthreads();  // every wave has read its last operands, and no copy is on its way
+  uint8_t* own = lds + wave * kOutBytes;
+  const int64_t first = tile.first + wt * RT * 16;
+  const int count = tile.count - wt * RT * 16;
+  if (a.y_bf16) write_rows<RN, RT, P, true>(a, acc, xs, ws, rbw, first, count, own);
+  else write_rows<RN, RT, P, false>(a, acc, xs, ws, rbw, first, count, own);
+}
+
+// Fewer tokens, and ragged groups: tiles of 16 RN WN packed rows x 16 RT tokens on WN waves, which
+// share the tokens and have 16 RN rows each: the weight goes from memory to the registers of
+// the wave that owns its rows, D blocks ahead, and only the tokens' codes go through LDS (NX
+// buffers).  LDS is read for the tokens alone, and two and more workgroups fit a unit, whose
+// waits, starts and ends hide one another's.  (256 x 128 against the same tile with both
+// operands in LDS: 128 gated experts of 1536 x 4096, 32768 rows 546 us from 601; 11008 x 4096,
+// 2048 tokens 84 from 90.  Of the 546, the copies and loads alone take 494.)
+template <int WN, int RN, int RT, int D, int NX, int P, bool GROUPED>
+__global__ __launch_bounds__(64 * WN, 2) void direct_kernel(Args a) {
+  constexpr int kRb = WN * RN, kTok = 16 * RT;
+  constexpr int kCopiesX = (2 * RT + WN - 1) / WN;  // of a wave, or of the first 2 RT waves
+  static_assert(RN % P == 0 && (2 * RT % WN == 0 || 2 * RT < WN) && NX >= 2, "");
+  constexpr int kOutBytes = 16 * (RN / P * kRowBlock * 4 + 16);
+  constexpr int kLds = NX * RT * kFp8TileBytes > WN * kOutBytes ? NX * RT * kFp8TileBytes : WN * kOutBytes;
+  __shared__ __align__(1024) uint8_t lds[kLds];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, c = lane >> 4;
+  // neighbouring tiles on one XCD
+  const int tiles_n = (a.rbs + kRb - 1) / kRb;
+  const int per = gridDim.x / 8, rest = gridDim.x % 8, xcd = blockIdx.x % 8;
+  const int wg = blockIdx.x / 8 + xcd * per + min(xcd, rest);
+  const int chunk = GROUPED ? 0 : wg % a.chunks, id = GROUPED ? wg : wg / a.chunks;
+  const int kb0 = chunk * a.chunk_kb, kb1 = min(kb0 + a.chunk_kb, a.kb);
+  Group g{0, 0, a.t, 0};
+  if constexpr (GROUPED) {
+    g = find_group<kTok>(a, id / tiles_n);
+    if (g.count == 0) return;
+  }
+  // as many token tiles of an expert as make it square, by as many row tiles as it takes
+  constexpr int kSide = 8;
+  const int local = id - g.tile0 * tiles_n, side = local / (kSide * tiles_n), in = local - side * kSide * tiles_n;
+  const int tiles_t = (g.count + kTok - 1) / kTok, gt = min(kSide, tiles_t - kSide * side);
+  const int rbw = in / gt * kRb + wave * RN;
+  const Tile tile = tile_of<kTok>(g, kSide * side + in % gt);
+  const uint8_t* codes = a.codes + int64_t(tile.expert) * a.stride;
+  const float* ws = a.ws + int64_t(tile.expert) * a.rbs * kRowBlock;
+  const uint8_t* wp[RN];
 #pragma unroll
-    for (int i = 0; i < RN; i += P) {
-      i32x4_t sum[P];
+  for (int i = 0; i < RN; ++i) wp[i] = codes + int64_t(min(rbw + i, a.rbs - 1)) * a.kb * kFp8TileBytes;
+  const int col = 16 * ((lane & 7) ^ (lane >> 3));
+  const uint8_t* xp[kCopiesX];
 #pragma unroll
-      for (int e = 0; e < P; ++e) sum[e] = acc[i + e][j];
-      if (rbw + i < a.rbs) finish<P>(a, row, rbw + i, c, sum, xs, ws);
+  for (int i = 0; i < kCopiesX; ++i) {
+    bool there;
+    xp[i] = a.xq + source(a, tile.first + min((i * WN + wave) * 8 + (lane >> 3), tile.count - 1), there) * a.ldq;
+  }
+  const int xread = r * 128 + 16 * (c ^ (r & 7));
+  auto copy_x = [&](int kb, int buf) __attribute__((always_inline)) {
+    const int at = min(kb, kb1 - 1) * kFp8Block + col;
+    const int off = at < a.xlim ? at : 0;
+    if (2 * RT < WN && wave >= 2 * RT) return;
+#pragma unroll
+    for (int i = 0; i < kCopiesX; ++i) to_lds_from(xp[i] + off, lds + buf * (RT * kFp8TileBytes) + (i * WN + wave) * 1024);
+  };
+  u32x4_t w[D][2][RN], x[RT];
+  auto load_w = [&](int kb, int s, int half) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < RN; ++i)
+      w[s][half][i] = *reinterpret_cast<const u32x4_t*>(wp[i] + int64_t(min(kb, kb1 - 1)) * kFp8TileBytes + half * 1024 + lane * 16);
+  };
+  auto read_x = [&](int buf, int half, int j) __attribute__((always_inline)) {
+    x[j] = *reinterpret_cast<const u32x4_t*>(lds + (buf * RT + j) * kFp8TileBytes + (xread ^ (64 * half)));
+  };
+  i32x4_t acc[RN][RT];
+#pragma unroll
+  for (int i = 0; i < RN; ++i)
+#pragma unroll
+    for (int j = 0; j < RT; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+
+#pragma unroll
+  for (int i = 0; i < NX; ++i) copy_x(kb0 + i, i);
+#pragma unroll
+  for (int i = 0; i < D; ++i) {
+    load_w(kb0 + i, i, 0);
+    load_w(kb0 + i, i, 1);
+  }
+  to_lds_wait<(NX - 1) * kCopiesX + D * 2 * RN>();
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < RT; ++j) read_x(0, 0, j);
+  int buf = 0;
+  for (int kb = kb0; kb < kb1; kb += D) {
+#pragma unroll
+    for (int s = 0; s < D; ++s) {
+      if (kb + s < kb1) {
+        const int next = buf == NX - 1 ? 0 : buf + 1;
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+#pragma unroll
+          for (int i = 0; i < RN; ++i) acc[i][j] = mfma_i8(w[s][0][i], x[j], acc[i][j]);
+          read_x(buf, 1, j);
+        }
+        load_w(kb + s + D, s, 0);
+        // the next block's codes are in: at most the copies and loads issued after them are on their way
+        to_lds_wait<(NX - 2) * kCopiesX + ((NX - 2) * 2 + 2) * RN>();
+        __syncthreads();
+        copy_x(kb + s + NX, buf);
+#pragma unroll
+        for (int j = 0; j < RT; ++j) {
+#pragma unroll
+          for (int i = 0; i < RN; ++i) acc[i][j] = mfma_i8(w[s][1][i], x[j], acc[i][j]);
+          read_x(next, 0, j);
+        }
+        load_w(kb + s + D, s, 1);
+        buf = next;
+      }
     }
   }
+  to_lds_wait<0>();  // none of them outlives the workgroup
+  if (!GROUPED && a.chunks > 1) {
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {
+      const int at = j * 16 + r;
+      if (at >= tile.count) continue;
+      int32_t* sums = a.part + (int64_t(chunk) * a.p + tile.first + at) * a.rbs * kRowBlock + 4 * c;
+#pragma unroll
+      for (int i = 0; i < RN; ++i)
+        if (rbw + i < a.rbs) *reinterpret_cast<i32x4_t*>(sums + (rbw + i) * kRowBlock) = acc[i][j];
+    }
+    return;
+  }
+  float xs[RT];
+#pragma unroll
+  for (int j = 0; j < RT; ++j) {
+    bool there;
+    const int from = source(a, tile.first + min(j * 16 + r, tile.count - 1), there);
+    xs[j] = there ? a.xs[from] : 0.f;
+  }
+  __syncthreads();  // every wave has read its last operands, and no copy is on its way
+  uint8_t* own = lds + wave * kOutBytes;
+  if (a.y_bf16) write_rows<RN, RT, P, true>(a, acc, xs, ws, rbw, tile.first, tile.count, own);
+  else write_rows<RN, RT, P, false>(a, acc, xs, ws, rbw, tile.first, tile.count, own);
 }
 
 // Joins the chunks of a split K: four outputs of one token a thread.
@@ -251,34 +472,48 @@ __global__ __launch_bounds__(256) void join_kernel(Args a) {
     for (int s = 1; s < a.chunks; ++s)
 #pragma unroll
       for (int e = 0; e < P; ++e) sum[e] += *reinterpret_cast<const i32x4_t*>(from + s * stride + kRowBlock * e);
-    finish<P>(a, token, rb, c, sum, a.xs[token], a.ws);
+    f32x4_t w[P];
+#pragma unroll
+    for (int e = 0; e < P; ++e) w[e] = *reinterpret_cast<const f32x4_t*>(a.ws + (rb + e) * kRowBlock + 4 * c);
+    finish<P>(a, token, rb, c, sum, a.xs[token], w);
   }
 }
 
 // Few tokens: a workgroup streams one row block (gated: the pair) for a tile of at most 16 TT
 // tokens; its W waves take every W-th 128-input block, and their sums meet in LDS.  A wave has
-// U blocks in its registers and the next U on their way; a block past the end is the last one
-// again, met by activations of 0, so that no load stands behind a test.
+// U blocks in its registers and the next U on their way; blocks past the end are loads out of
+// the buffer's range, so that no load of a step stands behind a test.
 // XT: the type of x.  Codes (MBQ_INT8) are read from memory; a few float tokens are quantized
 // here, once a workgroup into LDS, which saves the quantizing launch.
 template <int W, int TT, int XT, int P, bool GROUPED>
 __global__ __launch_bounds__(64 * W) void stream_kernel(Args a) {
   constexpr int U = (TT * P >= 4 ? 1 : TT * P == 2 ? 2 : 4) * 8 / W > 0 ? (TT * P >= 4 ? 1 : TT * P == 2 ? 2 : 4) * 8 / W : 1;
   constexpr bool kInline = XT != MBQ_INT8;
+  constexpr int kNt = 2;  // the weight is read once: it need not stay in the caches
   static_assert(!kInline || TT == 1, "a few tokens");
   extern __shared__ __align__(16) uint8_t lx[];  // inline: codes, rows 16 bytes apart in banks
   __shared__ i32x4_t red[W][P * TT][64];
-  __shared__ uint32_t amax[kInline ? 16 : 1][W];
+  __shared__ uint32_t amax[W];
+  __shared__ float ls[16];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, c = lane >> 4;
   const int rb0 = blockIdx.x * P;
   Tile tile{0, 0, a.t};
   if constexpr (GROUPED) {
-    tile = find_tile<16 * TT>(a, blockIdx.y);
-    if (tile.count == 0) return;
+    const Group g = find_group<16 * TT>(a, blockIdx.y);
+    if (g.count == 0) return;
+    tile = tile_of<16 * TT>(g, int(blockIdx.y) - g.tile0);
   }
-  const uint8_t* wp = a.codes + int64_t(tile.expert) * a.stride + int64_t(rb0) * a.kb * kFp8TileBytes + lane * 16;
-  const float* ws = a.ws + int64_t(tile.expert) * a.rbs * kRowBlock;
+  __amdgpu_buffer_rsrc_t rows[P];  // a row block each: loads past its end return 0 and touch no memory
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    rows[i] = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<uint8_t*>(a.codes + int64_t(tile.expert) * a.stride + int64_t(rb0 + i) * a.kb * kFp8TileBytes), 0,
+        a.kb * kFp8TileBytes, 0x00020000);
+  f32x4_t wscale[P];  // asked for now: after the sums their way would be waited for
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    wscale[i] = *reinterpret_cast<const f32x4_t*>(a.ws + (int64_t(tile.expert) * a.rbs + rb0 + i) * kRowBlock + 4 * c);
   const int ldl = a.kb * kFp8Block + 16;
   const uint8_t* xp[TT];
   float xs[TT];
@@ -298,19 +533,19 @@ __global__ __launch_bounds__(64 * W) void stream_kernel(Args a) {
   auto load = [&](int s, int k0) __attribute__((always_inline)) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int kb = min(k0 + u * W, a.kb - 1);
+      const int kb = k0 + u * W;
 #pragma unroll
       for (int i = 0; i < P; ++i)
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-          wf[s][u][i][h] = __builtin_nontemporal_load(
-              reinterpret_cast<const u32x4_t*>(wp + (int64_t(i) * a.kb + kb) * kFp8TileBytes + 1024 * h));
+          wf[s][u][i][h] = __builtin_bit_cast(
+              u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rows[i], kb * kFp8TileBytes + 1024 * h + lane * 16, 0, kNt));
       if constexpr (!kInline)
 #pragma unroll
         for (int j = 0; j < TT; ++j)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int col = kb * kFp8Block + 64 * h + 16 * c;  // past the end of a row: see gemm_kernel
+            const int col = kb * kFp8Block + 64 * h + 16 * c;  // past the end of a row: see shared_kernel
             xf[s][u][j][h] = *reinterpret_cast<const u32x4_t*>(xp[j] + (col < a.xlim ? col : 0));
           }
     }
@@ -324,7 +559,6 @@ __global__ __launch_bounds__(64 * W) void stream_kernel(Args a) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int kb = k0 + u * W;
-      const uint32_t keep = kb < a.kb ? ~0u : 0u;
 #pragma unroll
       for (int j = 0; j < TT; ++j)
 #pragma unroll
@@ -332,7 +566,6 @@ __global__ __launch_bounds__(64 * W) void stream_kernel(Args a) {
           u32x4_t v;
           if constexpr (kInline) v = *reinterpret_cast<const u32x4_t*>(xp[j] + min(kb, a.kb - 1) * kFp8Block + 64 * h);
           else v = xf[s][u][j][h];
-          v &= keep;
 #pragma unroll
           for (int i = 0; i < P; ++i) acc[i][j] = mfma_i8(wf[s][u][i][h], v, acc[i][j]);
         }
@@ -341,43 +574,61 @@ __global__ __launch_bounds__(64 * W) void stream_kernel(Args a) {
 
   if constexpr (kInline) {
     constexpr bool kBf = XT == MBQ_BF16;
-    const int tid = threadIdx.x;
-    Raw8<kBf> ahead;  // the first row's, asked for before the weight
-    auto row_of = [&](int i, bool& there) __attribute__((always_inline)) {
+    const int tid = threadIdx.x, end = a.kb * kFp8Block;
+    bool there;
+    auto row_of = [&](int i) __attribute__((always_inline)) {
       return static_cast<const uint8_t*>(a.x) + source(a, tile.first + i, there) * a.ldx * (kBf ? 2 : 4);
     };
-    bool there;
-    ahead.load(row_of(0, there), tid * 8, a.k);
-    load(0, wave);
-    for (int i = 0; i < tile.count; ++i) {
-      const uint8_t* row = row_of(i, there);
-      uint32_t m = 0;
+    if (tile.count == 1) {  // one row by all waves; its first elements are asked for before the weight
+      const uint8_t* row = row_of(0);
+      Raw8<kBf> ahead;
+      ahead.load(row, tid * 8, a.k);
+      load(0, wave);
       float v[8];
-      if (i == 0) ahead.get(v);
-      else load8<kBf>(row, tid * 8, a.k, v);
-      m = amax8(v);
+      ahead.get(v);
+      uint32_t m = amax8(v);
       for (int at = (tid + 64 * W) * 8; at < a.k; at += 64 * W * 8) {
         load8<kBf>(row, at, a.k, v);
         m = max(m, amax8(v));
       }
       m = max64(m);
-      if (lane == 0) amax[i][wave] = m;
-    }
-    __syncthreads();
-    for (int i = 0; i < tile.count; ++i) {
-      const uint8_t* row = row_of(i, there);
-      uint32_t m = 0;
+      if (lane == 0) amax[wave] = m;
+      __syncthreads();
 #pragma unroll
-      for (int w = 0; w < W; ++w) m = max(m, amax[i][w]);
+      for (int w = 0; w < W; ++w) m = max(m, amax[w]);
       const float f = int8_factor(m);
-      for (int at = tid * 8; at < a.kb * kFp8Block; at += 64 * W * 8) {
-        float v[8];
-        load8<kBf>(row, at, a.k, v);
-        store_int8x8(lx + i * ldl, at, ldl, v, f);
+      if (tid * 8 < end) {
+        ahead.get(v);
+        store_int8x8(lx, tid * 8, ldl, v, f);
       }
-      if (i == min(r, tile.count - 1)) xs[0] = there ? int8_scale(m) : 0.f;
+      for (int at = (tid + 64 * W) * 8; at < end; at += 64 * W * 8) {
+        load8<kBf>(row, at, a.k, v);
+        store_int8x8(lx, at, ldl, v, f);
+      }
+      if (tid == 0) ls[0] = there ? int8_scale(m) : 0.f;
+    } else {  // a wave a row
+      load(0, wave);
+      for (int i = wave; i < tile.count; i += W) {
+        const uint8_t* row = row_of(i);
+        uint32_t m = 0;
+        float v[8];
+#pragma unroll 4
+        for (int at = lane * 8; at < a.k; at += 512) {
+          load8<kBf>(row, at, a.k, v);
+          m = max(m, amax8(v));
+        }
+        m = max64(m);
+        const float f = int8_factor(m);
+#pragma unroll 4
+        for (int at = lane * 8; at < end; at += 512) {
+          load8<kBf>(row, at, a.k, v);
+          store_int8x8(lx + i * ldl, at, ldl, v, f);
+        }
+        if (lane == 0) ls[i] = there ? int8_scale(m) : 0.f;
+      }
     }
     __syncthreads();
+    xs[0] = ls[min(r, tile.count - 1)];
   } else {
     load(0, wave);
   }
@@ -406,14 +657,21 @@ __global__ __launch_bounds__(64 * W) void stream_kernel(Args a) {
 #pragma unroll
     for (int w = 1; w < W; ++w) sum[i] += red[w][i * TT + wave][lane];
   }
-  if (in < tile.count) finish<P>(a, tile.first + in, rb0, c, sum, scale, ws);
+  if (in < tile.count) finish<P>(a, tile.first + in, rb0, c, sum, scale, wscale);
 }
 
-template <int WN, int WT, int RN, int RT, int NS, int P, bool GROUPED>
-void launch_tiles(const Args& a, hipStream_t stream) {
+template <int WN, int WT, int RN, int RT, int NW, int NX, int P, bool GROUPED>
+void launch_shared(const Args& a, hipStream_t stream) {
   const int64_t tiles_n = (a.rbs + WN * RN - 1) / (WN * RN), tok = 16 * WT * RT;
   const int64_t tiles_t = GROUPED ? a.p / tok + std::min(a.experts, a.p) : (a.p + tok - 1) / tok;
-  gemm_kernel<WN, WT, RN, RT, NS, P, GROUPED><<<uint32_t(tiles_n * tiles_t * a.chunks), 64 * WN * WT, 0, stream>>>(a);
+  shared_kernel<WN, WT, RN, RT, NW, NX, P, GROUPED><<<uint32_t(tiles_n * tiles_t * a.chunks), 64 * WN * WT, 0, stream>>>(a);
+}
+
+template <int WN, int RN, int RT, int D, int NX, int P, bool GROUPED>
+void launch_direct(const Args& a, hipStream_t stream) {
+  const int64_t tiles_n = (a.rbs + WN * RN - 1) / (WN * RN), tok = 16 * RT;
+  const int64_t tiles_t = GROUPED ? a.p / tok + std::min(a.experts, a.p) : (a.p + tok - 1) / tok;
+  direct_kernel<WN, RN, RT, D, NX, P, GROUPED><<<uint32_t(tiles_n * tiles_t * a.chunks), 64 * WN, 0, stream>>>(a);
 }
 
 template <int W, int TT, int P, bool GROUPED>
@@ -439,13 +697,14 @@ hipError_t launch(Args& a, const Int8Plan& p, mbq_dtype x_dtype, hipStream_t str
     case Int8Form::kStream8x1: launch_stream<8, 1, P, GROUPED>(a, x_dtype, stream); break;
     case Int8Form::kStream16x1: launch_stream<16, 1, P, GROUPED>(a, x_dtype, stream); break;
     case Int8Form::kStream8x2: launch_stream<8, 2, P, GROUPED>(a, x_dtype, stream); break;
-    case Int8Form::kStream8x4: launch_stream<8, 4, P, GROUPED>(a, x_dtype, stream); break;
-    case Int8Form::k256x256: launch_tiles<2, 4, 8, 4, 2, P, GROUPED>(a, stream); break;
-    case Int8Form::k256x128: launch_tiles<2, 2, 8, 4, 3, P, GROUPED>(a, stream); break;
-    case Int8Form::k128x128: launch_tiles<2, 2, 4, 4, 3, P, GROUPED>(a, stream); break;
-    case Int8Form::k128x64: launch_tiles<2, 2, 4, 2, 3, P, GROUPED>(a, stream); break;
-    case Int8Form::k64x64: launch_tiles<2, 2, 2, 2, 3, P, GROUPED>(a, stream); break;
-    case Int8Form::k64x32: launch_tiles<2, 2, 2, 1, 3, P, GROUPED>(a, stream); break;
+    case Int8Form::kDirect64x16: launch_direct<2, 2, 1, 6, 4, P, GROUPED>(a, stream); break;
+    case Int8Form::kDirect128x16: launch_direct<4, 2, 1, 4, 4, P, GROUPED>(a, stream); break;
+    case Int8Form::kDirect128x32: launch_direct<4, 2, 2, 4, 4, P, GROUPED>(a, stream); break;
+    case Int8Form::kDirect128x64: launch_direct<4, 2, 4, 3, 3, P, GROUPED>(a, stream); break;
+    case Int8Form::kDirect256x64: launch_direct<4, 4, 4, 2, 3, P, GROUPED>(a, stream); break;
+    case Int8Form::kDirect256x128: launch_direct<4, 4, 8, 2, 2, P, GROUPED>(a, stream); break;
+    case Int8Form::kShared256x192: launch_shared<2, 4, 8, 3, 3, 2, P, GROUPED>(a, stream); break;
+    case Int8Form::kShared256x256: launch_shared<2, 4, 8, 4, 3, 2, P, GROUPED>(a, stream); break;
   }
   if (a.chunks > 1)
     join_kernel<P><<<uint32_t(std::min<int64_t>((int64_t(a.p) * (a.rbs / P) * 4 + 255) / 256, 4096)), 256, 0, stream>>>(a);

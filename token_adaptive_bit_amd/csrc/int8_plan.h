@@ -2,36 +2,107 @@
 #pragma once
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 
 namespace mbq {
 
-enum class Int8Form { kStream8x1, kStream16x1, kStream8x2, kStream8x4, k256x256, k256x128, k128x128, k128x64, k64x64, k64x32 };
+// Streaming (waves x token tiles of 16), direct and shared tiles (rows x tokens).
+enum class Int8Form {
+  kStream8x1, kStream16x1, kStream8x2,
+  kDirect64x16, kDirect128x16, kDirect128x32, kDirect128x64, kDirect256x64, kDirect256x128,
+  kShared256x192, kShared256x256
+};
+constexpr int kInt8Forms = 11;
+
+// The time of a form: workgroups take rounds of one on each of the 256 compute units.  A
+// workgroup's blocks of K take wait_us each from one to the next (latency, hidden from one
+// workgroup to another), block_us each of the unit (throughput, added up over its
+// workgroups), and the weight's bytes their time at `tbs` (`cold_tbs` where they are more than
+// the last-level cache keeps), a part `again` of them for every further tile of tokens; the three overlap.  tile_us starts and ends a workgroup, launch_us is
+// paid once, and split K (join_us) pays a second launch and the partial sums' traffic (join_tbs).
+// The times are a fit to 9364 timings of every form on 13 weights, plain and gated, 1 to 4096
+// tokens (the best split of each in profiles/int8_plan_timings.csv): the choice is 1.6% above the best on the mean, 6% at
+// the ninth tenth.  For instance, us of 64 x 16 / 128 x 64 / 256 x 128 / 256 x 256: 5120 x 5120 with 64
+// tokens 21.0 / 21.9 / 39.3 / 62.4, with 2048 181 / 74.5 / 63.0 / 65.0.
+struct Int8Cost {
+  int rows, tokens;
+  float wait_us, block_us, tile_us, launch_us, tbs, cold_tbs, again, join_us, join_tbs;
+};
+constexpr Int8Cost kInt8Costs[kInt8Forms] = {
+    {16, 16, 0.010f, 0.041f, 0.60f, 5.3f, 7.4f, 5.0f, 0.00f, 0.f, 1.f},
+    {16, 16, 0.023f, 0.034f, 0.45f, 5.7f, 7.7f, 5.0f, 0.00f, 0.f, 1.f},
+    {16, 32, 0.010f, 0.094f, 0.31f, 5.9f, 6.5f, 5.6f, 0.00f, 0.f, 1.f},
+    {64, 16, 0.146f, 0.102f, 0.14f, 5.7f, 6.6f, 4.8f, 0.05f, 1.9f, 1.6f},
+    {128, 16, 0.223f, 0.176f, 0.38f, 4.9f, 6.5f, 4.9f, 0.09f, 2.2f, 2.3f},
+    {128, 32, 0.250f, 0.191f, 0.60f, 4.9f, 6.5f, 5.3f, 0.16f, 2.5f, 3.2f},
+    {128, 64, 0.341f, 0.232f, 0.78f, 5.3f, 6.4f, 5.4f, 0.28f, 2.2f, 3.2f},
+    {256, 64, 0.504f, 0.403f, 1.18f, 5.6f, 6.2f, 5.7f, 0.27f, 2.1f, 3.5f},
+    {256, 128, 0.707f, 0.661f, 2.16f, 7.0f, 5.9f, 5.6f, 0.44f, 1.3f, 3.6f},
+    {256, 192, 0.010f, 0.937f, 5.10f, 4.5f, 6.5f, 5.3f, 0.76f, 2.9f, 3.9f},
+    {256, 256, 0.010f, 1.183f, 6.24f, 5.1f, 6.1f, 5.3f, 0.91f, 2.4f, 3.8f}};
+constexpr int kInt8Splits[] = {1, 2, 3, 4, 6, 8, 12};
+constexpr int kInt8Inline = 384;  // most blocks that are quantized in the kernel (48 KiB of LDS)
 
 struct Int8Plan {
   Int8Form form;
-  int chunks;      // of K (tiles of one weight only)
-  bool inline_x;   // float activations are quantized in the streaming kernel
+  int chunks;     // of K (tiles of one weight only)
+  bool inline_x;  // float activations are quantized in the streaming kernel
 };
 
 // t rows of x, p rows of y, experts (0: one weight, no groups), row groups of 16 outputs,
 // parts of a row group (2 gated), 128-input blocks.
 inline Int8Plan plan_int8(int32_t t, int32_t p, int32_t experts, int32_t groups, int32_t parts, int32_t kb, bool codes) {
-  Int8Plan plan{Int8Form::kStream8x1, 1, false};
-  const double rows = experts ? double(p) / std::min(experts, p) : t;  // of a weight that has some
-  if (experts ? rows <= 16 : t <= 16) {
-    plan.form = groups <= 256 && kb >= 64 ? Int8Form::kStream16x1 : Int8Form::kStream8x1;
-    plan.inline_x = !codes && int64_t(std::min(p, 16)) * kb <= 384;
-  } else if (rows <= 64) {
-    plan.form = Int8Form::k64x64;
-  } else if (rows <= 192) {
-    plan.form = Int8Form::k128x128;
-  } else if (rows <= 1024) {
-    plan.form = Int8Form::k256x128;
-  } else {
-    plan.form = Int8Form::k256x256;
+  // of the experts, were they equally popular, those that have a row, and their rows
+  const float used = experts ? experts * (1.f - std::exp(-float(p) / experts)) : 1.f, rows = p / used;
+  const float weight = used * groups * parts * kb * 2048.f;
+  const float quantize = codes ? 0.f : 2.5f + float(t) * kb * 128.f * 4e-6f / 5.f;  // a launch of its own
+  // The streaming kernel can quantize float activations itself, every workgroup all of its
+  // tile's rows: one row by all its waves at once, more a wave each (us within / before: 5120 x
+  // 5120 with 1 / 2 / 8 tokens 9.1 / 12.4, 12.3 / 12.5, 14.4 / 14.0; 18944 x 3584 13.8 / 19.0, 23.0 / 19.2,
+  // 24.6 / 20.1).
+  const bool inline_x = !codes && int64_t(std::min(p, 16)) * kb <= kInt8Inline;
+  Int8Plan best{Int8Form::kDirect128x64, 1, false};
+  float best_us = 1e30f;
+  for (int f = 0; f < kInt8Forms; ++f) {
+    const Int8Cost& c = kInt8Costs[f];
+    const bool stream = f < 3;
+    if (stream && (experts ? p > 16 * experts : t > c.tokens)) continue;  // grids of few tokens
+    const float tiles_n = stream ? groups : float((groups * parts * 16 + c.rows - 1) / c.rows);
+    // tiles of an expert: half of one more for its odd rows, one at least, more than that where some have few rows and some many
+    const float full = rows / c.tokens;
+    const float tiles_t = experts ? full + 0.5f + 0.5f * std::exp(-2.f * full) : float((t + c.tokens - 1) / c.tokens);
+    float before = quantize;
+    bool within = false;
+    if (inline_x && f < 2) {
+      const float sets = rows <= 1.1f ? 0.f : std::ceil(std::min(rows, 16.f) / (f == 0 ? 8.f : 16.f));
+      const float us = std::ceil(used * tiles_n * tiles_t / (f == 0 ? 512.f : 256.f)) * sets * (0.6f + 0.05f * kb);
+      within = us < quantize;
+      before = std::min(us, quantize);
+    }
+    float last = 1e30f;
+    for (int s : kInt8Splits) {
+      if (s > 1 && (experts || stream || kb / s < 3 || tiles_n * tiles_t * s > 1100.f)) break;
+      const int per = (kb + s - 1) / s, chunks = (kb + per - 1) / per;
+      if (chunks != s) continue;
+      const float all = used * tiles_n * tiles_t * s / 256.f;
+      const float rounds = std::max(1.f, experts ? all + 0.5f : std::ceil(all - 1e-3f));  // of experts only an estimate
+      const float wait = per * c.wait_us, work = rounds * per * c.block_us;
+      const float bytes = weight * (1.f + c.again * (tiles_t - 1.f)) / ((weight > 2e8f ? c.cold_tbs : c.tbs) * 1e6f);
+      const float w2 = wait * wait, k2 = work * work, b2 = bytes * bytes;
+      // starting and ending the workgroups; streaming ones of experts, which look for theirs first, run two at once
+      const float starts = experts && stream ? std::max(0.f, all - (f == 1 ? 1.f : 2.f)) * (c.tile_us + 1.6f) : rounds * (c.tile_us + (experts ? 0.3f : 0.f));
+      const float join = s == 1 ? 0.f : c.join_us + float(t) * groups * parts * 64.f * s / (c.join_tbs * 1e6f);
+      const float us = before + c.launch_us + std::sqrt(std::sqrt(w2 * w2 + k2 * k2 + b2 * b2)) + starts + join;
+      if (us < best_us) {
+        best_us = us;
+        best = {Int8Form(f), s, within};
+      }
+      if (us > 1.2f * last) break;  // more chunks only cost more
+      last = us;
+    }
   }
-  return plan;
+  return best;
 }
 
 }  // namespace mbq
