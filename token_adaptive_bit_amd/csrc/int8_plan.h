@@ -19,12 +19,15 @@ constexpr int kInt8Forms = 11;
 // workgroup's blocks of K take wait_us each from one to the next (latency, hidden from one
 // workgroup to another), block_us each of the unit (throughput, added up over its
 // workgroups), and the weight's bytes their time at `tbs` (`cold_tbs` where they are more than
-// the last-level cache keeps), a part `again` of them for every further tile of tokens; the three overlap.  tile_us starts and ends a workgroup, launch_us is
-// paid once, and split K (join_us) pays a second launch and the partial sums' traffic (join_tbs).
-// The times are a fit to 9364 timings of every form on 13 weights, plain and gated, 1 to 4096
-// tokens (the best split of each in profiles/int8_plan_timings.csv): the choice is 1.6% above the best on the mean, 6% at
-// the ninth tenth.  For instance, us of 64 x 16 / 128 x 64 / 256 x 128 / 256 x 256: 5120 x 5120 with 64
-// tokens 21.0 / 21.9 / 39.3 / 62.4, with 2048 181 / 74.5 / 63.0 / 65.0.
+// the last-level cache keeps), a part `again` of them for every further tile of tokens; the
+// three overlap.  tile_us starts and ends a workgroup, launch_us is paid once, and split K
+// (join_us) pays a second launch and the partial sums' traffic (join_tbs).  The times are a fit
+// to 9364 timings of every form on 13 weights, plain and gated, 1 to 4096 tokens (the best
+// split of each in profiles/int8_plan_timings.csv): the choice is 1.6% above the best on the
+// mean, 6% at the ninth tenth; for experts (70 drawn shapes, cold_tbs and the added terms are
+// theirs) 2.8% on the mean.  For instance, 5120 x 5120, us: 64 tokens 64 x 16 14.4, 128 x 64 14.9,
+// 256 x 128 18.4; 333 tokens 128 x 64 21.7, 256 x 128 27.2, 256 x 256 34.7; 2048 tokens 256 x 128
+// 63.7, 256 x 192 52.1, 256 x 256 56.3.
 struct Int8Cost {
   int rows, tokens;
   float wait_us, block_us, tile_us, launch_us, tbs, cold_tbs, again, join_us, join_tbs;
