@@ -30,6 +30,14 @@ at::Tensor empty(at::IntArrayRef sizes, at::ScalarType type, const at::Tensor& l
   return at::empty(sizes, like.options().dtype(type));
 }
 
+// A contiguous piece of a tensor's storage as a tensor of its own.
+at::Tensor part(const at::Tensor& whole, int64_t offset, at::IntArrayRef sizes) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::TensorImpl::VIEW, c10::Storage(whole.storage()), whole.key_set(), whole.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(offset);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(sizes);
+  return t;
+}
+
 // An optional float32 [k] vector: its address, or nullptr for None; ok says whether it is one of the two.
 const float* vector(PyObject* o, int64_t k, int64_t device, bool& ok) {
   if (o == Py_None) return nullptr;
@@ -284,9 +292,10 @@ PyObject* expert_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
   size_t need = 0;
   if (mbq_expert_route_workspace(int32_t(t), int32_t(e), &need) != MBQ_OK) Py_RETURN_NONE;
   at::AutoDispatchBelowADInplaceOrView guard;
-  const at::Tensor ids = empty({t, top}, at::kInt, *x), weights = empty({t, top}, at::kFloat, *x),
-                   perm = empty({t * top}, at::kInt, *x), offsets = empty({e + 1}, at::kInt, *x),
-                   place = empty({t, top}, at::kInt, *x);
+  // ids, place, perm and offsets share one allocation
+  const at::Tensor weights = empty({t, top}, at::kFloat, *x), all = empty({3 * t * top + e + 1}, at::kInt, *x);
+  const at::Tensor ids = part(all, 0, {t, top}), place = part(all, t * top, {t, top}), perm = part(all, 2 * t * top, {t * top}),
+                   offsets = part(all, 3 * t * top, {e + 1});
   at::Tensor ws;
   if (need) ws = empty({int64_t(need)}, at::kByte, *x);
   const auto ints = [](const at::Tensor& v) { return static_cast<int32_t*>(v.data_ptr()); };

@@ -18,11 +18,12 @@ struct RouteArgs {
   int32_t* ids;
   float* weights;
   int32_t *perm, *offsets, *place;
-  uint8_t* hist;  // [ceil(t / 16)][e rounded up to 4]: tokens of the group that took the expert
+  uint8_t* hist;  // [e][pitch]: tokens of the group of 16 that took the expert
+  int64_t pitch;  // groups, rounded up to spans
   int32_t* span;  // beyond one span: [spans + 1][e], tokens before the span that took the expert; last: all
 };
 
-__device__ __host__ inline int pad4(int e) { return (e + 3) & ~3; }
+constexpr int kSpanGroups = kSpan / kGroup;
 
 // Bits that order as the values do (-0 as +0).
 __device__ __forceinline__ uint32_t order_key(float v) {
@@ -31,15 +32,6 @@ __device__ __forceinline__ uint32_t order_key(float v) {
 }
 constexpr uint32_t kKeyNegInf = 0x007FFFFFu;  // order_key(-infinity)
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k); }
-
-__device__ __forceinline__ float sum64(float v) {
-  v += across<1>(v);
-  v += across<2>(v);
-  v += across<4>(v);
-  v += across<8>(v);
-  v += across<16>(v);
-  return v + across<32>(v);
-}
 
 // One token by one wave: lane l holds logits l V .. l V + V - 1.  Every round takes the wave's
 // largest key; among equal ones the lowest lane and in it the lowest element, which is the
@@ -114,9 +106,9 @@ __device__ __forceinline__ int choose(const RouteArgs& a, int64_t token, float& 
 // The choices of 16 tokens, a wave each, and their histogram.
 template <bool BF16, int V, bool SIGMOID>
 __global__ __launch_bounds__(1024) void choose_kernel(RouteArgs a) {
-  __shared__ uint32_t count[V * 16];  // four experts a word
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, words = pad4(a.e) / 4;
-  for (int i = threadIdx.x; i < words; i += 1024) count[i] = 0;
+  __shared__ uint32_t count[V * 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int i = threadIdx.x; i < a.e; i += 1024) count[i] = 0;
   __syncthreads();
   const int64_t token = int64_t(blockIdx.x) * kGroup + wave;
   if (token < a.t) {
@@ -125,35 +117,51 @@ __global__ __launch_bounds__(1024) void choose_kernel(RouteArgs a) {
     if (lane < a.top) {
       a.ids[token * a.top + lane] = id;
       a.weights[token * a.top + lane] = weight;
-      if (id >= 0) atomicAdd(&count[id >> 2], 1u << (8 * (id & 3)));  // a sum: its order is free
+      if (id >= 0) atomicAdd(&count[id], 1u);  // a sum: its order is free
     }
   }
   __syncthreads();
-  uint32_t* out = reinterpret_cast<uint32_t*>(a.hist + int64_t(blockIdx.x) * pad4(a.e));
-  for (int i = threadIdx.x; i < words; i += 1024) out[i] = count[i];
+  for (int i = threadIdx.x; i < a.e; i += 1024) a.hist[i * a.pitch + blockIdx.x] = uint8_t(count[i]);
 }
 
-// Histograms of groups g0 .. g1 - 1 added per expert, into sums[e]; 1024 threads, a quarter of
-// the experts' words each for a share of the groups.
-__device__ __forceinline__ void add_groups(const RouteArgs& a, int64_t g0, int64_t g1, int32_t* sums) {
-  const int words = pad4(a.e) / 4, lanes = 1024 / words, share = threadIdx.x / words, word = threadIdx.x - share * words;
-  if (share >= lanes) return;
-  int32_t s[4] = {0, 0, 0, 0};
-#pragma unroll 4
-  for (int64_t g = g0 + share; g < g1; g += lanes) {
-    const uint32_t v = reinterpret_cast<const uint32_t*>(a.hist + g * pad4(a.e))[word];
+// The tokens of a span that took each expert: those of groups before `mine` (a multiple of 4)
+// into before[e], the others into rest[e].  1024 threads: 2^k a expert, as many as there are, up to
+// one for each 16 of the span's 256 groups, summing four groups a instruction.
+__device__ __forceinline__ void add_groups(const RouteArgs& a, int64_t span, int mine, int32_t* before, int32_t* rest) {
+  int lanes = 16;
+  while (lanes * a.e > 1024) lanes >>= 1;
+  const int e = threadIdx.x / lanes, l = threadIdx.x - e * lanes;
+  const int64_t g0 = span * kSpanGroups, groups = (int64_t(a.t) + kGroup - 1) / kGroup;
+  const int there = int(min(groups - g0, int64_t(kSpanGroups)));
+  uint32_t s0 = 0, s1 = 0;
+  if (e < a.e) {
+    const u32x4_t* row = reinterpret_cast<const u32x4_t*>(a.hist + e * a.pitch + g0);
+    for (int c = l; c * 16 < there; c += lanes) {
+      const u32x4_t v = row[c];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s[i] += int32_t(v >> (8 * i) & 255u);
+      for (int i = 0; i < 4; ++i) {
+        const int g = c * 16 + 4 * i, n = there - g;  // bytes past the last group are no counts
+        const uint32_t w = n >= 4 ? v[i] : n <= 0 ? 0u : v[i] & (0xFFFFFFFFu >> (8 * (4 - n)));
+        const bool late = g >= mine;
+        s0 = __builtin_amdgcn_sad_u8(late ? 0u : w, 0u, s0);
+        s1 = __builtin_amdgcn_sad_u8(late ? w : 0u, 0u, s1);
+      }
+    }
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (s[i]) atomicAdd(&sums[word * 4 + i], s[i]);
+  if (lanes > 1) s0 += across<1>(s0), s1 += across<1>(s1);
+  if (lanes > 2) s0 += across<2>(s0), s1 += across<2>(s1);
+  if (lanes > 4) s0 += across<4>(s0), s1 += across<4>(s1);
+  if (lanes > 8) s0 += across<8>(s0), s1 += across<8>(s1);
+  if (e < a.e && l == 0) {
+    before[e] += int32_t(s0);
+    rest[e] += int32_t(s1);
+  }
 }
 
-// Exclusive sums of total[0 .. e - 1] to first[0 .. e] (1024 threads, e <= 1024).
-__device__ __forceinline__ void scan_experts(int e, const int32_t* total, int32_t* first) {
+// Exclusive sums of the threads' counts, an expert each, to first[0 .. e] (1024 threads, e <= 1024).
+__device__ __forceinline__ void scan_experts(int e, int32_t v, int32_t* first) {
   __shared__ int32_t part[16];
-  const int tid = threadIdx.x, v = tid < e ? total[tid] : 0, upto = scan64(v);
+  const int tid = threadIdx.x, upto = scan64(v);
   if ((tid & 63) == 63) part[tid >> 6] = upto;
   __syncthreads();
   int before = 0;
@@ -165,11 +173,10 @@ __device__ __forceinline__ void scan_experts(int e, const int32_t* total, int32_
 
 // Beyond one span: the tokens of a span that took each expert.
 __global__ __launch_bounds__(1024) void span_kernel(RouteArgs a) {
-  __shared__ int32_t sums[kMaxExperts];
+  __shared__ int32_t sums[kMaxExperts], none[kMaxExperts];
   sums[threadIdx.x] = 0;
   __syncthreads();
-  const int64_t groups = (int64_t(a.t) + kGroup - 1) / kGroup, g0 = int64_t(blockIdx.x) * (kSpan / kGroup);
-  add_groups(a, g0, min(g0 + kSpan / kGroup, groups), sums);
+  add_groups(a, blockIdx.x, kSpanGroups, sums, none);
   __syncthreads();
   if (int(threadIdx.x) < a.e) a.span[int64_t(blockIdx.x) * a.e + threadIdx.x] = sums[threadIdx.x];
 }
@@ -187,52 +194,60 @@ __global__ __launch_bounds__(64) void span_scan_kernel(RouteArgs a, int spans) {
   a.span[int64_t(spans) * a.e + e] = before;
 }
 
-// The places of 64 tokens' copies: tokens before them that took the expert, from the
-// histograms, and among the 64 a mask of bits an expert, whose bits below a token's are the
-// tokens before it.  masks and base in LDS, ready to be added to.
-__device__ __forceinline__ void place_tokens(const RouteArgs& a, int64_t t0, const int32_t* first, const int32_t* base,
-                                             const uint64_t* mask) {
-  const int pairs = int(min(int64_t(kPlaced), a.t - t0)) * a.top;
-  for (int i = threadIdx.x; i < pairs; i += 1024) {
-    const int token = i / a.top;
-    const int id = a.ids[t0 * a.top + i];
-    int at = -1;
-    if (id >= 0) {
-      at = first[id] + base[id] + __popcll(mask[id] & ((uint64_t(1) << token) - 1));
-      a.perm[at] = int32_t(t0 + token);
+// The places of 64 tokens' copies: behind the copies of the tokens before them that took the
+// expert, base[e], and of those among the 64, the bits below the token's in mask[e].
+constexpr int kHeld = kPlaced * MBQ_MAX_EXPERT_TOP / 1024;  // copies a thread
+struct Held {
+  int32_t id[kHeld];
+  __device__ __forceinline__ Held(const RouteArgs& a, int64_t t0, int pairs) {
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+      const int i = threadIdx.x + h * 1024;
+      id[h] = i < pairs ? a.ids[t0 * a.top + i] : -1;
     }
-    a.place[t0 * a.top + i] = at;
   }
-}
-__device__ __forceinline__ void mark_tokens(const RouteArgs& a, int64_t t0, uint64_t* mask) {
-  const int pairs = int(min(int64_t(kPlaced), a.t - t0)) * a.top;
-  for (int i = threadIdx.x; i < pairs; i += 1024) {
-    const int id = a.ids[t0 * a.top + i];
-    if (id >= 0) atomicOr(reinterpret_cast<unsigned long long*>(&mask[id]), 1ull << (i / a.top));
+  __device__ __forceinline__ void mark(const RouteArgs& a, uint64_t* mask) const {
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h)
+      if (id[h] >= 0)
+        atomicOr(reinterpret_cast<unsigned long long*>(&mask[id[h]]), 1ull << ((threadIdx.x + h * 1024) / a.top));
   }
-}
+  __device__ __forceinline__ void place(const RouteArgs& a, int64_t t0, int pairs, const int32_t* first, const int32_t* base,
+                                        const uint64_t* mask) const {
+#pragma unroll
+    for (int h = 0; h < kHeld; ++h) {
+      const int i = threadIdx.x + h * 1024, token = i / a.top;
+      if (i >= pairs) continue;
+      int at = -1;
+      if (id[h] >= 0) {
+        at = first[id[h]] + base[id[h]] + __popcll(mask[id[h]] & ((uint64_t(1) << token) - 1));
+        a.perm[at] = int32_t(t0 + token);
+      }
+      a.place[t0 * a.top + i] = at;
+    }
+  }
+};
 
 __global__ __launch_bounds__(1024) void place_kernel(RouteArgs a) {
   __shared__ int32_t base[kMaxExperts], total[kMaxExperts], first[kMaxExperts + 1];
   __shared__ uint64_t mask[kMaxExperts];
   const int tid = threadIdx.x;
-  const int64_t t0 = int64_t(blockIdx.x) * kPlaced, groups = (int64_t(a.t) + kGroup - 1) / kGroup, g = t0 / kGroup;
-  const int64_t s = t0 / kSpan, spans = (int64_t(a.t) + kSpan - 1) / kSpan;
+  const int64_t t0 = int64_t(blockIdx.x) * kPlaced, s = t0 / kSpan, spans = (int64_t(a.t) + kSpan - 1) / kSpan;
   const bool many = spans > 1;
-  if (tid < pad4(a.e)) {
-    base[tid] = many && tid < a.e ? a.span[s * a.e + tid] : 0;
-    total[tid] = many && tid < a.e ? a.span[spans * a.e + tid] : 0;
+  const int pairs = int(min(int64_t(kPlaced), a.t - t0)) * a.top;
+  const Held held(a, t0, pairs);
+  if (tid < a.e) {
+    base[tid] = many ? a.span[s * a.e + tid] : 0;
+    total[tid] = 0;
     mask[tid] = 0;
   }
   __syncthreads();
-  add_groups(a, s * (kSpan / kGroup), g, base);
-  if (!many) add_groups(a, g, groups, total);
-  mark_tokens(a, t0, mask);
+  add_groups(a, s, int((t0 - s * kSpan) / kGroup), base, total);
+  held.mark(a, mask);
   __syncthreads();
-  if (!many && tid < a.e) total[tid] += base[tid];
-  __syncthreads();
-  scan_experts(a.e, total, first);
-  place_tokens(a, t0, first, base, mask);
+  const int32_t all_of = tid >= a.e ? 0 : many ? a.span[spans * a.e + tid] : total[tid] + base[tid];
+  scan_experts(a.e, all_of, first);
+  held.place(a, t0, pairs, first, base, mask);
   if (blockIdx.x == 0)
     for (int i = tid; i <= a.e; i += 1024) a.offsets[i] = first[i];
   const int64_t all = int64_t(a.t) * a.top;  // rows of no copy
@@ -242,7 +257,7 @@ __global__ __launch_bounds__(1024) void place_kernel(RouteArgs a) {
 // At most 64 tokens: everything in one workgroup.
 template <bool BF16, int V, bool SIGMOID>
 __global__ __launch_bounds__(1024) void route_few_kernel(RouteArgs a) {
-  __shared__ int32_t base[kMaxExperts], total[kMaxExperts], first[kMaxExperts + 1];
+  __shared__ int32_t base[kMaxExperts], first[kMaxExperts + 1];
   __shared__ uint64_t mask[kMaxExperts];
   const int tid = threadIdx.x, lane = tid & 63;
   if (tid < a.e) {
@@ -261,28 +276,29 @@ __global__ __launch_bounds__(1024) void route_few_kernel(RouteArgs a) {
   }
   __threadfence_block();
   __syncthreads();
-  if (tid < a.e) total[tid] = __popcll(mask[tid]);
-  __syncthreads();
-  scan_experts(a.e, total, first);
-  place_tokens(a, 0, first, base, mask);
+  scan_experts(a.e, tid < a.e ? __popcll(mask[tid]) : 0, first);
+  const Held held(a, 0, a.t * a.top);
+  held.place(a, 0, a.t * a.top, first, base, mask);
   for (int i = tid; i <= a.e; i += 1024) a.offsets[i] = first[i];
   for (int i = first[a.e] + tid; i < a.t * a.top; i += 1024) a.perm[i] = -1;
 }
 
 // y[t] = residual[t] + sum_j weights[t][j] rows[place[t][j]], eight outputs a thread, the
-// copies' rows asked for U at a time.  Bound by traffic.  A place outside the rows adds its
+// copies' rows asked for U at a time.  Bound by traffic (8192 x 4096, 8 copies: 5.3 TB/s), and
+// for a few tokens by the way of a place and then a row.  The last piece of a row reads the
+// row's last eight elements and keeps those of its own.  A place outside the rows adds its
 // weight times 0: nothing, or NaN where the weight is one.
 template <bool BF16, bool RBF>
 __global__ __launch_bounds__(256) void combine_kernel(int32_t t, int32_t n, int32_t top, int32_t p, const void* __restrict__ rows,
                                                       int64_t ldr, const float* __restrict__ weights,
                                                       const int32_t* __restrict__ place, const void* residual,
                                                       int64_t ldres, void* y, int64_t ldy) {
-  constexpr int U = 4;
+  constexpr int U = 8;
   const int pieces = (n + 7) / 8;
   const int64_t all = int64_t(t) * pieces;
   for (int64_t b = int64_t(blockIdx.x) * 256 + threadIdx.x; b < all; b += int64_t(gridDim.x) * 256) {
     const int64_t token = b / pieces;
-    const int col = int(b - token * pieces) * 8;
+    const int own = int(b - token * pieces) * 8, col = max(min(own, n - 8), 0);
     float v[8], sum[8];
     if (residual) {
       load8<RBF>(static_cast<const uint8_t*>(residual) + token * ldres * (RBF ? 2 : 4), col, n, sum);
@@ -293,13 +309,23 @@ __global__ __launch_bounds__(256) void combine_kernel(int32_t t, int32_t n, int3
     for (int j0 = 0; j0 < top; j0 += U) {
       Raw8<BF16> raw[U];
       float w[U];
+      int at[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int j = min(j0 + u, top - 1);
-        const int at = place[token * top + j];
-        const bool there = uint32_t(at) < uint32_t(p);
-        w[u] = j0 + u < top ? weights[token * top + j] : 0.f;
-        raw[u].load(static_cast<const uint8_t*>(rows) + (there ? at : 0) * ldr * (BF16 ? 2 : 4), col, there && j0 + u < top ? n : 0);
+        at[u] = place[token * top + j];
+        w[u] = weights[token * top + j];
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const bool there = uint32_t(at[u]) < uint32_t(p) && j0 + u < top;
+        if (j0 + u >= top) w[u] = 0.f;
+        if (there) {
+          raw[u].load(static_cast<const uint8_t*>(rows) + at[u] * ldr * (BF16 ? 2 : 4), col, n);
+        } else {
+#pragma unroll
+          for (int h = 0; h < (BF16 ? 1 : 2); ++h) raw[u].w[h] = u32x4_t{0, 0, 0, 0};
+        }
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -308,12 +334,23 @@ __global__ __launch_bounds__(256) void combine_kernel(int32_t t, int32_t n, int3
         for (int e = 0; e < 8; ++e) sum[e] = fmaf(w[u], v[e], sum[e]);
       }
     }
-    store8<RBF>(static_cast<uint8_t*>(y) + token * ldy * (RBF ? 2 : 4), col, n, sum);
+    uint8_t* out = static_cast<uint8_t*>(y) + token * ldy * (RBF ? 2 : 4);
+    if (col == own) {
+      store8<RBF>(out, col, n, sum);
+    } else {  // the elements before its own are another thread's
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (col + e >= own) {
+          if constexpr (RBF) reinterpret_cast<uint16_t*>(out)[col + e] = uint16_t(bf16_pair(sum[e], 0.f));
+          else reinterpret_cast<float*>(out)[col + e] = sum[e];
+        }
+    }
   }
 }
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
-size_t hist_bytes(int32_t t, int32_t e) { return align256(size_t((t + kGroup - 1) / kGroup) * pad4(e)); }
+int64_t hist_pitch(int32_t t) { return (int64_t(t) + kSpan - 1) / kSpan * kSpanGroups; }
+size_t hist_bytes(int32_t t, int32_t e) { return align256(size_t(hist_pitch(t)) * e); }
 
 template <bool BF16, int V, bool SIGMOID>
 void launch_route(const RouteArgs& a, hipStream_t stream) {
@@ -351,7 +388,7 @@ hipError_t launch_expert_route(int32_t t, int32_t e, const void* logits, bool bf
                                bool normalize, float scale, int32_t* ids, float* weights, int32_t* perm, int32_t* offsets,
                                int32_t* place, void* ws, hipStream_t stream) {
   uint8_t* w = static_cast<uint8_t*>(ws);
-  const RouteArgs a{logits, ld, t, e, top, normalize, scale, ids, weights, perm, offsets, place, w,
+  const RouteArgs a{logits, ld, t, e, top, normalize, scale, ids, weights, perm, offsets, place, w, hist_pitch(t),
                     reinterpret_cast<int32_t*>(w + (t > kPlaced ? hist_bytes(t, e) : 0))};
   if (bf16) sigmoid ? launch_route<true, true>(a, stream) : launch_route<true, false>(a, stream);
   else sigmoid ? launch_route<false, true>(a, stream) : launch_route<false, false>(a, stream);

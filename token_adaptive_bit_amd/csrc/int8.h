@@ -39,11 +39,23 @@ __device__ __forceinline__ void store_int8x8(uint8_t* row, int64_t i, int64_t n,
   }
 }
 
-// Largest of a wave, in all its lanes.
+// Largest of a wave, the same for all its lanes: rows of 16 by register moves, the four rows
+// by scalar reads (an exchange through LDS takes longer than all of it).
 __device__ __forceinline__ uint32_t max64(uint32_t m) {
   m = max16(m);
-  m = max(m, across<16>(m));
-  return max(m, across<32>(m));
+  const uint32_t a = __builtin_amdgcn_readlane(int(m), 0), b = __builtin_amdgcn_readlane(int(m), 16);
+  const uint32_t c = __builtin_amdgcn_readlane(int(m), 32), d = __builtin_amdgcn_readlane(int(m), 48);
+  return max(max(a, b), max(c, d));
+}
+
+// Sum of a wave, the same for all its lanes, in a fixed order.
+__device__ __forceinline__ float sum64(float v) {
+  v += across<1>(v);
+  v += across<2>(v);
+  v += across<4>(v);
+  v += across<8>(v);
+  const auto row = [&](int lane) { return __uint_as_float(__builtin_amdgcn_readlane(__float_as_int(v), lane)); };
+  return (row(0) + row(16)) + (row(32) + row(48));
 }
 
 // Inclusive sums over a wave's lanes: rows of 16 by shifts, then each row's last lane into the

@@ -10,6 +10,8 @@
 namespace mbq {
 namespace {
 
+constexpr int kUnits = 256;  // compute units
+
 struct Args {
   const uint8_t* codes;  // packed tiles
   const float* ws;       // weight scales [experts][16 rbs], in the tiles' order
@@ -30,9 +32,25 @@ struct Tile {
   int expert, first, count;
 };
 
-// The expert that the tile-th tile of at most T rows, counted through the experts in their
-// order, belongs to: its rows, and the number of its first tile.  Offsets are data: whatever
-// they hold, the rows found lie in 0 .. p - 1.
+// The experts' rows, and their tiles of at most T rows counted through the experts in their
+// order.  Offsets are data: whatever they hold, the rows found lie in 0 .. p - 1.
+template <int T>
+__device__ __forceinline__ int tiles_at(const Args& a, int e, int& lo, int& hi) {
+  lo = hi = 0;
+  if (e < a.experts) {
+    lo = min(max(a.offsets[e], 0), a.p);
+    hi = min(max(a.offsets[e + 1], lo), a.p);
+  }
+  return (hi - lo + T - 1) / T;
+}
+template <int T>
+__device__ __forceinline__ int count_tiles(const Args& a) {
+  int tiles = 0, lo, hi;
+#pragma unroll 4
+  for (int e = threadIdx.x & 63; e < a.experts; e += 64) tiles += tiles_at<T>(a, e, lo, hi);
+  return __builtin_amdgcn_readlane(scan64(tiles), 63);
+}
+// The expert that a tile belongs to: its rows, and the number of its first tile.
 struct Group {
   int expert, first, count, tile0;
 };
@@ -41,12 +59,8 @@ __device__ __forceinline__ Group find_group(const Args& a, int tile) {
   const int lane = threadIdx.x & 63;
   int before = 0;
   for (int e0 = 0; e0 < a.experts; e0 += 64) {
-    int lo = 0, hi = 0;
-    if (e0 + lane < a.experts) {
-      lo = min(max(a.offsets[e0 + lane], 0), a.p);
-      hi = min(max(a.offsets[e0 + lane + 1], lo), a.p);
-    }
-    const int tiles = (hi - lo + T - 1) / T, upto = before + scan64(tiles);
+    int lo, hi;
+    const int tiles = tiles_at<T>(a, e0 + lane, lo, hi), upto = before + scan64(tiles);
     const uint64_t past = __ballot(tile < upto);
     if (past) {
       const int l = __builtin_ctzll(past), first = __builtin_amdgcn_readlane(lo, l);
@@ -185,22 +199,39 @@ __global__ __launch_bounds__(64 * WN * WT, 1) void shared_kernel(Args a) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, c = lane >> 4;
   const int wn = wave % WN, wt = wave / WN;
-  // neighbouring tiles on one XCD
-  const int tiles_n = (a.rbs + kRb - 1) / kRb;
-  const int per = gridDim.x / 8, rest = gridDim.x % 8, xcd = blockIdx.x % 8;
-  const int wg = blockIdx.x / 8 + xcd * per + min(xcd, rest);
-  const int chunk = GROUPED ? 0 : wg % a.chunks, id = GROUPED ? wg : wg / a.chunks;
+  const int tiles_n = (a.rbs + kRb - 1) / kRb, tiles_t = GROUPED ? count_tiles<kTok>(a) : (a.t + kTok - 1) / kTok;
+  // Neighbouring tiles on one XCD, in rounds of one on each unit.  Tiles left over by the last
+  // whole round, if they are half a round or less, are cut into halves or quarters of their
+  // tokens, which the units share: the last round then takes about 85 or 75% of a whole one (8
+  // experts of 4096 x 14336, 16384 rows: 850 us from 893; 18944 x 3584, 1024 tokens 76 from 86).
+  const int64_t tiles = int64_t(tiles_n) * tiles_t * (GROUPED ? 1 : a.chunks);
+  const int left = int(tiles % kUnits), cut = tiles < kUnits || left == 0 || left > kUnits / 2 ? 1 : left > kUnits / 4 ? 2 : 4;
+  const int64_t whole = cut > 1 ? tiles - left : tiles;
+  const int xcd = blockIdx.x % 8;
+  int64_t wg;
+  int part = 0;
+  if (int64_t(blockIdx.x) < whole) {
+    wg = blockIdx.x / 8 + xcd * (whole / 8) + min(xcd, int(whole % 8));
+  } else {
+    const int b = int(blockIdx.x - whole) / 8;
+    wg = whole + b / cut * 8 + xcd;
+    part = b % cut;
+    if (cut == 1 || wg >= tiles) return;
+  }
+  const int chunk = GROUPED ? 0 : int(wg % a.chunks), id = GROUPED ? int(wg) : int(wg / a.chunks);
   const int kb0 = chunk * a.chunk_kb, kb1 = min(kb0 + a.chunk_kb, a.kb);
   Group g{0, 0, a.t, 0};
-  if constexpr (GROUPED) {
-    g = find_group<kTok>(a, id / tiles_n);
-    if (g.count == 0) return;
-  }
+  if constexpr (GROUPED) g = find_group<kTok>(a, id / tiles_n);
   // four token tiles of an expert by as many row tiles as it takes
   const int local = id - g.tile0 * tiles_n, four = local / (4 * tiles_n), in = local - four * 4 * tiles_n;
-  const int tiles_t = (g.count + kTok - 1) / kTok, gt = min(4, tiles_t - 4 * four);
+  const int gt = min(4, (g.count + kTok - 1) / kTok - 4 * four);
   const int rb0 = in / gt * kRb;
-  const Tile tile = tile_of<kTok>(g, 4 * four + in % gt);
+  Tile tile = tile_of<kTok>(g, 4 * four + in % gt);
+  if (cut > 1 && int64_t(blockIdx.x) >= whole) {
+    tile.first += part * (kTok / cut);
+    tile.count = min(tile.count - part * (kTok / cut), kTok / cut);
+    if (tile.count <= 0) return;
+  }
   const uint8_t* codes = a.codes + int64_t(tile.expert) * a.stride;
   const float* ws = a.ws + int64_t(tile.expert) * a.rbs * kRowBlock;
 
@@ -273,24 +304,40 @@ __global__ __launch_bounds__(64 * WN * WT, 1) void shared_kernel(Args a) {
   }
   to_lds_wait<(NX - 1) * kCopies + kAhead>();
   __syncthreads();
-  read(0, 0, 0);
   int wbuf = 0, xbuf = 0;
-  for (int kb = kb0; kb < kb1 - 1; ++kb) {
-    read(wbuf, xbuf, 1);
-    products(0);
-    const int wnext = wbuf == NW - 1 ? 0 : wbuf + 1, xnext = xbuf == NX - 1 ? 0 : xbuf + 1;
-    to_lds_wait<(NX - 2) * kCopies + kAhead>();  // block kb + 1 is in
+  const auto step = [&]() __attribute__((always_inline)) {  // the next block is in, and this one's buffers are free
+    to_lds_wait<(NX - 2) * kCopies + kAhead>();
     __syncthreads();
-    read(wnext, xnext, 0);
+  };
+  const auto refill = [&](int kb) __attribute__((always_inline)) {
     next_x(kb + NX, xbuf);
     next_w(kb + NW, wbuf);
+  };
+  const auto advance = [&]() __attribute__((always_inline)) {
+    wbuf = wbuf == NW - 1 ? 0 : wbuf + 1;
+    xbuf = xbuf == NX - 1 ? 0 : xbuf + 1;
+  };
+  if (wt * RT * 16 < tile.count) {
+    read(0, 0, 0);
+    for (int kb = kb0; kb < kb1 - 1; ++kb) {
+      read(wbuf, xbuf, 1);
+      products(0);
+      step();
+      read(wbuf == NW - 1 ? 0 : wbuf + 1, xbuf == NX - 1 ? 0 : xbuf + 1, 0);
+      refill(kb);
+      products(1);
+      advance();
+    }
+    read(wbuf, xbuf, 1);
+    products(0);
     products(1);
-    wbuf = wnext;
-    xbuf = xnext;
+  } else {  // a wave without tokens copies for the others
+    for (int kb = kb0; kb < kb1 - 1; ++kb) {
+      step();
+      refill(kb);
+      advance();
+    }
   }
-  read(wbuf, xbuf, 1);
-  products(0);
-  products(1);
   to_lds_wait<0>();  // none of them outlives the workgroup
 
   const int rbw = rb0 + wn * RN;
@@ -340,9 +387,11 @@ __global__ __launch_bounds__(64 * WN, 2) void direct_kernel(Args a) {
   __shared__ __align__(1024) uint8_t lds[kLds];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, c = lane >> 4;
-  // neighbouring tiles on one XCD
+  // neighbouring tiles on one XCD: of as many as there are (experts' rows may fill fewer than the grid)
   const int tiles_n = (a.rbs + kRb - 1) / kRb;
-  const int per = gridDim.x / 8, rest = gridDim.x % 8, xcd = blockIdx.x % 8;
+  const int all = GROUPED ? min(int64_t(count_tiles<kTok>(a)) * tiles_n, int64_t(gridDim.x)) : gridDim.x;
+  if (int(blockIdx.x) >= all) return;
+  const int per = all / 8, rest = all % 8, xcd = blockIdx.x % 8;
   const int wg = blockIdx.x / 8 + xcd * per + min(xcd, rest);
   const int chunk = GROUPED ? 0 : wg % a.chunks, id = GROUPED ? wg : wg / a.chunks;
   const int kb0 = chunk * a.chunk_kb, kb1 = min(kb0 + a.chunk_kb, a.kb);
@@ -664,7 +713,8 @@ template <int WN, int WT, int RN, int RT, int NW, int NX, int P, bool GROUPED>
 void launch_shared(const Args& a, hipStream_t stream) {
   const int64_t tiles_n = (a.rbs + WN * RN - 1) / (WN * RN), tok = 16 * WT * RT;
   const int64_t tiles_t = GROUPED ? a.p / tok + std::min(a.experts, a.p) : (a.p + tok - 1) / tok;
-  shared_kernel<WN, WT, RN, RT, NW, NX, P, GROUPED><<<uint32_t(tiles_n * tiles_t * a.chunks), 64 * WN * WT, 0, stream>>>(a);
+  // and room for the cut tiles of a last round
+  shared_kernel<WN, WT, RN, RT, NW, NX, P, GROUPED><<<uint32_t(tiles_n * tiles_t * a.chunks + 2 * kUnits), 64 * WN * WT, 0, stream>>>(a);
 }
 
 template <int WN, int RN, int RT, int D, int NX, int P, bool GROUPED>

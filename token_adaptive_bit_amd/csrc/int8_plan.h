@@ -89,9 +89,13 @@ inline Int8Plan plan_int8(int32_t t, int32_t p, int32_t experts, int32_t groups,
       const int per = (kb + s - 1) / s, chunks = (kb + per - 1) / per;
       if (chunks != s) continue;
       const float all = used * tiles_n * tiles_t * s / 256.f;
-      const float rounds = std::max(1.f, experts ? all + 0.5f : std::ceil(all - 1e-3f));  // of experts only an estimate
+      float rounds = std::max(1.f, experts ? all + 0.5f : std::ceil(all - 1e-3f));  // of experts only an estimate
+      if (f >= 9 && s == 1 && all > 1.f) {  // shared tiles cut those of a last part round
+        const float part = all - std::floor(all);
+        rounds = experts ? all + 0.3f : std::floor(all) + (part < 1e-3f ? 0.f : part <= 0.25f ? 0.75f : part <= 0.5f ? 0.87f : 1.f);
+      }
       const float wait = per * c.wait_us, work = rounds * per * c.block_us;
-      const float bytes = weight * (1.f + c.again * (tiles_t - 1.f)) / ((weight > 2e8f ? c.cold_tbs : c.tbs) * 1e6f);
+      const float bytes = weight / ((weight > 2e8f ? c.cold_tbs : c.tbs) * 1e6f) + weight * c.again * (tiles_t - 1.f) / (c.tbs * 1e6f);
       const float w2 = wait * wait, k2 = work * work, b2 = bytes * bytes;
       // starting and ending the workgroups; streaming ones of experts, which look for theirs first, run two at once
       const float starts = experts && stream ? std::max(0.f, all - (f == 1 ? 1.f : 2.f)) * (c.tile_us + 1.6f) : rounds * (c.tile_us + (experts ? 0.3f : 0.f));

@@ -23,7 +23,14 @@ __global__ __launch_bounds__(WR < 4 ? 256 : 64 * WR) void quantize_rows_kernel(i
   Raw8<BF16> held[kHeld];
   uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < kHeld; ++j) held[j].load(src, at + j * kStep, end);
+  for (int j = 0; j < kHeld; ++j) {
+    if (at + j * kStep < end) {
+      held[j].load(src, at + j * kStep, end);
+    } else {
+#pragma unroll
+      for (int h = 0; h < (BF16 ? 1 : 2); ++h) held[j].w[h] = u32x4_t{0, 0, 0, 0};
+    }
+  }
 #pragma unroll
   for (int j = 0; j < kHeld; ++j) {
     float v[8];
