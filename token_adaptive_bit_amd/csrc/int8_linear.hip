@@ -10,7 +10,8 @@
 namespace mbq {
 namespace {
 
-constexpr int kUnits = 256;  // compute units
+constexpr int kUnits = 256;            // compute units
+constexpr int kCutRoom = 2 * kUnits;  // workgroups that the cut tiles of a last round may take
 
 struct Args {
   const uint8_t* codes;  // packed tiles
@@ -204,7 +205,7 @@ __global__ __launch_bounds__(64 * WN * WT, 1) void shared_kernel(Args a) {
   // whole round, if they are half a round or less, are cut into halves or quarters of their
   // tokens, which the units share: the last round then takes about 85 or 75% of a whole one (8
   // experts of 4096 x 14336, 16384 rows: 850 us from 893; 18944 x 3584, 1024 tokens 76 from 86).
-  const int64_t tiles = int64_t(tiles_n) * tiles_t * (GROUPED ? 1 : a.chunks);
+  const int64_t tiles = min(int64_t(tiles_n) * tiles_t * (GROUPED ? 1 : a.chunks), int64_t(gridDim.x) - kCutRoom);
   const int left = int(tiles % kUnits), cut = tiles < kUnits || left == 0 || left > kUnits / 2 ? 1 : left > kUnits / 4 ? 2 : 4;
   const int64_t whole = cut > 1 ? tiles - left : tiles;
   const int xcd = blockIdx.x % 8;
@@ -714,7 +715,7 @@ void launch_shared(const Args& a, hipStream_t stream) {
   const int64_t tiles_n = (a.rbs + WN * RN - 1) / (WN * RN), tok = 16 * WT * RT;
   const int64_t tiles_t = GROUPED ? a.p / tok + std::min(a.experts, a.p) : (a.p + tok - 1) / tok;
   // and room for the cut tiles of a last round
-  shared_kernel<WN, WT, RN, RT, NW, NX, P, GROUPED><<<uint32_t(tiles_n * tiles_t * a.chunks + 2 * kUnits), 64 * WN * WT, 0, stream>>>(a);
+  shared_kernel<WN, WT, RN, RT, NW, NX, P, GROUPED><<<uint32_t(tiles_n * tiles_t * a.chunks + kCutRoom), 64 * WN * WT, 0, stream>>>(a);
 }
 
 template <int WN, int RN, int RT, int D, int NX, int P, bool GROUPED>
