@@ -7,6 +7,8 @@
 #include "int8.h"
 #include "int8_plan.h"
 
+#include <type_traits>
+
 namespace mbq {
 namespace {
 
@@ -253,18 +255,18 @@ __global__ __launch_bounds__(64 * WN * WT, 1) void shared_kernel(Args a) {
   }
   const int xread = r * 128 + 16 * (c ^ (r & 7));  // the lane's first half of an operand in a tile
 
-  auto copy_x = [&](int kb, int buf) __attribute__((always_inline)) {
+  // The i-th copy of a block, the tokens' first.  One path without tests: past the end the last
+  // block is copied again, to a buffer that no one reads, so that the copies on their way are
+  // always as many as the waits count.
+  auto copy_x = [&](int kb, int buf, int i) __attribute__((always_inline)) {
     // past the end of a row of codes (k no multiple of 128) the lane copies the row's first
     // bytes: they meet weight codes of 0
-    const int at = kb * kFp8Block + col;
-    const int off = at < a.xlim ? at : 0;
-#pragma unroll
-    for (int i = 0; i < kCopiesX; ++i) to_lds_from(xp[i] + off, lx + buf * (kTb * kFp8TileBytes) + (i * kWaves + wave) * 1024);
+    const int at = min(kb, kb1 - 1) * kFp8Block + col;
+    to_lds_from(xp[i] + (at < a.xlim ? at : 0), lx + buf * (kTb * kFp8TileBytes) + (i * kWaves + wave) * 1024);
   };
-  auto copy_w = [&](int kb, int buf) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < kCopiesW; ++i)
-      to_lds<16>(wp[i] + int64_t(kb) * kFp8TileBytes, uint32_t(lane) * 16, lw + buf * (kRb * kFp8TileBytes) + (i * kWaves + wave) * 1024);
+  auto copy_w = [&](int kb, int buf, int i) __attribute__((always_inline)) {
+    to_lds<16>(wp[i] + int64_t(min(kb, kb1 - 1)) * kFp8TileBytes, uint32_t(lane) * 16,
+               lw + buf * (kRb * kFp8TileBytes) + (i * kWaves + wave) * 1024);
   };
 
   i32x4_t acc[RN][RT];
@@ -279,64 +281,76 @@ __global__ __launch_bounds__(64 * WN * WT, 1) void shared_kernel(Args a) {
   auto read_x = [&](int buf, int half, int j) __attribute__((always_inline)) {
     x[half][j] = *reinterpret_cast<const u32x4_t*>(lx + (buf * kTb + wt * RT + j) * kFp8TileBytes + (xread ^ (64 * half)));
   };
-  auto products = [&](int half) __attribute__((always_inline)) {
+  // A half's products, a row of them at a time, and between the rows the reads of the half
+  // after it (done two rows before the end) and the copies, one by one: left to itself the
+  // compiler puts the reads behind the products and waits for them (3120 clocks a block, of which
+  // the products take 2048).
+  auto half = [&](int h, bool reads, int wbuf, int xbuf, auto copy) __attribute__((always_inline)) {
+    constexpr int kReads = RN + RT, kEach = RN > 2 ? (kReads + RN - 3) / (RN - 2) : kReads;
 #pragma unroll
-    for (int i = 0; i < RN; ++i)
+    for (int i = 0; i < RN; ++i) {
 #pragma unroll
-      for (int j = 0; j < RT; ++j) acc[i][j] = mfma_i8(w[half][i], x[half][j], acc[i][j]);
+      for (int j = 0; j < RT; ++j) acc[i][j] = mfma_i8(w[h][i], x[h][j], acc[i][j]);
+      __builtin_amdgcn_sched_barrier(0);  // the products first: a read before them would be waited for with theirs
+      if (reads)
+#pragma unroll
+        for (int q = i * kEach; q < (i + 1) * kEach && q < kReads; ++q) {
+          if (q < RT) read_x(xbuf, 1 - h, q);
+          else read_w(wbuf, 1 - h, q - RT);
+        }
+      copy(i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
-  auto read = [&](int wbuf, int xbuf, int half) __attribute__((always_inline)) {
-#pragma unroll
-    for (int j = 0; j < RT; ++j) read_x(xbuf, half, j);
-#pragma unroll
-    for (int i = 0; i < RN; ++i) read_w(wbuf, half, i);
-  };
+  auto none = [](int) {};
 
-  // One path without tests: past the end the last block is copied again, to a buffer that no
-  // one reads, so that the copies on their way are always as many as the waits count.
-  auto next_x = [&](int kb, int buf) __attribute__((always_inline)) { copy_x(min(kb, kb1 - 1), buf); };
-  auto next_w = [&](int kb, int buf) __attribute__((always_inline)) { copy_w(min(kb, kb1 - 1), buf); };
 #pragma unroll
-  for (int i = 0; i < NW - NX; ++i) next_w(kb0 + i, i);
+  for (int i = 0; i < NW - NX; ++i)
+#pragma unroll
+    for (int q = 0; q < kCopiesW; ++q) copy_w(kb0 + i, i, q);
 #pragma unroll
   for (int i = 0; i < NX; ++i) {
-    next_x(kb0 + i, i);
-    next_w(kb0 + i + NW - NX, i + NW - NX);
+#pragma unroll
+    for (int q = 0; q < kCopiesX; ++q) copy_x(kb0 + i, i, q);
+#pragma unroll
+    for (int q = 0; q < kCopiesW; ++q) copy_w(kb0 + i + NW - NX, i + NW - NX, q);
   }
   to_lds_wait<(NX - 1) * kCopies + kAhead>();
   __syncthreads();
   int wbuf = 0, xbuf = 0;
-  const auto step = [&]() __attribute__((always_inline)) {  // the next block is in, and this one's buffers are free
-    to_lds_wait<(NX - 2) * kCopies + kAhead>();
-    __syncthreads();
-  };
-  const auto refill = [&](int kb) __attribute__((always_inline)) {
-    next_x(kb + NX, xbuf);
-    next_w(kb + NW, wbuf);
-  };
-  const auto advance = [&]() __attribute__((always_inline)) {
-    wbuf = wbuf == NW - 1 ? 0 : wbuf + 1;
-    xbuf = xbuf == NX - 1 ? 0 : xbuf + 1;
-  };
   if (wt * RT * 16 < tile.count) {
-    read(0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < RT; ++j) read_x(0, 0, j);
+#pragma unroll
+    for (int i = 0; i < RN; ++i) read_w(0, 0, i);
     for (int kb = kb0; kb < kb1 - 1; ++kb) {
-      read(wbuf, xbuf, 1);
-      products(0);
-      step();
-      read(wbuf == NW - 1 ? 0 : wbuf + 1, xbuf == NX - 1 ? 0 : xbuf + 1, 0);
-      refill(kb);
-      products(1);
-      advance();
+      const int wnext = wbuf == NW - 1 ? 0 : wbuf + 1, xnext = xbuf == NX - 1 ? 0 : xbuf + 1;
+      half(0, true, wbuf, xbuf, none);
+      to_lds_wait<(NX - 2) * kCopies + kAhead>();  // the next block is in, and this one's buffers are free
+      __syncthreads();
+      half(1, true, wnext, xnext, [&](int i) __attribute__((always_inline)) {
+        constexpr int kEach = (kCopies + RN - 1) / RN;
+#pragma unroll
+        for (int q = i * kEach; q < (i + 1) * kEach && q < kCopies; ++q) {
+          if (q < kCopiesX) copy_x(kb + NX, xbuf, q);
+          else copy_w(kb + NW, wbuf, q - kCopiesX);
+        }
+      });
+      wbuf = wnext;
+      xbuf = xnext;
     }
-    read(wbuf, xbuf, 1);
-    products(0);
-    products(1);
+    half(0, true, wbuf, xbuf, none);
+    half(1, false, 0, 0, none);
   } else {  // a wave without tokens copies for the others
     for (int kb = kb0; kb < kb1 - 1; ++kb) {
-      step();
-      refill(kb);
-      advance();
+      to_lds_wait<(NX - 2) * kCopies + kAhead>();
+      __syncthreads();
+#pragma unroll
+      for (int q = 0; q < kCopiesX; ++q) copy_x(kb + NX, xbuf, q);
+#pragma unroll
+      for (int q = 0; q < kCopiesW; ++q) copy_w(kb + NW, wbuf, q);
+      wbuf = wbuf == NW - 1 ? 0 : wbuf + 1;
+      xbuf = xbuf == NX - 1 ? 0 : xbuf + 1;
     }
   }
   to_lds_wait<0>();  // none of them outlives the workgroup
@@ -453,34 +467,44 @@ __global__ __launch_bounds__(64 * WN, 2) void direct_kernel(Args a) {
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < RT; ++j) read_x(0, 0, j);
+  // Left to itself the compiler puts the reads behind the products and waits for them (13824 x
+  // 5120, 64 tokens 19.3 us from 16.7 so); the largest tile has no registers for another order.
+  constexpr bool kPinned = RN * RT <= 16;
   int buf = 0;
-  for (int kb = kb0; kb < kb1; kb += D) {
+  // The weight's block is in slot s. The wait leaves on their way what is issued after the next
+  // block's codes: copies, and with ahead set the weight's loads. The blocks behind the loop load
+  // nothing: what no product uses the compiler takes out, and the wait would count loads not made.
+  auto block = [&](int kb, int s, auto ahead) __attribute__((always_inline)) {
+    constexpr bool kAhead = decltype(ahead)::value;
+    const int next = buf == NX - 1 ? 0 : buf + 1;
 #pragma unroll
-    for (int s = 0; s < D; ++s) {
-      if (kb + s < kb1) {
-        const int next = buf == NX - 1 ? 0 : buf + 1;
+    for (int j = 0; j < RT; ++j) {
 #pragma unroll
-        for (int j = 0; j < RT; ++j) {
-#pragma unroll
-          for (int i = 0; i < RN; ++i) acc[i][j] = mfma_i8(w[s][0][i], x[j], acc[i][j]);
-          read_x(buf, 1, j);
-        }
-        load_w(kb + s + D, s, 0);
-        // the next block's codes are in: at most the copies and loads issued after them are on their way
-        to_lds_wait<(NX - 2) * kCopiesX + ((NX - 2) * 2 + 2) * RN>();
-        __syncthreads();
-        copy_x(kb + s + NX, buf);
-#pragma unroll
-        for (int j = 0; j < RT; ++j) {
-#pragma unroll
-          for (int i = 0; i < RN; ++i) acc[i][j] = mfma_i8(w[s][1][i], x[j], acc[i][j]);
-          read_x(next, 0, j);
-        }
-        load_w(kb + s + D, s, 1);
-        buf = next;
-      }
+      for (int i = 0; i < RN; ++i) acc[i][j] = mfma_i8(w[s][0][i], x[j], acc[i][j]);
+      read_x(buf, 1, j);
+      if constexpr (kPinned) __builtin_amdgcn_sched_barrier(0);
     }
-  }
+    if constexpr (kAhead) load_w(kb + D, s, 0);
+    to_lds_wait<(NX - 2) * kCopiesX + (kAhead ? ((NX - 2) * 2 + 2) * RN : 0)>();
+    __syncthreads();
+    copy_x(kb + NX, buf);
+#pragma unroll
+    for (int j = 0; j < RT; ++j) {
+#pragma unroll
+      for (int i = 0; i < RN; ++i) acc[i][j] = mfma_i8(w[s][1][i], x[j], acc[i][j]);
+      read_x(next, 0, j);
+      if constexpr (kPinned) __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (kAhead) load_w(kb + D, s, 1);
+    buf = next;
+  };
+  int kb = kb0;
+  for (; kb + D <= kb1; kb += D)
+#pragma unroll
+    for (int s = 0; s < D; ++s) block(kb + s, s, std::true_type{});
+#pragma unroll
+  for (int s = 0; s < D - 1; ++s)
+    if (kb + s < kb1) block(kb + s, s, std::false_type{});
   to_lds_wait<0>();  // none of them outlives the workgroup
   if (!GROUPED && a.chunks > 1) {
 #pragma unroll
