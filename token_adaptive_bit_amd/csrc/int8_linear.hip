@@ -761,7 +761,8 @@ void launch_stream(const Args& a, mbq_dtype x_dtype, hipStream_t stream) {
       return;
     }
   }
-  stream_kernel<W, TT, MBQ_INT8, P, GROUPED><<<grid, block, 0, stream>>>(a);
+  // one weight's codes go to 16 waves
+  if constexpr (W != 8 || TT != 1 || GROUPED) stream_kernel<W, TT, MBQ_INT8, P, GROUPED><<<grid, block, 0, stream>>>(a);
 }
 
 template <int P, bool GROUPED>

@@ -18,32 +18,32 @@ constexpr int kInt8Forms = 11;
 // The time of a form: workgroups take rounds of one on each of the 256 compute units.  A
 // workgroup's blocks of K take wait_us each from one to the next (latency, hidden from one
 // workgroup to another), block_us each of the unit (throughput, added up over its
-// workgroups), and the weight's bytes their time at `tbs` (`cold_tbs` where they are more than
-// the last-level cache keeps), a part `again` of them for every further tile of tokens; the
-// three overlap.  tile_us starts and ends a workgroup, launch_us is paid once, and split K
-// (join_us) pays a second launch and the partial sums' traffic (join_tbs).  The times are a fit
-// to 9364 timings of every form on 13 weights, plain and gated, 1 to 4096 tokens (the best
-// split of each in profiles/int8_plan_timings.csv): the choice is 1.6% above the best on the
-// mean, 6% at the ninth tenth; for experts (70 drawn shapes, cold_tbs and the added terms are
-// theirs) 2.8% on the mean.  For instance, 5120 x 5120, us: 64 tokens 64 x 16 14.4, 128 x 64 14.9,
-// 256 x 128 18.4; 333 tokens 128 x 64 21.7, 256 x 128 27.2, 256 x 256 34.7; 2048 tokens 256 x 128
-// 63.7, 256 x 192 52.1, 256 x 256 56.3.
+// workgroups; of streaming ones token_us more for each token), and the weight's bytes their time
+// at `tbs` (`cold_tbs` where they are more than the last-level cache keeps), a part `again` of
+// them for every further tile of tokens; the three overlap.  tile_us starts and ends a
+// workgroup, launch_us is paid once, and split K (join_us) pays a second launch and the partial
+// sums' traffic (join_tbs).  The times are a fit to 9364 timings of every form on 13 weights, plain
+// and gated, 1 to 4096 tokens (the best split of each in profiles/int8_plan_timings.csv): the
+// choice is 2.0% above the best on the mean, 7% at the ninth tenth; for experts (70 drawn shapes,
+// cold_tbs and the added terms are theirs) 4.3% on the mean.  For instance, 5120 x 5120, us: 64 tokens
+// 128 x 16 12.3, 64 x 16 13.1, 256 x 128 18.6; 333 tokens 128 x 64 17.7, 256 x 128 27.6, 256 x 256 33.7;
+// 2048 tokens 256 x 128 65.0, 256 x 192 51.6, 256 x 256 60.2.
 struct Int8Cost {
   int rows, tokens;
-  float wait_us, block_us, tile_us, launch_us, tbs, cold_tbs, again, join_us, join_tbs;
+  float wait_us, block_us, token_us, tile_us, launch_us, tbs, cold_tbs, again, join_us, join_tbs;
 };
 constexpr Int8Cost kInt8Costs[kInt8Forms] = {
-    {16, 16, 0.010f, 0.041f, 0.60f, 5.3f, 7.4f, 5.0f, 0.00f, 0.f, 1.f},
-    {16, 16, 0.023f, 0.034f, 0.45f, 5.7f, 7.7f, 5.0f, 0.00f, 0.f, 1.f},
-    {16, 32, 0.010f, 0.094f, 0.31f, 5.9f, 6.5f, 5.6f, 0.00f, 0.f, 1.f},
-    {64, 16, 0.146f, 0.102f, 0.14f, 5.7f, 6.6f, 4.8f, 0.05f, 1.9f, 1.6f},
-    {128, 16, 0.223f, 0.176f, 0.38f, 4.9f, 6.5f, 4.9f, 0.09f, 2.2f, 2.3f},
-    {128, 32, 0.250f, 0.191f, 0.60f, 4.9f, 6.5f, 5.3f, 0.16f, 2.5f, 3.2f},
-    {128, 64, 0.341f, 0.232f, 0.78f, 5.3f, 6.4f, 5.4f, 0.28f, 2.2f, 3.2f},
-    {256, 64, 0.504f, 0.403f, 1.18f, 5.6f, 6.2f, 5.7f, 0.27f, 2.1f, 3.5f},
-    {256, 128, 0.707f, 0.661f, 2.16f, 7.0f, 5.9f, 5.6f, 0.44f, 1.3f, 3.6f},
-    {256, 192, 0.010f, 0.937f, 5.10f, 4.5f, 6.5f, 5.3f, 0.76f, 2.9f, 3.9f},
-    {256, 256, 0.010f, 1.183f, 6.24f, 5.1f, 6.1f, 5.3f, 0.91f, 2.4f, 3.8f}};
+    {16, 16, 0.029f, 0.011f, 0.0040f, 0.60f, 5.6f, 7.8f, 5.0f, 0.00f, 0.f, 1.f},
+    {16, 16, 0.026f, 0.010f, 0.0040f, 0.46f, 5.7f, 7.8f, 5.0f, 0.00f, 0.f, 1.f},
+    {16, 32, 0.010f, 0.031f, 0.0030f, 0.38f, 5.9f, 6.8f, 5.6f, 0.00f, 0.f, 1.f},
+    {64, 16, 0.058f, 0.097f, 0.f, 0.12f, 6.0f, 7.1f, 4.8f, 0.04f, 1.9f, 1.8f},
+    {128, 16, 0.010f, 0.164f, 0.f, 0.48f, 5.2f, 7.0f, 4.9f, 0.11f, 2.3f, 2.7f},
+    {128, 32, 0.010f, 0.188f, 0.f, 0.65f, 5.4f, 7.0f, 5.3f, 0.17f, 2.3f, 2.9f},
+    {128, 64, 0.010f, 0.226f, 0.f, 0.79f, 5.8f, 7.0f, 5.4f, 0.32f, 2.2f, 3.0f},
+    {256, 64, 0.289f, 0.403f, 0.f, 1.74f, 5.2f, 6.6f, 5.7f, 0.26f, 2.3f, 3.5f},
+    {256, 128, 0.777f, 0.638f, 0.f, 2.64f, 6.8f, 6.1f, 5.6f, 0.50f, 1.5f, 3.8f},
+    {256, 192, 0.010f, 0.772f, 0.f, 5.23f, 5.2f, 7.2f, 5.3f, 0.93f, 1.5f, 3.8f},
+    {256, 256, 0.452f, 0.970f, 0.f, 6.94f, 5.4f, 6.1f, 5.3f, 1.00f, 0.5f, 3.8f}};
 constexpr int kInt8Splits[] = {1, 2, 3, 4, 6, 8, 12};
 constexpr int kInt8Inline = 384;  // most blocks that are quantized in the kernel (48 KiB of LDS)
 
@@ -83,6 +83,7 @@ inline Int8Plan plan_int8(int32_t t, int32_t p, int32_t experts, int32_t groups,
       within = us < quantize;
       before = std::min(us, quantize);
     }
+    if (f == 0 && !experts && !within) continue;  // on codes of one weight 8 waves take 1.037 times as long as 16
     float last = 1e30f;
     for (int s : kInt8Splits) {
       if (s > 1 && (experts || stream || kb / s < 3 || tiles_n * tiles_t * s > 1100.f)) break;
@@ -94,7 +95,7 @@ inline Int8Plan plan_int8(int32_t t, int32_t p, int32_t experts, int32_t groups,
         const float part = all - std::floor(all);
         rounds = experts ? all + 0.3f : std::floor(all) + (part < 1e-3f ? 0.f : part <= 0.25f ? 0.75f : part <= 0.5f ? 0.87f : 1.f);
       }
-      const float wait = per * c.wait_us, work = rounds * per * c.block_us;
+      const float wait = per * c.wait_us, work = rounds * per * (c.block_us + c.token_us * std::min(rows, float(c.tokens)));
       const float bytes = weight / ((weight > 2e8f ? c.cold_tbs : c.tbs) * 1e6f) + weight * c.again * (tiles_t - 1.f) / (c.tbs * 1e6f);
       const float w2 = wait * wait, k2 = work * work, b2 = bytes * bytes;
       // starting and ending the workgroups; streaming ones of experts, which look for theirs first, run two at once
