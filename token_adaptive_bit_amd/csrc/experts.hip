@@ -103,7 +103,8 @@ __device__ __forceinline__ int choose(const RouteArgs& a, int64_t token, float& 
   return chosen;
 }
 
-// The choices of 16 tokens, a wave each, and their histogram.
+// The choices of 16 tokens, a wave each, and their histogram.  Bound by the chain of maxima, one
+// for each choice (4096 tokens of 128, 8 chosen: 5.2 us).
 template <bool BF16, int V, bool SIGMOID>
 __global__ __launch_bounds__(1024) void choose_kernel(RouteArgs a) {
   __shared__ uint32_t count[V * 64];
@@ -194,6 +195,7 @@ __global__ __launch_bounds__(64) void span_scan_kernel(RouteArgs a, int spans) {
   a.span[int64_t(spans) * a.e + e] = before;
 }
 
+// (4096 tokens of 128, 8 chosen: 4.0 us, of which a launch and the histograms' way are most.)
 // The places of 64 tokens' copies: behind the copies of the tokens before them that took the
 // expert, base[e], and of those among the 64, the bits below the token's in mask[e].
 constexpr int kHeld = kPlaced * MBQ_MAX_EXPERT_TOP / 1024;  // copies a thread
@@ -254,7 +256,7 @@ __global__ __launch_bounds__(1024) void place_kernel(RouteArgs a) {
   for (int64_t i = first[a.e] + int64_t(blockIdx.x) * 1024 + tid; i < all; i += int64_t(gridDim.x) * 1024) a.perm[i] = -1;
 }
 
-// At most 64 tokens: everything in one workgroup.
+// At most 64 tokens: everything in one workgroup (one token of 64, 6 chosen: 3.1 us, a launch).
 template <bool BF16, int V, bool SIGMOID>
 __global__ __launch_bounds__(1024) void route_few_kernel(RouteArgs a) {
   __shared__ int32_t base[kMaxExperts], first[kMaxExperts + 1];

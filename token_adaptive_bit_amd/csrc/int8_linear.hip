@@ -184,10 +184,11 @@ __device__ __forceinline__ void write_rows(const Args& a, const i32x4_t (&acc)[R
 // products run, the next half's operands are read from LDS; the barrier stands between the
 // halves, where the block's buffers have been read to their end and the next block's copies
 // are in, and frees the buffers for new ones.  The weight, which comes from farther away, has a
-// buffer more (4096 tokens, 3584 x 18944: 206 us from 213; 8 experts of 4096 x 14336, 16384
-// rows: 912 from 954).  256 x 256 fills LDS to its last byte: its reads and copies
-// take 2048 clocks a block, as many as the products.
-// (Four waves of 128 x 128, which read a third less, have nothing to hide a wait behind: 304 us.)
+// buffer more (256 x 256, 4096 tokens of 3584 x 18944: 205 us from 213; 8 experts of 4096 x 14336,
+// 16384 rows: 820 from 865).  256 x 256 fills LDS to its last byte: its reads and copies
+// take 2048 clocks a block, as many as the products, which keep the matrix units busy for 83% of
+// those 205 us (2.7 P op/s) and 71% of the experts'.  (Four waves of 128 x 128 would read a
+// third less, but have no registers for operands that are read ahead.)
 template <int WN, int WT, int RN, int RT, int NW, int NX, int P, bool GROUPED>
 __global__ __launch_bounds__(64 * WN * WT, 1) void shared_kernel(Args a) {
   constexpr int kWaves = WN * WT, kRb = WN * RN, kTb = WT * RT, kTok = 16 * kTb;
@@ -206,7 +207,7 @@ __global__ __launch_bounds__(64 * WN * WT, 1) void shared_kernel(Args a) {
   // Neighbouring tiles on one XCD, in rounds of one on each unit.  Tiles left over by the last
   // whole round, if they are half a round or less, are cut into halves or quarters of their
   // tokens, which the units share: the last round then takes about 85 or 75% of a whole one (8
-  // experts of 4096 x 14336, 16384 rows: 850 us from 893; 18944 x 3584, 1024 tokens 76 from 86).
+  // experts of 4096 x 14336, 16384 rows: 820 us from 848; 18944 x 3584, 1024 tokens 75 from 84).
   const int64_t tiles = min(int64_t(tiles_n) * tiles_t * (GROUPED ? 1 : a.chunks), int64_t(gridDim.x) - kCutRoom);
   const int left = int(tiles % kUnits), cut = tiles < kUnits || left == 0 || left > kUnits / 2 ? 1 : left > kUnits / 4 ? 2 : 4;
   const int64_t whole = cut > 1 ? tiles - left : tiles;
@@ -283,8 +284,8 @@ __global__ __launch_bounds__(64 * WN * WT, 1) void shared_kernel(Args a) {
   };
   // A half's products, a row of them at a time, and between the rows the reads of the half
   // after it (done two rows before the end) and the copies, one by one: left to itself the
-  // compiler puts the reads behind the products and waits for them (3120 clocks a block, of which
-  // the products take 2048).
+  // compiler puts the reads behind the products and waits for them (8 experts of 4096 x 14336,
+  // 16384 rows: 868 us against 820; 4096 tokens of 3584 x 18944 221 against 209).
   auto half = [&](int h, bool reads, int wbuf, int xbuf, auto copy) __attribute__((always_inline)) {
     constexpr int kReads = RN + RT, kEach = RN > 2 ? (kReads + RN - 3) / (RN - 2) : kReads;
 #pragma unroll
@@ -390,8 +391,9 @@ __global__ __launch_bounds__(64 * WN * WT, 1) void shared_kernel(Args a) {
 // the wave that owns its rows, D blocks ahead, and only the tokens' codes go through LDS (NX
 // buffers).  LDS is read for the tokens alone, and two and more workgroups fit a unit, whose
 // waits, starts and ends hide one another's.  (256 x 128 against the same tile with both
-// operands in LDS: 128 gated experts of 1536 x 4096, 32768 rows 546 us from 601; 11008 x 4096,
-// 2048 tokens 84 from 90.  Of the 546, the copies and loads alone take 494.)
+// operands in LDS: 128 gated experts of 1536 x 4096, 32768 rows 498 us from 515; 11008 x 4096,
+// 2048 tokens 88 from 96.)  Large tiles are bound by their loads (of the 498 us the matrix units
+// are busy for 55%), small ones by the weight's bytes or by the way of the first of them.
 template <int WN, int RN, int RT, int D, int NX, int P, bool GROUPED>
 __global__ __launch_bounds__(64 * WN, 2) void direct_kernel(Args a) {
   constexpr int kRb = WN * RN, kTok = 16 * RT;
@@ -468,7 +470,8 @@ __global__ __launch_bounds__(64 * WN, 2) void direct_kernel(Args a) {
 #pragma unroll
   for (int j = 0; j < RT; ++j) read_x(0, 0, j);
   // Left to itself the compiler puts the reads behind the products and waits for them (13824 x
-  // 5120, 64 tokens 19.3 us from 16.7 so); the largest tile has no registers for another order.
+  // 5120, 64 tokens in 128 x 64: 19.0 us against 18.3); the largest tile has no registers for
+  // another order.
   constexpr bool kPinned = RN * RT <= 16;
   int buf = 0;
   // The weight's block is in slot s. The wait leaves on their way what is issued after the next
@@ -556,7 +559,9 @@ __global__ __launch_bounds__(256) void join_kernel(Args a) {
 // Few tokens: a workgroup streams one row block (gated: the pair) for a tile of at most 16 TT
 // tokens; its W waves take every W-th 128-input block, and their sums meet in LDS.  A wave has
 // U blocks in its registers and the next U on their way; blocks past the end are loads out of
-// the buffer's range, so that no load of a step stands behind a test.
+// the buffer's range, so that no load of a step stands behind a test.  Bound by the weight's
+// bytes where they are many (4096 x 14336, one token 12.8 us with the launch: 4.6 TB/s) and by
+// the ways of x, a block and the sums where they are few (5120 x 5120 7.2 us without it).
 // XT: the type of x.  Codes (MBQ_INT8) are read from memory; a few float tokens are quantized
 // here, once a workgroup into LDS, which saves the quantizing launch.
 template <int W, int TT, int XT, int P, bool GROUPED>

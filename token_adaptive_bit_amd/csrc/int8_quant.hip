@@ -6,7 +6,8 @@ namespace mbq {
 namespace {
 
 // One token by WR waves, its elements held in registers between the maximum and the codes
-// (longer rows are read again).  Bound by traffic: x once, one byte a code.
+// (longer rows are read again).  Bound by traffic: x once, one byte a code (4096 rows of 18944
+// bfloat16 37 us, 6.3 TB/s).
 template <bool BF16, bool PAD, int WR>
 __global__ __launch_bounds__(WR < 4 ? 256 : 64 * WR) void quantize_rows_kernel(int32_t t, int32_t k, const void* __restrict__ x,
                                                                                int64_t ldx, uint8_t* __restrict__ q, int64_t ldq,
@@ -69,6 +70,7 @@ __global__ __launch_bounds__(WR < 4 ? 256 : 64 * WR) void quantize_rows_kernel(i
 
 // 16 rows of one weight of one expert per workgroup: 16 lanes a row, 128 inputs at a step,
 // first for the row's maximum and then for its codes (the second read comes from the caches).
+// Bound by traffic (codes of 128 experts of 1536 x 4096 345 us, 4.7 TB/s).
 template <int WT>  // 0 float32, 1 bfloat16, 2 codes with scales given
 __global__ __launch_bounds__(256) void pack_int8_kernel(mbq_int8_desc d, int32_t part, const void* __restrict__ w,
                                                         const float* __restrict__ w_scale, uint8_t* __restrict__ packed,
