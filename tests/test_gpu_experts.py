@@ -33,7 +33,7 @@ def check_route(api, logits, top, score="softmax", normalize=True, scale=1.0):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("t,e,top", [(1, 1, 1), (1, 64, 6), (2, 5, 5), (64, 128, 8), (65, 128, 8), (63, 130, 2), (200, 7, 3),
+@pytest.mark.parametrize("t,e,top", [(1, 1, 1), (1, 64, 6), (17, 9, 4), (32, 64, 6), (33, 257, 9), (2, 5, 5), (64, 128, 8), (65, 128, 8), (63, 130, 2), (200, 7, 3),
                                      (1000, 256, 8), (300, 1000, 32), (257, 300, 4), (129, 64, 1), (40, 1024, 32)])
 def test_route(api, t, e, top, dtype):
     rng = np.random.default_rng(t + e * 5 + top)
@@ -42,7 +42,7 @@ def test_route(api, t, e, top, dtype):
     check_route(api, z, top, "sigmoid", False, 2.5)
 
 
-@pytest.mark.parametrize("t", [5, 64, 90, 5000])
+@pytest.mark.parametrize("t", [5, 32, 33, 64, 90, 5000])
 def test_route_masks_ties_and_bad_rows(api, t):
     rng = np.random.default_rng(t)
     z = rng.standard_normal((t, 40)).astype(np.float32)

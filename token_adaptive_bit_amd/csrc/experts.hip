@@ -8,6 +8,7 @@ namespace {
 constexpr int kGroup = 16;     // tokens of a histogram: one count fits a byte, one token a wave
 constexpr int kSpan = 4096;    // tokens whose histograms one place workgroup adds up by itself
 constexpr int kPlaced = 64;    // tokens of a place workgroup: one bit each in a 64-bit mask
+constexpr int kFew = 32;       // most tokens that one workgroup routes by itself
 constexpr int kMaxExperts = 1024;
 
 struct RouteArgs {
@@ -256,7 +257,9 @@ __global__ __launch_bounds__(1024) void place_kernel(RouteArgs a) {
   for (int64_t i = first[a.e] + int64_t(blockIdx.x) * 1024 + tid; i < all; i += int64_t(gridDim.x) * 1024) a.perm[i] = -1;
 }
 
-// At most 64 tokens: everything in one workgroup (one token of 64, 6 chosen: 3.1 us, a launch).
+// At most 32 tokens: everything in one workgroup, two tokens a wave (one token of 64 experts, 6 chosen:
+// 3.1 us, a launch).  With launches, us here / by choose and place: 64 experts, 6 chosen: 32 tokens
+// 6.1 / 7.0, 64 tokens 9.2 / 7.1; 256 experts, 8 chosen: 32 tokens 9.8 / 9.2, 64 tokens 16.2 / 9.3.
 template <bool BF16, int V, bool SIGMOID>
 __global__ __launch_bounds__(1024) void route_few_kernel(RouteArgs a) {
   __shared__ int32_t base[kMaxExperts], first[kMaxExperts + 1];
@@ -356,7 +359,7 @@ size_t hist_bytes(int32_t t, int32_t e) { return align256(size_t(hist_pitch(t)) 
 
 template <bool BF16, int V, bool SIGMOID>
 void launch_route(const RouteArgs& a, hipStream_t stream) {
-  if (a.t <= kPlaced) {
+  if (a.t <= kFew) {
     route_few_kernel<BF16, V, SIGMOID><<<1, 1024, 0, stream>>>(a);
     return;
   }
@@ -381,7 +384,7 @@ void launch_route(const RouteArgs& a, hipStream_t stream) {
 }  // namespace
 
 size_t expert_route_workspace(int32_t t, int32_t e) {
-  if (t <= kPlaced) return 0;
+  if (t <= kFew) return 0;
   const int spans = (t + kSpan - 1) / kSpan;
   return hist_bytes(t, e) + (spans > 1 ? align256(size_t(spans + 1) * e * 4) : 0);
 }
@@ -391,7 +394,7 @@ hipError_t launch_expert_route(int32_t t, int32_t e, const void* logits, bool bf
                                int32_t* place, void* ws, hipStream_t stream) {
   uint8_t* w = static_cast<uint8_t*>(ws);
   const RouteArgs a{logits, ld, t, e, top, normalize, scale, ids, weights, perm, offsets, place, w, hist_pitch(t),
-                    reinterpret_cast<int32_t*>(w + (t > kPlaced ? hist_bytes(t, e) : 0))};
+                    reinterpret_cast<int32_t*>(w + (t > kFew ? hist_bytes(t, e) : 0))};
   if (bf16) sigmoid ? launch_route<true, true>(a, stream) : launch_route<true, false>(a, stream);
   else sigmoid ? launch_route<false, true>(a, stream) : launch_route<false, false>(a, stream);
   return hipGetLastError();
