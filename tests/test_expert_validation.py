@@ -120,7 +120,7 @@ def test_route_refuses():
     n = ctypes.c_size_t(0)
     assert L.mbq_expert_route_workspace(100, 8, ctypes.byref(n)) == OK and n.value > 0
     assert call(ws=None) == WS and call(wsb=n.value - 1) == WS and call(ws=P(FAKE + 4)) == WS
-    assert L.mbq_expert_route_workspace(64, 8, ctypes.byref(n)) == OK and n.value == 0
+    assert L.mbq_expert_route_workspace(32, 8, ctypes.byref(n)) == OK and n.value == 0
     assert L.mbq_expert_route_workspace(-1, 8, ctypes.byref(n)) == SHAPE and L.mbq_expert_route_workspace(4, 0, ctypes.byref(n)) == SHAPE
     assert L.mbq_expert_route_workspace(4, 8, None) == ARG
     for t in (1, 64, 65, 4096, 4097, 1 << 21):

@@ -33,8 +33,9 @@ def check_route(api, logits, top, score="softmax", normalize=True, scale=1.0):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("t,e,top", [(1, 1, 1), (1, 64, 6), (17, 9, 4), (32, 64, 6), (33, 257, 9), (2, 5, 5), (64, 128, 8), (65, 128, 8), (63, 130, 2), (200, 7, 3),
-                                     (1000, 256, 8), (300, 1000, 32), (257, 300, 4), (129, 64, 1), (40, 1024, 32)])
+@pytest.mark.parametrize("t,e,top", [(1, 1, 1), (1, 64, 6), (17, 9, 4), (32, 64, 6), (33, 257, 9), (2, 5, 5), (64, 128, 8),
+                                     (65, 128, 8), (63, 130, 2), (200, 7, 3), (1000, 256, 8), (300, 1000, 32), (257, 300, 4),
+                                     (129, 64, 1), (40, 1024, 32)])
 def test_route(api, t, e, top, dtype):
     rng = np.random.default_rng(t + e * 5 + top)
     z = torch.from_numpy((rng.standard_normal((t, e)) * 2).astype(np.float32)).to(DT[dtype]).to(DEV)   # bfloat16: many ties
