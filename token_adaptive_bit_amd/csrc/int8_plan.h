@@ -84,6 +84,8 @@ inline Int8Plan plan_int8(int32_t t, int32_t p, int32_t experts, int32_t groups,
       before = std::min(us, quantize);
     }
     if (f == 0 && !experts && !within) continue;  // on codes of one weight 8 waves take 1.037 times as long as 16
+    const float bytes = weight / ((weight > 2e8f ? c.cold_tbs : c.tbs) * 1e6f) + weight * c.again * (tiles_t - 1.f) / (c.tbs * 1e6f);
+    if (before + c.launch_us + bytes >= best_us) continue;  // no split is faster than that
     float last = 1e30f;
     for (int s : kInt8Splits) {
       if (s > 1 && (experts || stream || kb / s < 3 || tiles_n * tiles_t * s > 1100.f)) break;
@@ -96,7 +98,6 @@ inline Int8Plan plan_int8(int32_t t, int32_t p, int32_t experts, int32_t groups,
         rounds = experts ? all + 0.3f : std::floor(all) + (part < 1e-3f ? 0.f : part <= 0.25f ? 0.75f : part <= 0.5f ? 0.87f : 1.f);
       }
       const float wait = per * c.wait_us, work = rounds * per * (c.block_us + c.token_us * std::min(rows, float(c.tokens)));
-      const float bytes = weight / ((weight > 2e8f ? c.cold_tbs : c.tbs) * 1e6f) + weight * c.again * (tiles_t - 1.f) / (c.tbs * 1e6f);
       const float w2 = wait * wait, k2 = work * work, b2 = bytes * bytes;
       // starting and ending the workgroups; streaming ones of experts, which look for theirs first, run two at once
       const float starts = experts && stream ? std::max(0.f, all - (f == 1 ? 1.f : 2.f)) * (c.tile_us + 1.6f) : rounds * (c.tile_us + (experts ? 0.3f : 0.f));
