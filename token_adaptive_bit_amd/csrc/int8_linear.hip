@@ -784,6 +784,8 @@ hipError_t launch(Args& a, const Int8Plan& p, mbq_dtype x_dtype, hipStream_t str
     case Int8Form::kDirect128x64: launch_direct<4, 2, 4, 3, 3, P, GROUPED>(a, stream); break;
     case Int8Form::kDirect256x64: launch_direct<4, 4, 4, 2, 3, P, GROUPED>(a, stream); break;
     case Int8Form::kDirect256x128: launch_direct<4, 4, 8, 2, 2, P, GROUPED>(a, stream); break;
+    case Int8Form::kShared128x128: launch_shared<2, 4, 4, 2, 3, 3, P, GROUPED>(a, stream); break;
+    case Int8Form::kShared256x128: launch_shared<4, 2, 4, 4, 3, 3, P, GROUPED>(a, stream); break;
     case Int8Form::kShared256x192: launch_shared<2, 4, 8, 3, 3, 2, P, GROUPED>(a, stream); break;
     case Int8Form::kShared256x256: launch_shared<2, 4, 8, 4, 3, 2, P, GROUPED>(a, stream); break;
   }

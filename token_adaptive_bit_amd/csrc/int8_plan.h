@@ -11,9 +11,9 @@ namespace mbq {
 enum class Int8Form {
   kStream8x1, kStream16x1, kStream8x2,
   kDirect64x16, kDirect128x16, kDirect128x32, kDirect128x64, kDirect256x64, kDirect256x128,
-  kShared256x192, kShared256x256
+  kShared128x128, kShared256x128, kShared256x192, kShared256x256
 };
-constexpr int kInt8Forms = 11;
+constexpr int kInt8Forms = 13;
 
 // The time of a form: workgroups take rounds of one on each of the 256 compute units.  A
 // workgroup's blocks of K take wait_us each from one to the next (latency, hidden from one
@@ -22,9 +22,9 @@ constexpr int kInt8Forms = 11;
 // at `tbs` (`cold_tbs` where they are more than the last-level cache keeps), a part `again` of
 // them for every further tile of tokens; the three overlap.  tile_us starts and ends a
 // workgroup, launch_us is paid once, and split K (join_us) pays a second launch and the partial
-// sums' traffic (join_tbs).  The times are a fit to 9364 timings of every form on 13 weights, plain
+// sums' traffic (join_tbs).  The times are a fit to 11637 timings of every form on 13 weights, plain
 // and gated, 1 to 4096 tokens (the best split of each in profiles/int8_plan_timings.csv): the
-// choice is 2.0% above the best on the mean, 7% at the ninth tenth; for experts (70 drawn shapes,
+// choice is 2.1% above the best on the mean, 7% at the ninth tenth; for experts (70 drawn shapes,
 // cold_tbs and the added terms are theirs) 4.3% on the mean.  For instance, 5120 x 5120, us: 64 tokens
 // 128 x 16 12.3, 64 x 16 13.1, 256 x 128 18.6; 333 tokens 128 x 64 17.7, 256 x 128 27.6, 256 x 256 33.7;
 // 2048 tokens 256 x 128 65.0, 256 x 192 51.6, 256 x 256 60.2.
@@ -33,17 +33,19 @@ struct Int8Cost {
   float wait_us, block_us, token_us, tile_us, launch_us, tbs, cold_tbs, again, join_us, join_tbs;
 };
 constexpr Int8Cost kInt8Costs[kInt8Forms] = {
-    {16, 16, 0.029f, 0.011f, 0.0040f, 0.60f, 5.6f, 7.8f, 5.0f, 0.00f, 0.f, 1.f},
-    {16, 16, 0.026f, 0.010f, 0.0040f, 0.46f, 5.7f, 7.8f, 5.0f, 0.00f, 0.f, 1.f},
-    {16, 32, 0.010f, 0.031f, 0.0030f, 0.38f, 5.9f, 6.8f, 5.6f, 0.00f, 0.f, 1.f},
-    {64, 16, 0.058f, 0.097f, 0.f, 0.12f, 6.0f, 7.1f, 4.8f, 0.04f, 1.9f, 1.8f},
-    {128, 16, 0.010f, 0.164f, 0.f, 0.48f, 5.2f, 7.0f, 4.9f, 0.11f, 2.3f, 2.7f},
-    {128, 32, 0.010f, 0.188f, 0.f, 0.65f, 5.4f, 7.0f, 5.3f, 0.17f, 2.3f, 2.9f},
-    {128, 64, 0.010f, 0.226f, 0.f, 0.79f, 5.8f, 7.0f, 5.4f, 0.32f, 2.2f, 3.0f},
-    {256, 64, 0.289f, 0.403f, 0.f, 1.74f, 5.2f, 6.6f, 5.7f, 0.26f, 2.3f, 3.5f},
-    {256, 128, 0.777f, 0.638f, 0.f, 2.64f, 6.8f, 6.1f, 5.6f, 0.50f, 1.5f, 3.8f},
-    {256, 192, 0.010f, 0.772f, 0.f, 5.23f, 5.2f, 7.2f, 5.3f, 0.93f, 1.5f, 3.8f},
-    {256, 256, 0.452f, 0.970f, 0.f, 6.94f, 5.4f, 6.1f, 5.3f, 1.00f, 0.5f, 3.8f}};
+    {16, 16, 0.030f, 0.012f, 0.0040f, 0.60f, 5.5f, 7.7f, 5.0f, 0.00f, 0.f, 1.f},
+    {16, 16, 0.027f, 0.010f, 0.0040f, 0.47f, 5.6f, 7.8f, 5.0f, 0.00f, 0.f, 1.f},
+    {16, 32, 0.010f, 0.027f, 0.0030f, 0.38f, 5.9f, 6.8f, 5.6f, 0.00f, 0.f, 1.f},
+    {64, 16, 0.062f, 0.096f, 0.f, 0.09f, 6.0f, 7.1f, 4.8f, 0.04f, 1.9f, 1.7f},
+    {128, 16, 0.010f, 0.162f, 0.f, 0.44f, 5.3f, 7.0f, 4.9f, 0.11f, 2.2f, 2.7f},
+    {128, 32, 0.010f, 0.186f, 0.f, 0.62f, 5.5f, 7.1f, 5.3f, 0.16f, 2.3f, 2.9f},
+    {128, 64, 0.010f, 0.227f, 0.f, 0.79f, 5.7f, 7.0f, 5.4f, 0.33f, 2.2f, 3.0f},
+    {256, 64, 0.311f, 0.398f, 0.f, 1.80f, 5.1f, 6.7f, 5.7f, 0.27f, 2.3f, 3.5f},
+    {256, 128, 0.781f, 0.626f, 0.f, 2.93f, 6.3f, 6.2f, 5.6f, 0.52f, 1.7f, 3.8f},
+    {128, 128, 0.010f, 0.321f, 0.f, 2.77f, 4.7f, 6.8f, 5.4f, 0.74f, 2.2f, 3.0f},
+    {256, 128, 0.010f, 0.616f, 0.f, 4.54f, 4.4f, 6.8f, 5.5f, 0.62f, 1.6f, 3.6f},
+    {256, 192, 0.371f, 0.766f, 0.f, 5.36f, 5.0f, 7.0f, 5.3f, 0.96f, 1.4f, 3.9f},
+    {256, 256, 0.516f, 0.954f, 0.f, 7.31f, 5.1f, 6.0f, 5.3f, 1.00f, 0.5f, 3.9f}};
 constexpr int kInt8Splits[] = {1, 2, 3, 4, 6, 8, 12};
 constexpr int kInt8Inline = 384;  // most blocks that are quantized in the kernel (48 KiB of LDS)
 
