@@ -189,6 +189,11 @@ __device__ __forceinline__ void write_rows(const Args& a, const i32x4_t (&acc)[R
 // take 2048 clocks a block, as many as the products, which keep the matrix units busy for 83% of
 // those 205 us (2.7 P op/s) and 71% of the experts'.  (Four waves of 128 x 128 would read a
 // third less, but have no registers for operands that are read ahead.)
+// The smaller tiles, 128 x 128 and 256 x 128, take over where the large ones are too few for the
+// units and the direct ones too many for the caches: 128 tokens of 18944 x 3584 18.3 us from 20.3,
+// 256 tokens of gated 11008 x 4096 32.2 from 35.9, 8 experts of 4096 x 14336 with 1024 rows 116
+// from 138.  They too are eight waves: two a SIMD, of which one multiplies while the other waits
+// (256 x 128 on four: 43 us instead of 32).
 template <int WN, int WT, int RN, int RT, int NW, int NX, int P, bool GROUPED>
 __global__ __launch_bounds__(64 * WN * WT, 1) void shared_kernel(Args a) {
   constexpr int kWaves = WN * WT, kRb = WN * RN, kTb = WT * RT, kTok = 16 * kTb;

@@ -24,10 +24,10 @@ constexpr int kInt8Forms = 13;
 // workgroup, launch_us is paid once, and split K (join_us) pays a second launch and the partial
 // sums' traffic (join_tbs).  The times are a fit to 11637 timings of every form on 13 weights, plain
 // and gated, 1 to 4096 tokens (the best split of each in profiles/int8_plan_timings.csv): the
-// choice is 2.1% above the best on the mean, 7% at the ninth tenth; for experts (70 drawn shapes,
-// cold_tbs and the added terms are theirs) 4.3% on the mean.  For instance, 5120 x 5120, us: 64 tokens
-// 128 x 16 12.3, 64 x 16 13.1, 256 x 128 18.6; 333 tokens 128 x 64 17.7, 256 x 128 27.6, 256 x 256 33.7;
-// 2048 tokens 256 x 128 65.0, 256 x 192 51.6, 256 x 256 60.2.
+// choice is 2.1% above the best on the mean, 7% at the ninth tenth; for experts (220 drawn shapes,
+// cold_tbs and the added terms are theirs) 3.9% on the mean.  For instance, 5120 x 5120, us: 64 tokens
+// direct 128 x 16 12.4, 64 x 16 13.2, 256 x 128 18.6; 333 tokens direct 128 x 64 17.7, shared 128 x 128
+// 21.5, 256 x 256 33.6; 2048 tokens direct 256 x 128 65.7, shared 256 x 192 53.6, 256 x 256 60.0.
 struct Int8Cost {
   int rows, tokens;
   float wait_us, block_us, token_us, tile_us, launch_us, tbs, cold_tbs, again, join_us, join_tbs;
@@ -94,15 +94,17 @@ inline Int8Plan plan_int8(int32_t t, int32_t p, int32_t experts, int32_t groups,
       const int per = (kb + s - 1) / s, chunks = (kb + per - 1) / per;
       if (chunks != s) continue;
       const float all = used * tiles_n * tiles_t * s / 256.f;
-      float rounds = std::max(1.f, experts ? all + 0.5f : std::ceil(all - 1e-3f));  // of experts only an estimate
-      if (f >= 9 && s == 1 && all > 1.f) {  // shared tiles cut those of a last part round
+      // of experts only an estimate: half a round more than the tiles fill, once they may fill one
+      float rounds = std::max(1.f, experts ? all + 0.5f * std::clamp(all - 0.5f, 0.f, 1.f) : std::ceil(all - 1e-3f));
+      if (f >= 9 && s == 1 && !experts && all > 1.f) {  // shared tiles cut those of a last part round
         const float part = all - std::floor(all);
-        rounds = experts ? all + 0.3f : std::floor(all) + (part < 1e-3f ? 0.f : part <= 0.25f ? 0.75f : part <= 0.5f ? 0.87f : 1.f);
+        rounds = std::floor(all) + (part < 1e-3f ? 0.f : part <= 0.25f ? 0.75f : part <= 0.5f ? 0.87f : 1.f);
       }
       const float wait = per * c.wait_us, work = rounds * per * (c.block_us + c.token_us * std::min(rows, float(c.tokens)));
       const float w2 = wait * wait, k2 = work * work, b2 = bytes * bytes;
       // starting and ending the workgroups; streaming ones of experts, which look for theirs first, run two at once
-      const float starts = experts && stream ? std::max(0.f, all - (f == 1 ? 1.f : 2.f)) * (c.tile_us + 1.6f) : rounds * (c.tile_us + (experts ? 0.3f : 0.f));
+      const float starts = experts && stream ? 1.5f + std::max(0.f, all - (f == 1 ? 1.f : 2.f)) * (c.tile_us + 1.6f)
+                                             : rounds * (c.tile_us + (experts ? 0.3f : 0.f));
       const float join = s == 1 ? 0.f : c.join_us + float(t) * groups * parts * 64.f * s / (c.join_tbs * 1e6f);
       const float us = before + c.launch_us + std::sqrt(std::sqrt(w2 * w2 + k2 * k2 + b2 * b2)) + starts + join;
       if (us < best_us) {
