@@ -278,3 +278,60 @@ def test_on_another_stream(api):
         got = b(x, logits, residual)[0]
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def test_two_streams_at_once(api):
+    rng = np.random.default_rng(3)
+    b = Block(api, rng, 9, 300, 200, 3)
+    args = [(torch.randn(t, 300, device=DEV, dtype=torch.bfloat16), torch.randn(t, 9, device=DEV), torch.randn(t, 300, device=DEV))
+            for t in (700, 33)]
+    want = [b(*a)[0] for a in args]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for _ in range(10):
+        for s, a in zip(streams, args):
+            with torch.cuda.stream(s):
+                got.append(b(*a)[0])
+    torch.cuda.synchronize()
+    for i, y in enumerate(got):
+        assert torch.equal(y, want[i % 2])
+
+
+def test_two_graphs_share_a_workspace(api):
+    """Replayed one after the other: nothing that a call leaves in its workspace is read by the next."""
+    rng = np.random.default_rng(4)
+    w, _ = make_w(rng, 5, 190, 330)
+    p = api.expert_pack(w)
+    wide, _ = make_w(rng, 1, 70, 16000)
+    q = api.int8_pack(wide[0])
+    x, logits = torch.randn(90, 330, device=DEV, dtype=torch.bfloat16), torch.randn(90, 5, device=DEV)
+    z = torch.randn(100, 16000, device=DEV)
+    need = max(api.int8_workspace(p, 90, rows=180), api.int8_workspace(q, 100, torch.float32), api.expert_route_workspace(90, 5))
+    workspace = torch.empty(need, dtype=torch.uint8, device=DEV)
+    a, b = torch.empty(180, 190, device=DEV), torch.empty(100, 70, device=DEV)
+
+    def first():
+        r = api.expert_route(logits, 2, workspace=workspace)
+        return api.expert_linear(p, x, r.offsets, r.perm, y=a, workspace=workspace)
+
+    def second():
+        return api.int8_linear(q, z, y=b, workspace=workspace)
+
+    first(), second()
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    for g, f in zip(graphs, (first, second)):
+        with torch.cuda.graph(g):
+            f()
+    for i in range(3):
+        x.normal_()
+        logits.normal_()
+        z.normal_()
+        r = api.expert_route(logits, 2)
+        want = api.expert_linear(p, x, r.offsets, r.perm, out_dtype=torch.float32), api.int8_linear(q, z)
+        a.zero_()
+        b.zero_()
+        for k in (0, 1, 0) if i % 2 else (1, 0, 1):
+            graphs[k].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, want[0]) and torch.equal(b, want[1])
