@@ -688,9 +688,10 @@ mbq_status mbq_int8_workspace(const mbq_int8_desc* desc, int32_t t, int32_t p, i
  * outside 0 .. t - 1 makes a row of zeros (gated: act(0) * 0); offsets that descend leave
  * rows unwritten or written twice.  Codes with k % 16 == 0 are read in place and need
  * ldx % 16 == 0 and 16-byte alignment; for other k they are copied to the workspace.
- * Sums are exact; a sum is rounded to float32 once and multiplied by the product of the
- * scales, a gate is float32, and y is rounded once.  A row that holds a NaN or infinity
- * yields NaN for itself only.  Calls that overlap in time must not share a workspace.
+ * Sums are exact; a sum is rounded to float32 once and multiplied by the token's and then the
+ * output's scale, with no exponent lost between them; a gate is float32, and y is rounded once.
+ * A row that holds a NaN or infinity yields NaN for itself only.  Calls that overlap in time must
+ * not share a workspace.
  */
 mbq_status mbq_int8_linear(const mbq_int8_desc* desc, const void* packed, const mbq_int8_args* args, hipStream_t stream);
 

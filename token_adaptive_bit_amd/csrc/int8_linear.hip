@@ -90,14 +90,29 @@ __device__ __forceinline__ void to_lds_from(const uint8_t* p, const void* l) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"{m0}"(at), "v"(p) : "memory");
 }
 
+// A sum times its token's and then its output's scale: the first product is at most 2^31 times
+// the token's scale, and with that in 2^-126 .. 2^97 it is 0 or a normal number, so that nothing
+// is lost before the last product, whatever the output's scale.  For other tokens (FAR) the
+// mantissas are multiplied, and the exponents come last.  Where both forms serve they give
+// the same bits.
+template <bool FAR>
+__device__ __forceinline__ float scaled(int32_t sum, float xs, float ws) {
+  if constexpr (!FAR) return float(sum) * xs * ws;
+  return __builtin_ldexpf(float(sum) * __builtin_amdgcn_frexp_mantf(xs) * __builtin_amdgcn_frexp_mantf(ws),
+                          __builtin_amdgcn_frexp_expf(xs) + __builtin_amdgcn_frexp_expf(ws));
+}
+__device__ __forceinline__ bool far_scale(float xs) {
+  return (__float_as_uint(xs) & 0x7FFFFFFFu) - 0x00800000u >= 0x70000000u - 0x00800000u;
+}
+
 // Four outputs of a token from their sums (gated: from both products').
-template <int P>
+template <int P, bool FAR>
 __device__ __forceinline__ void outputs(const Args& a, const i32x4_t (&sum)[P], float xs, const f32x4_t (&ws)[P], float (&v)[4]) {
   float u[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    v[e] = float(sum[0][e]) * (xs * ws[0][e]);
-    u[e] = float(sum[P - 1][e]) * (xs * ws[P - 1][e]);
+    v[e] = scaled<FAR>(sum[0][e], xs, ws[0][e]);
+    u[e] = scaled<FAR>(sum[P - 1][e], xs, ws[P - 1][e]);
   }
   if constexpr (P == 2) {
     if (a.gelu) {
@@ -114,7 +129,7 @@ template <int P>
 __device__ __forceinline__ void finish(const Args& a, int64_t row, int rb, int c, const i32x4_t (&sum)[P], float xs,
                                        const f32x4_t (&ws)[P]) {
   float v[4];
-  outputs<P>(a, sum, xs, ws, v);
+  outputs<P, true>(a, sum, xs, ws, v);  // of four outputs the other form would save less than its choice costs
   if (a.y_bf16) store4<true>(a.y, row, a.n, rb / P * kRowBlock + 4 * c, v);
   else store4<false>(a.y, row, a.n, rb / P * kRowBlock + 4 * c, v);
 }
@@ -122,14 +137,11 @@ __device__ __forceinline__ void finish(const Args& a, int64_t row, int rb, int c
 // A wave's 16 RN / P outputs of 16 RT tokens to y, 16 tokens at a time: from the instruction's
 // layout, where a lane holds four outputs of one token, through the wave's own LDS to whole
 // rows.  (Stored as they lie, in pieces of 8 bytes, a tile of 256 x 256 took 10 us more.)
-template <int RN, int RT, int P, bool YBF>
-__device__ __forceinline__ void write_rows(const Args& a, const i32x4_t (&acc)[RN][RT], const float (&xs)[RT], const float* ws,
-                                           int rb, int64_t first, int count, uint8_t* lds) {
+template <int RN, int RT, int P, bool YBF, bool FAR>
+__device__ __forceinline__ void write_rows(const Args& a, const i32x4_t (&acc)[RN][RT], const float (&xs)[RT],
+                                           const f32x4_t (&w)[RN], int rb, int64_t first, int count, uint8_t* lds) {
   constexpr int kBytes = YBF ? 2 : 4, kRow = RN / P * kRowBlock * kBytes, kPieces = kRow / 16, kStride = kRow + 16;
   const int lane = threadIdx.x & 63, r = lane & 15, c = lane >> 4;
-  f32x4_t w[RN];
-#pragma unroll
-  for (int i = 0; i < RN; ++i) w[i] = *reinterpret_cast<const f32x4_t*>(ws + min(rb + i, a.rbs - 1) * kRowBlock + 4 * c);
 #pragma unroll
   for (int j = 0; j < RT; ++j) {
     if (j * 16 >= count) break;
@@ -143,7 +155,7 @@ __device__ __forceinline__ void write_rows(const Args& a, const i32x4_t (&acc)[R
         scale[e] = w[i + e];
       }
       float v[4];
-      outputs<P>(a, sum, xs[j], scale, v);
+      outputs<P, FAR>(a, sum, xs[j], scale, v);
       uint8_t* at = lds + r * kStride + (i / P * kRowBlock + 4 * c) * kBytes;
       if constexpr (YBF) {
         *reinterpret_cast<uint64_t*>(at) = uint64_t(bf16_pair(v[2], v[3])) << 32 | bf16_pair(v[0], v[1]);
@@ -175,6 +187,25 @@ __device__ __forceinline__ void write_rows(const Args& a, const i32x4_t (&acc)[R
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  }
+}
+
+template <int RN, int RT, int P>
+__device__ __forceinline__ void write_tile(const Args& a, const i32x4_t (&acc)[RN][RT], const float (&xs)[RT], const float* ws,
+                                           int rb, int64_t first, int count, uint8_t* lds) {
+  const int c = (threadIdx.x & 63) >> 4;
+  f32x4_t w[RN];  // asked for before the tokens' scales are looked at
+#pragma unroll
+  for (int i = 0; i < RN; ++i) w[i] = *reinterpret_cast<const f32x4_t*>(ws + min(rb + i, a.rbs - 1) * kRowBlock + 4 * c);
+  bool far = false;
+#pragma unroll
+  for (int j = 0; j < RT; ++j) far |= far_scale(xs[j]);
+  if (__builtin_expect(__ballot(far) != 0, 0)) {  // the wave's tokens together
+    if (a.y_bf16) write_rows<RN, RT, P, true, true>(a, acc, xs, w, rb, first, count, lds);
+    else write_rows<RN, RT, P, false, true>(a, acc, xs, w, rb, first, count, lds);
+  } else {
+    if (a.y_bf16) write_rows<RN, RT, P, true, false>(a, acc, xs, w, rb, first, count, lds);
+    else write_rows<RN, RT, P, false, false>(a, acc, xs, w, rb, first, count, lds);
   }
 }
 
@@ -387,8 +418,7 @@ __global__ __launch_bounds__(64 * WN * WT, 1) void shared_kernel(Args a) {
   uint8_t* own = lds + wave * kOutBytes;
   const int64_t first = tile.first + wt * RT * 16;
   const int count = tile.count - wt * RT * 16;
-  if (a.y_bf16) write_rows<RN, RT, P, true>(a, acc, xs, ws, rbw, first, count, own);
-  else write_rows<RN, RT, P, false>(a, acc, xs, ws, rbw, first, count, own);
+  write_tile<RN, RT, P>(a, acc, xs, ws, rbw, first, count, own);
 }
 
 // Fewer tokens, and ragged groups: tiles of 16 RN WN packed rows x 16 RT tokens on WN waves, which
@@ -535,8 +565,7 @@ __global__ __launch_bounds__(64 * WN, 2) void direct_kernel(Args a) {
   }
   __syncthreads();  // every wave has read its last operands, and no copy is on its way
   uint8_t* own = lds + wave * kOutBytes;
-  if (a.y_bf16) write_rows<RN, RT, P, true>(a, acc, xs, ws, rbw, tile.first, tile.count, own);
-  else write_rows<RN, RT, P, false>(a, acc, xs, ws, rbw, tile.first, tile.count, own);
+  write_tile<RN, RT, P>(a, acc, xs, ws, rbw, tile.first, tile.count, own);
 }
 
 // Joins the chunks of a split K: four outputs of one token a thread.
