@@ -631,7 +631,7 @@ mbq_status mbq_int8_describe(int32_t n, int32_t k, int32_t gated, int32_t expert
   d.k_blocks = (k + mbq::kFp8Block - 1) / mbq::kFp8Block;
   d.expert_stride = uint64_t(d.row_blocks) * d.k_blocks * mbq::kFp8TileBytes;
   d.scales_offset = d.expert_stride * experts;
-  if (d.scales_offset >= (uint64_t(1) << 36)) return MBQ_ERR_SHAPE;  // 64 GiB: grids stay in range
+  if (d.scales_offset >= (uint64_t(1) << 36)) return MBQ_ERR_SHAPE;  // 64 GiB: fewer than 2^25 groups of 16 rows
   d.total_bytes = d.scales_offset + align256(uint64_t(experts) * d.row_blocks * mbq::kRowBlock * 4);
   *out = d;
   return MBQ_OK;

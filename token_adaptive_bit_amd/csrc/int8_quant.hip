@@ -68,60 +68,63 @@ __global__ __launch_bounds__(WR < 4 ? 256 : 64 * WR) void quantize_rows_kernel(i
   if (at == 0) scale[row] = int8_scale(m);
 }
 
-// 16 rows of one weight of one expert per workgroup: 16 lanes a row, 128 inputs at a step,
-// first for the row's maximum and then for its codes (the second read comes from the caches).
+// 16 rows of one weight of one expert per workgroup and step: 16 lanes a row, 128 inputs at a
+// time, first for the row's maximum and then for its codes (the second read comes from the caches).
 // Bound by traffic (codes of 128 experts of 1536 x 4096 345 us, 4.7 TB/s).
 template <int WT>  // 0 float32, 1 bfloat16, 2 codes with scales given
 __global__ __launch_bounds__(256) void pack_int8_kernel(mbq_int8_desc d, int32_t part, const void* __restrict__ w,
                                                         const float* __restrict__ w_scale, uint8_t* __restrict__ packed,
                                                         int32_t* __restrict__ status) {
   const int blocks = (d.n + kRowBlock - 1) / kRowBlock;
-  const int64_t expert = blockIdx.x / blocks;
-  const int block = int(blockIdx.x - expert * blocks), r = threadIdx.x >> 4, l = threadIdx.x & 15;
-  const int64_t row = int64_t(block) * kRowBlock + r;
-  const bool there = row < d.n;
-  const int end = there ? d.k : 0;
-  const uint8_t* src = static_cast<const uint8_t*>(w) + (expert * d.n + (there ? row : 0)) * d.k * (WT == 0 ? 4 : WT == 1 ? 2 : 1);
-  float f = 0.f, s = 0.f;
-  bool bad = false;
-  if constexpr (WT == 2) {
-    if (there) s = w_scale[expert * d.n + row];
-    bad = (__float_as_uint(s) & 0x7F800000u) == 0x7F800000u;
-  } else {
-    uint32_t m = 0;
-    for (int i = l * 8; i < end; i += 128) {
-      float v[8];
-      load8<WT == 1>(src, i, end, v);
-      m = max(m, amax8(v));
-    }
-    m = max16(m);
-    f = int8_factor(m);
-    if (there) s = int8_scale(m);
-    bad = m >= 0x7F800000u;
-  }
-  const int64_t rb = int64_t(block) * (d.gated + 1) + part;
-  uint8_t* tiles = packed + expert * d.expert_stride + rb * d.k_blocks * kFp8TileBytes;
-  for (int kb = 0; kb < d.k_blocks; ++kb) {
-    const int i = kb * kFp8Block + l * 8;  // inputs i .. i + 7: half l / 8, lane group l / 2 % 4, its first or last 8 bytes
-    uint8_t* out = tiles + int64_t(kb) * kFp8TileBytes + 1024 * (l >> 3) + 256 * (l >> 1 & 3) + 16 * r + 8 * (l & 1);
+  const int r = threadIdx.x >> 4, l = threadIdx.x & 15;
+  for (int64_t b = blockIdx.x; b < int64_t(d.experts) * blocks; b += gridDim.x) {
+    const int64_t expert = b / blocks;
+    const int block = int(b - expert * blocks);
+    const int64_t row = int64_t(block) * kRowBlock + r;
+    const bool there = row < d.n;
+    const int end = there ? d.k : 0;
+    const uint8_t* src = static_cast<const uint8_t*>(w) + (expert * d.n + (there ? row : 0)) * d.k * (WT == 0 ? 4 : WT == 1 ? 2 : 1);
+    float f = 0.f, s = 0.f;
+    bool bad = false;
     if constexpr (WT == 2) {
-      u32x2_a1 c = {0, 0};
-      if (i + 8 <= end) {
-        c = *reinterpret_cast<const u32x2_a1*>(src + i);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (i + e < end) c[e / 4] |= uint32_t(src[i + e]) << (8 * (e & 3));
-      }
-      *reinterpret_cast<u32x2_a1*>(out) = c;
+      if (there) s = w_scale[expert * d.n + row];
+      bad = (__float_as_uint(s) & 0x7F800000u) == 0x7F800000u;
     } else {
-      float v[8];
-      load8<WT == 1>(src, i, end, v);
-      store_int8x8(out, 0, 8, v, f);
+      uint32_t m = 0;
+      for (int i = l * 8; i < end; i += 128) {
+        float v[8];
+        load8<WT == 1>(src, i, end, v);
+        m = max(m, amax8(v));
+      }
+      m = max16(m);
+      f = int8_factor(m);
+      if (there) s = int8_scale(m);
+      bad = m >= 0x7F800000u;
     }
+    const int64_t rb = int64_t(block) * (d.gated + 1) + part;
+    uint8_t* tiles = packed + expert * d.expert_stride + rb * d.k_blocks * kFp8TileBytes;
+    for (int kb = 0; kb < d.k_blocks; ++kb) {
+      const int i = kb * kFp8Block + l * 8;  // inputs i .. i + 7: half l / 8, lane group l / 2 % 4, its first or last 8 bytes
+      uint8_t* out = tiles + int64_t(kb) * kFp8TileBytes + 1024 * (l >> 3) + 256 * (l >> 1 & 3) + 16 * r + 8 * (l & 1);
+      if constexpr (WT == 2) {
+        u32x2_a1 c = {0, 0};
+        if (i + 8 <= end) {
+          c = *reinterpret_cast<const u32x2_a1*>(src + i);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            if (i + e < end) c[e / 4] |= uint32_t(src[i + e]) << (8 * (e & 3));
+        }
+        *reinterpret_cast<u32x2_a1*>(out) = c;
+      } else {
+        float v[8];
+        load8<WT == 1>(src, i, end, v);
+        store_int8x8(out, 0, 8, v, f);
+      }
+    }
+    if (l == 0) reinterpret_cast<float*>(packed + d.scales_offset)[(expert * d.row_blocks + rb) * kRowBlock + r] = s;
+    if (bad && status) atomicOr(status, 1);
   }
-  if (l == 0) reinterpret_cast<float*>(packed + d.scales_offset)[(expert * d.row_blocks + rb) * kRowBlock + r] = s;
-  if (bad && status) atomicOr(status, 1);
 }
 
 }  // namespace
@@ -145,7 +148,8 @@ hipError_t launch_int8_quantize(int32_t t, int32_t k, const void* x, bool x_bf16
 
 hipError_t launch_int8_pack(const mbq_int8_desc& d, int32_t part, const void* w, mbq_dtype w_dtype, const float* w_scale,
                             void* packed, int32_t* dev_status, hipStream_t stream) {
-  const dim3 grid(uint32_t(d.experts) * uint32_t((d.n + kRowBlock - 1) / kRowBlock));
+  // a launch holds fewer than 2^32 threads (more are cut without an error); there may be 2^25 groups of rows
+  const dim3 grid(std::min(uint32_t(d.experts) * uint32_t((d.n + kRowBlock - 1) / kRowBlock), 1u << 22));
   uint8_t* out = static_cast<uint8_t*>(packed);
   if (w_dtype == MBQ_F32) pack_int8_kernel<0><<<grid, 256, 0, stream>>>(d, part, w, w_scale, out, dev_status);
   else if (w_dtype == MBQ_BF16) pack_int8_kernel<1><<<grid, 256, 0, stream>>>(d, part, w, w_scale, out, dev_status);
