@@ -703,7 +703,8 @@ mbq_status mbq_int8_linear(const mbq_int8_desc* desc, const void* packed, const 
   if (a->ldx < desc->k || (direct && a->ldx % 16 != 0)) return MBQ_ERR_SHAPE;
   const size_t need = mbq::int8_workspace(*desc, a->t, a->p, a->offsets != nullptr, mbq_dtype(a->x_dtype));
   if (need && (!a->workspace || a->ws_bytes < need || !aligned(a->workspace, 256))) return MBQ_ERR_WORKSPACE;
-  return launched(mbq::launch_int8_linear(*desc, packed, *a, stream));
+  const hipError_t e = mbq::launch_int8_linear(*desc, packed, *a, stream);
+  return e == hipErrorInvalidConfiguration ? MBQ_ERR_SHAPE : launched(e);  // more tiles than a launch holds
 }
 
 mbq_status mbq_expert_route_workspace(int32_t t, int32_t experts, size_t* bytes) {

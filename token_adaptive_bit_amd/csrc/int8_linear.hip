@@ -12,8 +12,8 @@
 namespace mbq {
 namespace {
 
-constexpr int kUnits = 256;            // compute units
-constexpr int kCutRoom = 2 * kUnits;  // workgroups that the cut tiles of a last round may take
+constexpr int kUnits = 256;  // compute units
+constexpr int kCutRoom = kInt8CutRoom;
 
 struct Args {
   const uint8_t* codes;  // packed tiles
@@ -773,25 +773,27 @@ __global__ __launch_bounds__(64 * W) void stream_kernel(Args a) {
   if (in < tile.count) finish<P>(a, tile.first + in, rb0, c, sum, scale, wscale);
 }
 
-template <int WN, int WT, int RN, int RT, int NW, int NX, int P, bool GROUPED>
-void launch_shared(const Args& a, hipStream_t stream) {
-  const int64_t tiles_n = (a.rbs + WN * RN - 1) / (WN * RN), tok = 16 * WT * RT;
-  const int64_t tiles_t = GROUPED ? a.p / tok + std::min(a.experts, a.p) : (a.p + tok - 1) / tok;
-  // and room for the cut tiles of a last round
-  shared_kernel<WN, WT, RN, RT, NW, NX, P, GROUPED><<<uint32_t(tiles_n * tiles_t * a.chunks + kCutRoom), 64 * WN * WT, 0, stream>>>(a);
+// The plan counts a form's tiles and threads by its table.
+template <Int8Form F>
+constexpr bool is_form(int rows, int tokens, int threads) {
+  return kInt8Costs[int(F)].rows == rows && kInt8Costs[int(F)].tokens == tokens && kInt8Threads[int(F)] == threads;
+}
+template <Int8Form F, int WN, int WT, int RN, int RT, int NW, int NX, int P, bool GROUPED>
+void launch_shared(const Args& a, dim3 grid, hipStream_t stream) {
+  static_assert(is_form<F>(16 * RN * WN, 16 * RT * WT, 64 * WN * WT));
+  shared_kernel<WN, WT, RN, RT, NW, NX, P, GROUPED><<<grid, 64 * WN * WT, 0, stream>>>(a);
 }
 
-template <int WN, int RN, int RT, int D, int NX, int P, bool GROUPED>
-void launch_direct(const Args& a, hipStream_t stream) {
-  const int64_t tiles_n = (a.rbs + WN * RN - 1) / (WN * RN), tok = 16 * RT;
-  const int64_t tiles_t = GROUPED ? a.p / tok + std::min(a.experts, a.p) : (a.p + tok - 1) / tok;
-  direct_kernel<WN, RN, RT, D, NX, P, GROUPED><<<uint32_t(tiles_n * tiles_t * a.chunks), 64 * WN, 0, stream>>>(a);
+template <Int8Form F, int WN, int RN, int RT, int D, int NX, int P, bool GROUPED>
+void launch_direct(const Args& a, dim3 grid, hipStream_t stream) {
+  static_assert(is_form<F>(16 * RN * WN, 16 * RT, 64 * WN));
+  direct_kernel<WN, RN, RT, D, NX, P, GROUPED><<<grid, 64 * WN, 0, stream>>>(a);
 }
 
-template <int W, int TT, int P, bool GROUPED>
-void launch_stream(const Args& a, mbq_dtype x_dtype, hipStream_t stream) {
-  const int tok = 16 * TT;
-  const dim3 grid(a.rbs / P, GROUPED ? a.p / tok + std::min(a.experts, a.p) : 1), block(64 * W);
+template <Int8Form F, int W, int TT, int P, bool GROUPED>
+void launch_stream(const Args& a, dim3 grid, mbq_dtype x_dtype, hipStream_t stream) {
+  static_assert(is_form<F>(16, 16 * TT, 64 * W));
+  const dim3 block(64 * W);
   if constexpr (TT == 1) {
     if (a.x) {
       const size_t lds = size_t(std::min(a.p, 16)) * (a.kb * kFp8Block + 16);
@@ -805,23 +807,24 @@ void launch_stream(const Args& a, mbq_dtype x_dtype, hipStream_t stream) {
 }
 
 template <int P, bool GROUPED>
-hipError_t launch(Args& a, const Int8Plan& p, mbq_dtype x_dtype, hipStream_t stream) {
+hipError_t launch(Args& a, const Int8Plan& p, dim3 grid, mbq_dtype x_dtype, hipStream_t stream) {
   a.chunks = p.chunks;
   a.chunk_kb = (a.kb + p.chunks - 1) / p.chunks;
+  using F = Int8Form;
   switch (p.form) {
-    case Int8Form::kStream8x1: launch_stream<8, 1, P, GROUPED>(a, x_dtype, stream); break;
-    case Int8Form::kStream16x1: launch_stream<16, 1, P, GROUPED>(a, x_dtype, stream); break;
-    case Int8Form::kStream8x2: launch_stream<8, 2, P, GROUPED>(a, x_dtype, stream); break;
-    case Int8Form::kDirect64x16: launch_direct<2, 2, 1, 6, 4, P, GROUPED>(a, stream); break;
-    case Int8Form::kDirect128x16: launch_direct<4, 2, 1, 4, 4, P, GROUPED>(a, stream); break;
-    case Int8Form::kDirect128x32: launch_direct<4, 2, 2, 4, 4, P, GROUPED>(a, stream); break;
-    case Int8Form::kDirect128x64: launch_direct<4, 2, 4, 3, 3, P, GROUPED>(a, stream); break;
-    case Int8Form::kDirect256x64: launch_direct<4, 4, 4, 2, 3, P, GROUPED>(a, stream); break;
-    case Int8Form::kDirect256x128: launch_direct<4, 4, 8, 2, 2, P, GROUPED>(a, stream); break;
-    case Int8Form::kShared128x128: launch_shared<2, 4, 4, 2, 3, 3, P, GROUPED>(a, stream); break;
-    case Int8Form::kShared256x128: launch_shared<4, 2, 4, 4, 3, 3, P, GROUPED>(a, stream); break;
-    case Int8Form::kShared256x192: launch_shared<2, 4, 8, 3, 3, 2, P, GROUPED>(a, stream); break;
-    case Int8Form::kShared256x256: launch_shared<2, 4, 8, 4, 3, 2, P, GROUPED>(a, stream); break;
+    case F::kStream8x1: launch_stream<F::kStream8x1, 8, 1, P, GROUPED>(a, grid, x_dtype, stream); break;
+    case F::kStream16x1: launch_stream<F::kStream16x1, 16, 1, P, GROUPED>(a, grid, x_dtype, stream); break;
+    case F::kStream8x2: launch_stream<F::kStream8x2, 8, 2, P, GROUPED>(a, grid, x_dtype, stream); break;
+    case F::kDirect64x16: launch_direct<F::kDirect64x16, 2, 2, 1, 6, 4, P, GROUPED>(a, grid, stream); break;
+    case F::kDirect128x16: launch_direct<F::kDirect128x16, 4, 2, 1, 4, 4, P, GROUPED>(a, grid, stream); break;
+    case F::kDirect128x32: launch_direct<F::kDirect128x32, 4, 2, 2, 4, 4, P, GROUPED>(a, grid, stream); break;
+    case F::kDirect128x64: launch_direct<F::kDirect128x64, 4, 2, 4, 3, 3, P, GROUPED>(a, grid, stream); break;
+    case F::kDirect256x64: launch_direct<F::kDirect256x64, 4, 4, 4, 2, 3, P, GROUPED>(a, grid, stream); break;
+    case F::kDirect256x128: launch_direct<F::kDirect256x128, 4, 4, 8, 2, 2, P, GROUPED>(a, grid, stream); break;
+    case F::kShared128x128: launch_shared<F::kShared128x128, 2, 4, 4, 2, 3, 3, P, GROUPED>(a, grid, stream); break;
+    case F::kShared256x128: launch_shared<F::kShared256x128, 4, 2, 4, 4, 3, 3, P, GROUPED>(a, grid, stream); break;
+    case F::kShared256x192: launch_shared<F::kShared256x192, 2, 4, 8, 3, 3, 2, P, GROUPED>(a, grid, stream); break;
+    case F::kShared256x256: launch_shared<F::kShared256x256, 2, 4, 8, 4, 3, 2, P, GROUPED>(a, grid, stream); break;
   }
   if (a.chunks > 1)
     join_kernel<P><<<uint32_t(std::min<int64_t>((int64_t(a.p) * (a.rbs / P) * 4 + 255) / 256, 4096)), 256, 0, stream>>>(a);
@@ -829,8 +832,8 @@ hipError_t launch(Args& a, const Int8Plan& p, mbq_dtype x_dtype, hipStream_t str
 }
 
 template <int P>
-hipError_t launch(Args& a, const Int8Plan& p, mbq_dtype x_dtype, hipStream_t stream) {
-  return a.offsets ? launch<P, true>(a, p, x_dtype, stream) : launch<P, false>(a, p, x_dtype, stream);
+hipError_t launch(Args& a, const Int8Plan& p, dim3 grid, mbq_dtype x_dtype, hipStream_t stream) {
+  return a.offsets ? launch<P, true>(a, p, grid, x_dtype, stream) : launch<P, false>(a, p, grid, x_dtype, stream);
 }
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
@@ -864,6 +867,9 @@ size_t int8_workspace(const mbq_int8_desc& d, int32_t t, int32_t p, bool grouped
 hipError_t launch_int8_linear(const mbq_int8_desc& d, const void* packed, const mbq_int8_args& g, hipStream_t stream) {
   const mbq_dtype x_dtype = mbq_dtype(g.x_dtype);
   const Int8Plan plan = plan_of(d, g.t, g.p, g.offsets != nullptr, x_dtype);
+  const Int8Grid n = grid_int8(plan, g.p, g.offsets ? d.experts : 0, d.row_blocks / (d.gated + 1), d.gated + 1);
+  if (!holds_int8(n)) return hipErrorInvalidConfiguration;
+  const dim3 grid(uint32_t(n.x), uint32_t(n.y));
   const Layout l = layout(d, g.t, g.p, plan, x_dtype);
   uint8_t* ws = static_cast<uint8_t*>(g.workspace);
   Args a{};
@@ -906,7 +912,7 @@ hipError_t launch_int8_linear(const mbq_int8_desc& d, const void* packed, const 
   if (e != hipSuccess) return e;
   a.gelu = d.gated && g.act == MBQ_ACT_GELU_TANH;
   a.y_bf16 = g.y_dtype == MBQ_BF16;
-  return d.gated ? launch<2>(a, plan, x_dtype, stream) : launch<1>(a, plan, x_dtype, stream);
+  return d.gated ? launch<2>(a, plan, grid, x_dtype, stream) : launch<1>(a, plan, grid, x_dtype, stream);
 }
 
 }  // namespace mbq

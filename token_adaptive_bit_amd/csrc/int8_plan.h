@@ -46,6 +46,8 @@ constexpr Int8Cost kInt8Costs[kInt8Forms] = {
     {256, 128, 0.010f, 0.616f, 0.f, 4.54f, 4.4f, 6.8f, 5.5f, 0.62f, 1.6f, 3.6f},
     {256, 192, 0.371f, 0.766f, 0.f, 5.36f, 5.0f, 7.0f, 5.3f, 0.96f, 1.4f, 3.9f},
     {256, 256, 0.516f, 0.954f, 0.f, 7.31f, 5.1f, 6.0f, 5.3f, 1.00f, 0.5f, 3.9f}};
+constexpr int kInt8Threads[kInt8Forms] = {512, 1024, 512, 128, 256, 256, 256, 256, 256, 512, 512, 512, 512};  // of a workgroup
+constexpr int kInt8CutRoom = 512;  // workgroups that the cut tiles of a shared form's last round may take
 constexpr int kInt8Splits[] = {1, 2, 3, 4, 6, 8, 12};
 constexpr int kInt8Inline = 384;  // most blocks that are quantized in the kernel (48 KiB of LDS)
 
@@ -117,5 +119,23 @@ inline Int8Plan plan_int8(int32_t t, int32_t p, int32_t experts, int32_t groups,
   }
   return best;
 }
+
+// The launch of a plan for p rows of y: workgroups along x and y, threads of each.
+struct Int8Grid {
+  int64_t x, y;
+  int threads;
+};
+inline Int8Grid grid_int8(const Int8Plan& plan, int32_t p, int32_t experts, int32_t groups, int32_t parts) {
+  const int f = int(plan.form);
+  const Int8Cost& c = kInt8Costs[f];
+  // no more tiles than that, however the rows are spread over the experts
+  const int64_t tiles_t = experts ? int64_t(p) / c.tokens + std::min(experts, p) : (int64_t(p) + c.tokens - 1) / c.tokens;
+  if (f < 3) return {groups, tiles_t, kInt8Threads[f]};
+  const int64_t tiles_n = (int64_t(groups) * parts * 16 + c.rows - 1) / c.rows;
+  return {tiles_n * tiles_t * plan.chunks + (f < 9 ? 0 : kInt8CutRoom), 1, kInt8Threads[f]};
+}
+// A launch takes the threads along a direction modulo 2^32, without an error, and up to 65535
+// workgroups along y.
+inline bool holds_int8(const Int8Grid& g) { return g.x * g.threads < (int64_t(1) << 32) && g.y < 65536; }
 
 }  // namespace mbq
