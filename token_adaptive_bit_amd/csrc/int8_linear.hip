@@ -802,8 +802,7 @@ void launch_stream(const Args& a, dim3 grid, mbq_dtype x_dtype, hipStream_t stre
       return;
     }
   }
-  // one weight's codes go to 16 waves
-  if constexpr (W != 8 || TT != 1 || GROUPED) stream_kernel<W, TT, MBQ_INT8, P, GROUPED><<<grid, block, 0, stream>>>(a);
+  if constexpr (serves_int8(F, GROUPED, false)) stream_kernel<W, TT, MBQ_INT8, P, GROUPED><<<grid, block, 0, stream>>>(a);
 }
 
 template <int P, bool GROUPED>
@@ -869,6 +868,7 @@ hipError_t launch_int8_linear(const mbq_int8_desc& d, const void* packed, const 
   const Int8Plan plan = plan_of(d, g.t, g.p, g.offsets != nullptr, x_dtype);
   const Int8Grid n = grid_int8(plan, g.p, g.offsets ? d.experts : 0, d.row_blocks / (d.gated + 1), d.gated + 1);
   if (!holds_int8(n)) return hipErrorInvalidConfiguration;
+  if (!serves_int8(plan.form, g.offsets ? d.experts : 0, plan.inline_x)) return hipErrorInvalidValue;
   const dim3 grid(uint32_t(n.x), uint32_t(n.y));
   const Layout l = layout(d, g.t, g.p, plan, x_dtype);
   uint8_t* ws = static_cast<uint8_t*>(g.workspace);

@@ -57,6 +57,12 @@ struct Int8Plan {
   bool inline_x;  // float activations are quantized in the streaming kernel
 };
 
+// Whether a form serves the call: on codes of one weight 8 waves take 1.037 times as long as 16
+// and are not built.
+constexpr bool serves_int8(Int8Form form, int32_t experts, bool inline_x) {
+  return form != Int8Form::kStream8x1 || experts || inline_x;
+}
+
 // t rows of x, p rows of y, experts (0: one weight, no groups), row groups of 16 outputs,
 // parts of a row group (2 gated), 128-input blocks.
 inline Int8Plan plan_int8(int32_t t, int32_t p, int32_t experts, int32_t groups, int32_t parts, int32_t kb, bool codes) {
@@ -87,7 +93,7 @@ inline Int8Plan plan_int8(int32_t t, int32_t p, int32_t experts, int32_t groups,
       within = us < quantize;
       before = std::min(us, quantize);
     }
-    if (f == 0 && !experts && !within) continue;  // on codes of one weight 8 waves take 1.037 times as long as 16
+    if (!serves_int8(Int8Form(f), experts, within)) continue;
     const float bytes = weight / ((weight > 2e8f ? c.cold_tbs : c.tbs) * 1e6f) + weight * c.again * (tiles_t - 1.f) / (c.tbs * 1e6f);
     if (before + c.launch_us + bytes >= best_us) continue;  // no split is faster than that
     float last = 1e30f;
