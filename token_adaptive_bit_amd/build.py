@@ -55,6 +55,9 @@ SPILL_FREE = ("decode_stream.hip", "prefill_mfma.hip", "route_mlp.hip", "lowrank
               "fp8_quant.hip", "fp8_linear.hip", "block_norm.hip", "token_logprobs.hip",
               "int8_quant.hip", "int8_linear.hip", "experts.hip")
 
+# Translation units whose assembly is read: waits that count the compiler's own loads.
+COUNTED_WAITS = ("int8_linear.hip",)
+
 COMMON = [
     "--offload-arch=gfx950", "-O3", "-fPIC", "-std=c++17",
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -95,6 +98,91 @@ def _spills(remarks: str) -> list:
 def _warnings(text: str) -> list:
     """The warnings of a compiler's output; the host pass's about the GPU feature switched off in COMMON is none."""
     return [line for line in text.splitlines() if "warning:" in line and "-packed-fp32-ops" not in line]
+
+
+_WAIT = re.compile(r"s_waitcnt vmcnt\((\d+)\) ; at most (\d+) copies of the youngest")
+_VMEM = re.compile(r"(global|buffer|flat|scratch)_(load|store|atomic)")
+_COPY = re.compile(r"(global|buffer)_load_lds|buffer_load\w* .*\blds\b")
+
+
+def _late_copies(assembly: str) -> list:
+    """What is wrong with the counted waits of an assembly: (kernel, line, N, copies allowed, copies found) where on some way to
+    a wait more of the N youngest vector memory operations are copies than it says; (kernel, 0, 0, 0, 0) for no wait at all."""
+    bad, name, waits = [], None, 0
+    ops, labels = [], {}                   # ops: (kind, what, line number); kind of "op", "copy", "wait", "end", "go", "maybe", "-"
+
+    def check():
+        back = [[] for _ in ops]           # where each operation can be reached from
+        for i, (kind, what, _) in enumerate(ops):
+            if i + 1 < len(ops) and kind not in ("end", "go"):
+                back[i + 1].append(i)
+            if kind in ("go", "maybe") and labels.get(what, len(ops)) < len(ops):
+                back[labels[what]].append(i)
+        for i, (kind, what, line) in enumerate(ops):
+            if kind != "wait":
+                continue
+            n, allowed = what
+            worst, seen, todo = 0, set(), [(j, n, 0) for j in back[i]]
+            while todo:
+                at, left, copies = state = todo.pop()
+                if state in seen or left == 0:
+                    continue
+                seen.add(state)
+                if ops[at][0] in ("op", "copy"):
+                    left, copies = left - 1, copies + (ops[at][0] == "copy")
+                    worst = max(worst, copies)
+                todo += [(j, left, copies) for j in back[at]]
+            if worst > allowed:
+                bad.append((name, line, n, allowed, worst))
+
+    for number, text in enumerate(assembly.splitlines(), 1):
+        word = text.strip()
+        if re.match(r"_Z\w+:", word):
+            name, ops, labels, waits = word.split(":")[0], [], {}, 0
+        elif name is None or not word:
+            continue
+        elif word.startswith(".Lfunc_end"):
+            check()
+            if "direct_kernel" in name and not waits:
+                bad.append((name, 0, 0, 0, 0))
+            name = None
+        elif re.match(r"\.L\w+:", word):
+            labels[word.split(":")[0]] = len(ops)
+            ops.append(("-", None, number))
+        elif _WAIT.search(word):
+            ops.append(("wait", tuple(map(int, _WAIT.search(word).groups())), number))
+            waits += 1
+        elif word.startswith((";", ".")):
+            continue
+        elif _COPY.match(word):
+            ops.append(("copy", None, number))
+        elif _VMEM.match(word):
+            ops.append(("op", None, number))
+        elif word.startswith("s_endpgm"):
+            ops.append(("end", None, number))
+        elif word.startswith("s_branch"):
+            ops.append(("go", word.split()[1], number))
+        elif word.startswith("s_cbranch"):
+            ops.append(("maybe", word.split()[1], number))
+        elif word.startswith(("s_setpc", "s_swappc", "s_call")):
+            bad.append((name, number, 0, 0, 0))
+    return bad
+
+
+def _assembly(src: str, extra: list) -> str:
+    """The GPU assembly of a translation unit."""
+    out = os.path.join(BUILD_DIR, src.replace(".hip", ".s"))
+    _run([hipcc(), *COMMON, *extra, "--cuda-device-only", "-S", os.path.join(CSRC, src), "-o", out], f"compiling {src} to assembly", False)
+    with open(out) as f:
+        return f.read()
+
+
+def _check_waits(src: str, extra: list) -> None:
+    bad = _late_copies(_assembly(src, extra))
+    if bad:
+        lines = "\n".join(f"  {k}, line {line}: of the {n} youngest operations {found} may be copies, {allowed} are allowed"
+                          for k, line, n, allowed, found in bad)
+        raise RuntimeError(f"{src}: waits that may pass before a copy is in:\n{lines}")
 
 
 def _compile(src: str, extra: list, verbose: bool) -> str:
@@ -169,7 +257,10 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
     lacks = _binding_lacks()
     with cf.ThreadPoolExecutor(jobs) as ex:
         bind = None if lacks else ex.submit(_compile_bind, verbose)
+        waits = [ex.submit(_check_waits, src, SOURCES[src]) for src in COUNTED_WAITS]
         objs = list(ex.map(lambda kv: _compile(kv[0], kv[1], verbose), SOURCES.items()))
+        for w in waits:
+            w.result()
         tmp = OUT + ".tmp"
         _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs], "link", verbose)
         os.replace(tmp, OUT)

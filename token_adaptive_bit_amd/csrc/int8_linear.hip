@@ -105,6 +105,15 @@ __device__ __forceinline__ bool far_scale(float xs) {
   return (__float_as_uint(xs) & 0x7FFFFFFFu) - 0x00800000u >= 0x70000000u - 0x00800000u;
 }
 
+// As to_lds_wait, where among the N operations that may be on their way COPIES are copies and the
+// others loads of the compiler's.  Were one of those moved or taken out, a copy too many could be:
+// the build looks in the assembly that of the N youngest vector memory operations at this wait, on
+// every way to it, no more are copies (build.py).
+template <int N, int COPIES>
+__device__ __forceinline__ void counted_wait() {
+  asm volatile("s_waitcnt vmcnt(%0) ; at most %1 copies of the youngest %0" ::"n"(N), "n"(COPIES) : "memory");
+}
+
 // Four outputs of a token from their sums (gated: from both products').
 template <int P, bool FAR>
 __device__ __forceinline__ void outputs(const Args& a, const i32x4_t (&sum)[P], float xs, const f32x4_t (&ws)[P], float (&v)[4]) {
@@ -500,7 +509,7 @@ __global__ __launch_bounds__(64 * WN, 2) void direct_kernel(Args a) {
     load_w(kb0 + i, i, 0);
     load_w(kb0 + i, i, 1);
   }
-  to_lds_wait<(NX - 1) * kCopiesX + D * 2 * RN>();
+  counted_wait<(NX - 1) * kCopiesX + D * 2 * RN, (NX - 1) * kCopiesX>();
   __syncthreads();
 #pragma unroll
   for (int j = 0; j < RT; ++j) read_x(0, 0, j);
@@ -523,7 +532,7 @@ __global__ __launch_bounds__(64 * WN, 2) void direct_kernel(Args a) {
       if constexpr (kPinned) __builtin_amdgcn_sched_barrier(0);
     }
     if constexpr (kAhead) load_w(kb + D, s, 0);
-    to_lds_wait<(NX - 2) * kCopiesX + (kAhead ? ((NX - 2) * 2 + 2) * RN : 0)>();
+    counted_wait<(NX - 2) * kCopiesX + (kAhead ? ((NX - 2) * 2 + 2) * RN : 0), (NX - 2) * kCopiesX>();
     __syncthreads();
     copy_x(kb + NX, buf);
 #pragma unroll
