@@ -202,6 +202,8 @@ def _compile(src: str, extra: list, verbose: bool) -> str:
         if bad:
             lines = "\n".join(f"  {n}: {v} VGPR / {s} SGPR spills, {b} B scratch" for n, v, s, b in bad)
             raise RuntimeError(f"{src}: kernels spill registers:\n{lines}")
+    if src in COUNTED_WAITS:
+        _check_waits(src, extra)
     return obj
 
 
@@ -257,10 +259,7 @@ def build(verbose: bool = False, jobs: int | None = None) -> str:
     lacks = _binding_lacks()
     with cf.ThreadPoolExecutor(jobs) as ex:
         bind = None if lacks else ex.submit(_compile_bind, verbose)
-        waits = [ex.submit(_check_waits, src, SOURCES[src]) for src in COUNTED_WAITS]
         objs = list(ex.map(lambda kv: _compile(kv[0], kv[1], verbose), SOURCES.items()))
-        for w in waits:
-            w.result()
         tmp = OUT + ".tmp"
         _run([hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs], "link", verbose)
         os.replace(tmp, OUT)
