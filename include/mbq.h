@@ -689,9 +689,10 @@ mbq_status mbq_int8_workspace(const mbq_int8_desc* desc, int32_t t, int32_t p, i
  * rows unwritten or written twice.  Codes with k % 16 == 0 are read in place and need
  * ldx % 16 == 0 and 16-byte alignment; for other k they are copied to the workspace.
  * Sums are exact; a sum is rounded to float32 once and multiplied by the token's and then the
- * output's scale, with no exponent lost between them; a gate is float32, and y is rounded once.
- * A row that holds a NaN or infinity yields NaN for itself only.  Calls that overlap in time must
- * not share a workspace.  Outputs that no launch holds (beyond 2^37 of them) are MBQ_ERR_SHAPE.
+ * output's scale, with no exponent lost between them; a gate is float32 (silu(g) within
+ * (|g| + 4) 2^-22 of itself), and y is rounded once.  A row that holds a NaN or infinity yields
+ * NaN for itself only.  Calls that overlap in time must not share a workspace.  Outputs that no
+ * launch holds (beyond 2^37 of them) are MBQ_ERR_SHAPE.
  */
 mbq_status mbq_int8_linear(const mbq_int8_desc* desc, const void* packed, const mbq_int8_args* args, hipStream_t stream);
 

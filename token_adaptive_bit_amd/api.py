@@ -1042,7 +1042,8 @@ def expert_gated(p: Int8Linear, x: torch.Tensor, offsets: torch.Tensor, rows: to
 class ExpertRoute(NamedTuple):
     """Per token its experts (-1: none) and their weights [t, top], the token of every grouped row
     [t * top] (-1: no copy), the first grouped row of every expert [experts + 1], and the grouped
-    row of every copy [t, top] (-1: none)."""
+    row of every copy [t, top] (-1: none).  All but the weights may lie in one allocation: clone
+    the one that is to be kept or saved without the others."""
     ids: torch.Tensor
     weights: torch.Tensor
     perm: torch.Tensor

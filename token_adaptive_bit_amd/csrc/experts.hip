@@ -196,7 +196,6 @@ __global__ __launch_bounds__(64) void span_scan_kernel(RouteArgs a, int spans) {
   a.span[int64_t(spans) * a.e + e] = before;
 }
 
-// (4096 tokens of 128, 8 chosen: 4.0 us, of which a launch and the histograms' way are most.)
 // The places of 64 tokens' copies: behind the copies of the tokens before them that took the
 // expert, base[e], and of those among the 64, the bits below the token's in mask[e].
 constexpr int kHeld = kPlaced * MBQ_MAX_EXPERT_TOP / 1024;  // copies a thread
@@ -231,6 +230,8 @@ struct Held {
   }
 };
 
+// The places of every 64 tokens' copies, a workgroup each (4096 tokens of 128, 8 chosen: 4.5 us, of
+// which a launch and the histograms' way are most).
 __global__ __launch_bounds__(1024) void place_kernel(RouteArgs a) {
   __shared__ int32_t base[kMaxExperts], total[kMaxExperts], first[kMaxExperts + 1];
   __shared__ uint64_t mask[kMaxExperts];
@@ -289,7 +290,7 @@ __global__ __launch_bounds__(1024) void route_few_kernel(RouteArgs a) {
 }
 
 // y[t] = residual[t] + sum_j weights[t][j] rows[place[t][j]], eight outputs a thread, the
-// copies' rows asked for U at a time.  Bound by traffic (8192 x 4096, 8 copies: 5.3 TB/s), and
+// copies' rows asked for U at a time.  Bound by traffic (8192 x 4096, 8 copies: 5.4 TB/s), and
 // for a few tokens by the way of a place and then a row.  The last piece of a row reads the
 // row's last eight elements and keeps those of its own.  A place outside the rows adds its
 // weight times 0: nothing, or NaN where the weight is one.

@@ -604,7 +604,7 @@ __global__ __launch_bounds__(256) void join_kernel(Args a) {
 // U blocks in its registers and the next U on their way; blocks past the end are loads out of
 // the buffer's range, so that no load of a step stands behind a test.  Bound by the weight's
 // bytes where they are many (4096 x 14336, one token 12.8 us with the launch: 4.6 TB/s) and by
-// the ways of x, a block and the sums where they are few (5120 x 5120 7.2 us without it).
+// the ways of x, a block and the sums where they are few (5120 x 5120 7.3 us without it).
 // XT: the type of x.  Codes (MBQ_INT8) are read from memory; a few float tokens are quantized
 // here, once a workgroup into LDS, which saves the quantizing launch.
 template <int W, int TT, int XT, int P, bool GROUPED>

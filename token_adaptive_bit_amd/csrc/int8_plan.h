@@ -22,12 +22,15 @@ constexpr int kInt8Forms = 13;
 // at `tbs` (`cold_tbs` where they are more than the last-level cache keeps), a part `again` of
 // them for every further tile of tokens; the three overlap.  tile_us starts and ends a
 // workgroup, launch_us is paid once, and split K (join_us) pays a second launch and the partial
-// sums' traffic (join_tbs).  The times are a fit to 11637 timings of every form on 13 weights, plain
+// sums' traffic (join_tbs).  The times are a fit to 11507 timings of the forms on 13 weights, plain
 // and gated, 1 to 4096 tokens (the best split of each in profiles/int8_plan_timings.csv): the
-// choice is 2.1% above the best on the mean, 7% at the ninth tenth; for experts (220 drawn shapes,
-// cold_tbs and the added terms are theirs) 3.9% on the mean.  For instance, 5120 x 5120, us: 64 tokens
-// direct 128 x 16 12.4, 64 x 16 13.2, 256 x 128 18.6; 333 tokens direct 128 x 64 17.7, shared 128 x 128
-// 21.5, 256 x 256 33.6; 2048 tokens direct 256 x 128 65.7, shared 256 x 192 53.6, 256 x 256 60.0.
+// choice is 2.1% above the best on the mean, 8.3% at the ninth tenth and 30% at worst, over 463 of
+// 488 shapes (for many tokens of small weights the plan has 25 times a tile that was not timed).
+// For experts, whose are cold_tbs and the added terms, 4.1% on the mean, 14% at the ninth tenth and
+// 34% at worst, over 209 of 214 drawn shapes of n and k up to 7936 (profiles/expert_plan_timings.csv).
+// For instance, 5120 x 5120, us: 64 tokens direct 128 x 16 12.4, 64 x 16 13.2, 256 x 128 18.6; 333
+// tokens direct 128 x 64 17.7, shared 128 x 128 21.5, 256 x 256 33.6; 2048 tokens direct 256 x 128
+// 65.7, shared 256 x 192 53.6, 256 x 256 60.0.
 struct Int8Cost {
   int rows, tokens;
   float wait_us, block_us, token_us, tile_us, launch_us, tbs, cold_tbs, again, join_us, join_tbs;

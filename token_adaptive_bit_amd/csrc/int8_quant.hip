@@ -69,8 +69,9 @@ __global__ __launch_bounds__(WR < 4 ? 256 : 64 * WR) void quantize_rows_kernel(i
 }
 
 // 16 rows of one weight of one expert per workgroup and step: 16 lanes a row, 128 inputs at a
-// time, first for the row's maximum and then for its codes (the second read comes from the caches).
-// Bound by traffic (codes of 128 experts of 1536 x 4096 345 us, 4.7 TB/s).
+// time, first for the row's maximum and then for its codes.  Bound by traffic: codes, which have no
+// maximum, once (128 experts of 1536 x 4096 330 us, 4.9 TB/s); float weights twice, the second time
+// from memory too (the same from float32 1414 us, 5.1 TB/s with both reads, from bfloat16 767 us, 5.3).
 template <int WT>  // 0 float32, 1 bfloat16, 2 codes with scales given
 __global__ __launch_bounds__(256) void pack_int8_kernel(mbq_int8_desc d, int32_t part, const void* __restrict__ w,
                                                         const float* __restrict__ w_scale, uint8_t* __restrict__ packed,
