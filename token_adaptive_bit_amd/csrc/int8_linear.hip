@@ -721,11 +721,11 @@ __global__ __launch_bounds__(64 * W) void stream_kernel(Args a) {
       const float f = int8_factor(m);
       if (tid * 8 < end) {
         ahead.get(v);
-        store_int8x8(lx, tid * 8, ldl, v, f);
+        store_int8x8<false>(lx, tid * 8, ldl, v, f);
       }
       for (int at = (tid + 64 * W) * 8; at < end; at += 64 * W * 8) {
         load8<kBf>(row, at, a.k, v);
-        store_int8x8(lx, at, ldl, v, f);
+        store_int8x8<false>(lx, at, ldl, v, f);
       }
       if (tid == 0) ls[0] = there ? int8_scale(m) : 0.f;
     } else {  // a wave a row
@@ -744,7 +744,7 @@ __global__ __launch_bounds__(64 * W) void stream_kernel(Args a) {
 #pragma unroll 4
         for (int at = lane * 8; at < end; at += 512) {
           load8<kBf>(row, at, a.k, v);
-          store_int8x8(lx + i * ldl, at, ldl, v, f);
+          store_int8x8<false>(lx + i * ldl, at, ldl, v, f);
         }
         if (lane == 0) ls[i] = there ? int8_scale(m) : 0.f;
       }
