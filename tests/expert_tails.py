@@ -7,7 +7,7 @@ import random
 
 UNITS = 256
 TILES = {9: (128, 128), 10: (256, 128), 11: (256, 192), 12: (256, 256)}   # packed rows x tokens
-ROUNDS = {
+TAILS = {
     (0, 9, 1): (467, 16673, 1702, 281, 2064, 3, 1), (0, 9, 2): (70, 13816, 4510, 263, 784, 2, 0),
     (0, 9, 4): (179, 9160, 6476, 275, 528, 30, 0), (0, 10, 4): (551, 1864, 2320, 3211, 528, 8, 1),
     (0, 11, 1): (446, 2115, 9279, 6437, 1552, 7, 1), (0, 11, 2): (381, 1537, 6865, 7611, 656, 4, 1),
@@ -33,7 +33,7 @@ def counts(experts, rows, seed):
 def tiles(key):
     """Rows of every tile in the order that the kernel deals them: four token tiles of an expert by its row tiles."""
     gated, form, _ = key
-    _, rows, seed, n, _, experts, _ = ROUNDS[key]
+    _, rows, seed, n, _, experts, _ = TAILS[key]
     high, tokens = TILES[form]
     across = -(-((n + 15) // 16 * 16 * (gated + 1)) // high)
     out = []

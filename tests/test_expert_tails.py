@@ -1,4 +1,4 @@
-"""The shapes of tests/expert_rounds.py (no GPU): the plan chooses their form, their tiles pass a round of the units, and the
+"""The shapes of tests/expert_tails.py (no GPU): the plan chooses their form, their tiles pass a round of the units, and the
 last part round is dealt as their key says, with tiles that leave parts without tokens and tiles that end inside 16."""
 import os
 import shutil
@@ -6,7 +6,7 @@ import subprocess
 
 import pytest
 
-from expert_rounds import ROUNDS, TILES, UNITS, counts, tiles
+from expert_tails import TAILS, TILES, UNITS, counts, tiles
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 PROGRAM = r"""
@@ -27,12 +27,12 @@ def test_forms(tmp_path):
     subprocess.run(["g++", "-std=c++17", "-O1", "-I", os.path.join(ROOT, "token_adaptive_bit_amd", "csrc"), str(tmp_path / "plan.cpp"),
                     "-o", str(tmp_path / "plan")], check=True)
     lines = [f"{t} {sum(counts(e, rows, seed))} {n} {k} {key[0]} {e} {codes}"
-             for key, (t, rows, seed, n, k, e, codes) in ROUNDS.items()]
+             for key, (t, rows, seed, n, k, e, codes) in TAILS.items()]
     out = subprocess.run([str(tmp_path / "plan")], input="\n".join(lines), capture_output=True, text=True, check=True).stdout.split()
-    assert [int(f) for f in out] == [key[1] for key in ROUNDS]
+    assert [int(f) for f in out] == [key[1] for key in TAILS]
 
 
-@pytest.mark.parametrize("key", sorted(ROUNDS), ids=str)
+@pytest.mark.parametrize("key", sorted(TAILS), ids=str)
 def test_last_round(key):
     _, form, parts = key
     all_ = tiles(key)
@@ -48,5 +48,5 @@ def test_last_round(key):
 
 def test_every_form_is_there():
     for gated in (0, 1):
-        assert {key[1] for key in ROUNDS if key[0] == gated} == set(TILES)
-        assert {key[2] for key in ROUNDS if key[0] == gated} == {1, 2, 4}
+        assert {key[1] for key in TAILS if key[0] == gated} == set(TILES)
+        assert {key[2] for key in TAILS if key[0] == gated} == {1, 2, 4}

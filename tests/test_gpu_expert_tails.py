@@ -1,5 +1,5 @@
 """Ragged expert products on shared tiles past one round of the units, where the tiles of the last part round are whole, halves
-or quarters (tests/expert_rounds.py), plain and gated, through gathered rows: against sums in float64 (exact: they stay below
+or quarters (tests/expert_tails.py), plain and gated, through gathered rows: against sums in float64 (exact: they stay below
 2^53), every row of every expert.
 
 Tolerances as in test_gpu_int8_linear.
@@ -8,17 +8,17 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from expert_rounds import ROUNDS, counts
+from expert_tails import TAILS, counts
 from test_gpu_int8_paths import BF, DEV, F32, api, weight   # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("key", sorted(ROUNDS), ids=lambda k: "gated%d-form%d-parts%d" % k)
-def test_rounds(api, key):
+@pytest.mark.parametrize("key", sorted(TAILS), ids=lambda k: "gated%d-form%d-parts%d" % k)
+def test_tails(api, key):
     gated = key[0]
-    t, asked, seed, n, k, experts, codes = ROUNDS[key]
-    print("rounds", key, ROUNDS[key], flush=True)
+    t, asked, seed, n, k, experts, codes = TAILS[key]
+    print("tails", key, TAILS[key], flush=True)
     each = counts(experts, asked, seed)
     p = sum(each)
     ends = [sum(each[:e]) for e in range(experts + 1)]
